@@ -680,3 +680,9 @@ __all__ = [
     "MpStepState", "MpLaunch", "mp_step_launches", "LIB_PATH", "mp_grad_sumsq", "mp_clip_scale_from_sumsq",
     "LRSchedule", "MpLrSchedule", "LR_KINDS", "HostGradPipeline", "mp_copy_from_host",
 ]
+
+# the operators of include/mp_train.h; after the names above, which they use
+from . import train  # noqa: E402
+from .train import *  # noqa: E402,F401,F403
+
+__all__ += train.__all__

@@ -21,7 +21,8 @@ LIB = os.path.join(PKG, "libmpadamw.so")
 # compute-free stream probes, a separate library that only the benchmark loads
 PROBE_LIB = os.path.join(PKG, "libmpprobe.so")
 
-SOURCES = ["mp_api.cu", "mp_step.cu", "mp_norm.cu", "mp_sr.cu", "mp_outlier.cu", "mp_small.cu", "mp_copy.cu"]
+SOURCES = ["mp_api.cu", "mp_step.cu", "mp_norm.cu", "mp_sr.cu", "mp_outlier.cu", "mp_small.cu", "mp_copy.cu",
+           "mp_layernorm.cu", "mp_logprob.cu", "mp_distill.cu"]
 PROBE_SOURCES = ["mp_probe.cu"]
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = [
@@ -42,7 +43,7 @@ def nvcc() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(INCLUDE, "mp_adamw.h"))
+    files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     files.append(os.path.abspath(__file__))
     return files
 

@@ -1,0 +1,121 @@
+// mp_rows.cuh — element types and reductions of the row-wise operators
+// (layer norm, token log probabilities, distillation).
+#pragma once
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "mp_train.h"
+
+namespace mpk {
+
+// ---- argument checks shared by the entry points ---------------------------
+constexpr int64_t kMaxRows = int64_t{1} << 40;  // also of a row stride
+
+inline bool type_ok(int32_t t) { return t == MP_BF16 || t == MP_FP16 || t == MP_FP32; }
+inline bool index_type_ok(int32_t t) { return t == MP_INT32 || t == MP_INT64; }
+inline bool rows_ok(int64_t rows) { return rows >= 0 && rows < kMaxRows; }
+inline bool vocab_ok(int64_t vocab) { return vocab >= 1 && vocab <= INT32_MAX; }
+inline bool stride_ok(int64_t stride, int64_t length) { return stride >= length && stride < kMaxRows; }
+inline bool scale_ok(float scale) { return scale > 0.0f && std::isfinite(scale); }
+inline bool aligned_to(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+inline bool aligned4(const void* p) { return aligned_to(p, 4); }
+inline bool type_aligned(const void* p, int32_t t) { return aligned_to(p, t == MP_FP32 ? 4 : 2); }
+inline bool index_aligned(const void* p, int32_t t) { return aligned_to(p, t == MP_INT64 ? 8 : 4); }
+
+// ---- elements ---------------------------------------------------------------
+
+constexpr float kInf = INFINITY;
+constexpr float kLog2E = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+
+// A matrix element of mp_dtype_t `T` as stored, widened to fp32 exactly and
+// rounded back to nearest even.
+template <int T>
+struct Elem;
+
+template <>
+struct Elem<MP_BF16> {
+  using type = uint16_t;
+  static __device__ __forceinline__ float get(uint16_t h) { return __uint_as_float(static_cast<uint32_t>(h) << 16); }
+  static __device__ __forceinline__ uint16_t put(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+};
+
+template <>
+struct Elem<MP_FP16> {
+  using type = uint16_t;
+  static __device__ __forceinline__ float get(uint16_t h) { return __half2float(__ushort_as_half(h)); }
+  static __device__ __forceinline__ uint16_t put(float x) { return __half_as_ushort(__float2half_rn(x)); }
+};
+
+template <>
+struct Elem<MP_FP32> {
+  using type = float;
+  static __device__ __forceinline__ float get(float x) { return x; }
+  static __device__ __forceinline__ float put(float x) { return x; }
+};
+
+// One element of a vector whose type is known at run time only (weights:
+// read or written once per block or launch).
+__device__ __forceinline__ float load_as(const void* p, int64_t i, int type) {
+  if (type == MP_FP32) return static_cast<const float*>(p)[i];
+  const uint16_t h = static_cast<const uint16_t*>(p)[i];
+  return type == MP_BF16 ? Elem<MP_BF16>::get(h) : Elem<MP_FP16>::get(h);
+}
+
+__device__ __forceinline__ void store_as(void* p, int64_t i, int type, float x) {
+  if (type == MP_FP32)
+    static_cast<float*>(p)[i] = x;
+  else
+    static_cast<uint16_t*>(p)[i] = type == MP_BF16 ? Elem<MP_BF16>::put(x) : Elem<MP_FP16>::put(x);
+}
+
+__device__ __forceinline__ int64_t load_index(const void* p, int64_t i, int type) {
+  return type == MP_INT64 ? static_cast<const int64_t*>(p)[i] : static_cast<const int32_t*>(p)[i];
+}
+
+// 2^x, to 2 ulp of fp32; results below 2^-126 are 0. NaN stays NaN.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// max(a, b), NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+// Order of the alternatives as unsigned integers: rising value, -0 equal to
+// +0, NaN (of any kind) last.
+__device__ __forceinline__ uint32_t order_of(float x) {
+  const uint32_t b = __float_as_uint(__fadd_rn(x, 0.0f));
+  if (x != x) return 0xFFFFFFFFu;
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+// The value that order_of maps to `key` (NaN for the NaN key).
+__device__ __forceinline__ float value_of_order(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? (key ^ 0x80000000u) : ~key);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+
+}  // namespace mpk
