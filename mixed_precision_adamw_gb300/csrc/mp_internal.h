@@ -122,6 +122,21 @@ void prefer_max_shared(void (*kernel)(Params...), std::atomic<bool> (&done)[64])
     done[dev].store(true, std::memory_order_relaxed);
 }
 
+// Lets `kernel` be launched with up to `bytes` of dynamic shared memory (above
+// 48 KB a kernel has to ask). Once per kernel (`done` belongs to that kernel)
+// and device.
+template <typename... Params>
+cudaError_t allow_shared(void (*kernel)(Params...), int bytes, std::atomic<bool> (&done)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev >= 0 && dev < 64;
+  if (known && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && known) done[dev].store(true, std::memory_order_relaxed);
+  return e;
+}
+
 struct DeviceInfo {
   int device;
   int sms;

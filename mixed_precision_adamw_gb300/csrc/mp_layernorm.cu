@@ -3,7 +3,10 @@
 //
 // The mean and the variance are taken in two passes over the row (the sum,
 // then the squared distances from the mean), so a row with a large common
-// offset loses nothing to cancellation; all sums are fp32.
+// offset loses nothing to cancellation; all sums are fp32. A row stays in
+// registers between the passes, so each element is read from memory once.
+// Everything is bound by HBM: 4 B an element forward and 6 B backward for
+// 16-bit types.
 #include "mp_device.cuh"
 #include "mp_internal.h"
 #include "mp_rows.cuh"
@@ -13,17 +16,6 @@ namespace {
 
 constexpr int kLnThreads = 256;
 constexpr int64_t kMaxD = int64_t{1} << 24;
-
-// Sum over the block, to every thread; `red` holds one float per warp.
-__device__ float block_sum(float v, float* red) {
-  v = warp_sum(v);
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
-  __syncthreads();
-  float s = 0.0f;
-  for (int w = 0; w < blockDim.x / 32; ++w) s = __fadd_rn(s, red[w]);
-  return s;
-}
 
 struct LnArgs {
   void* y;  // dx in the backward pass
@@ -40,8 +32,173 @@ struct LnArgs {
   int weight_type;
 };
 
+// A row divided over a group of L threads, NV units of eight elements each:
+// element e of unit v of thread t.
+template <bool Wide>
+__device__ __forceinline__ int64_t column(int v, int e, int t, int L) {
+  return Wide ? (static_cast<int64_t>(v) * L + t) * 8 + e : (static_cast<int64_t>(v) * 8 + e) * L + t;
+}
+
+template <int T, bool Wide>
+__device__ __forceinline__ void load_unit(Pack8<T>& u, const typename Elem<T>::type* row, int v, int t, int L,
+                                          int64_t d) {
+  const int64_t j = column<Wide>(v, 0, t, L);
+  if (Wide) {
+    if (j < d)
+      u.load(row + j);
+    else
+      u.zero();
+  } else {
+    u.load_stepped(row, j, L, d);
+  }
+}
+
+template <int T, bool Wide>
+__device__ __forceinline__ void store_unit(const Pack8<T>& u, typename Elem<T>::type* row, int v, int t, int L,
+                                           int64_t d) {
+  const int64_t j = column<Wide>(v, 0, t, L);
+  if (!Wide)
+    u.store_stepped(row, j, L, d);
+  else if (j < d)
+    u.store(row + j);
+}
+
+// Whether element e of a unit lies in the row (Wide units are in or out whole).
+template <bool Wide>
+__device__ __forceinline__ bool in_row(int v, int e, int t, int L, int64_t d) {
+  return column<Wide>(v, Wide ? 0 : e, t, L) < d;
+}
+
+// Sum over groups of L <= 32 neighbouring lanes, to each of them.
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+
+// Sum over the block, to every thread; `red` holds one float per warp.
+__device__ __forceinline__ float block_sum(float v, float* red) {
+  v = warp_sum(v);
+  __syncthreads();
+  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
+  __syncthreads();
+  float s = 0.0f;
+  for (int w = 0; w < blockDim.x / 32; ++w) s = __fadd_rn(s, red[w]);
+  return s;
+}
+
+// ---- forward ----------------------------------------------------------------
+// Groups of L threads take a row each: L <= 32 lanes of a warp (no barrier in
+// the loop), or L = 256, a whole block. Weight and bias are widened into
+// shared memory once a block: at most 8 B a column are read there for 4 B or
+// more of memory traffic, and neither their type nor their alignment (they
+// may sit anywhere in a flat buffer) matters afterwards.
+//
+// Eight weights of a unit lie in two planes of four, so that the lanes of a
+// warp read 16 consecutive bytes each.
+__device__ __forceinline__ int plane_index(int64_t unit, int e, int64_t units) {
+  return static_cast<int>((e / 4 * units + unit) * 4 + e % 4);
+}
+
+template <bool Wide>
+__device__ __forceinline__ void stage_weights(float* sw, const LnArgs& a, int64_t units, int threads) {
+  for (int64_t j = threadIdx.x; j < a.d; j += threads) {
+    const int at = Wide ? plane_index(j / 8, j % 8, units) : static_cast<int>(j);
+    sw[at] = a.weight ? load_as(a.weight, j, a.weight_type) : 1.0f;
+    sw[8 * units + at] = a.bias ? load_as(a.bias, j, a.weight_type) : 0.0f;
+  }
+}
+
+template <int T, bool Wide, int L, int NV>
+__global__ void __launch_bounds__(kLnThreads, NV >= 8 ? 3 : 4) ln_forward_kernel(LnArgs a) {
+  pdl_enter();
+  using E = typename Elem<T>::type;
+  constexpr bool kBlock = L > 32;
+  __shared__ float red[kLnThreads / 32];
+  extern __shared__ float sw[];
+  const int t = threadIdx.x % L;
+  const int64_t units = (a.d + 7) / 8;
+  const float* sb = sw + 8 * units;
+  const int64_t groups = static_cast<int64_t>(gridDim.x) * (kLnThreads / L);
+  const float n = static_cast<float>(a.d);
+  // every lane of a warp runs the same number of rounds (the shuffles are whole-warp)
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kLnThreads / L) + threadIdx.x / L;
+  for (int64_t r0 = 0; r0 < a.rows; r0 += groups) {
+    const int64_t r = r0 + first;
+    const bool live = r < a.rows;
+    const E* x = static_cast<const E*>(a.x) + (live ? r : 0) * a.x_stride;
+    Pack8<T> u[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) load_unit<T, Wide>(u[v], x, v, t, L, live ? a.d : 0);
+    if (r0 == 0) {  // with the first rows on their way
+      stage_weights<Wide>(sw, a, units, kLnThreads);
+      __syncthreads();
+    }
+    if (kBlock && !live) break;
+    float s = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float f[8];
+      u[v].get(f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s = __fadd_rn(s, f[e]);  // elements past the row are 0
+    }
+    const float mean = __fdiv_rn(kBlock ? block_sum(s, red) : lanes_sum<kBlock ? 32 : L>(s), n);
+    float q = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float f[8];
+      u[v].get(f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (in_row<Wide>(v, e, t, L, a.d)) {
+          const float c = __fsub_rn(f[e], mean);
+          q = __fmaf_rn(c, c, q);
+        }
+    }
+    const float var = __fdiv_rn(kBlock ? block_sum(q, red) : lanes_sum<kBlock ? 32 : L>(q), n);
+    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(var, a.eps)));
+    if (!live) continue;
+    E* y = static_cast<E*>(a.y) + r * a.y_stride;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float f[8], w[8], b[8];
+      u[v].get(f);
+      if (Wide) {
+        const int64_t unit = static_cast<int64_t>(v) * L + t;
+        if (unit >= units) continue;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float4 p = *reinterpret_cast<const float4*>(sw + (h * units + unit) * 4);
+          const float4 q4 = *reinterpret_cast<const float4*>(sb + (h * units + unit) * 4);
+          w[4 * h] = p.x, w[4 * h + 1] = p.y, w[4 * h + 2] = p.z, w[4 * h + 3] = p.w;
+          b[4 * h] = q4.x, b[4 * h + 1] = q4.y, b[4 * h + 2] = q4.z, b[4 * h + 3] = q4.w;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int64_t j = column<Wide>(v, e, t, L);
+          w[e] = j < a.d ? sw[j] : 0.0f;
+          b[e] = j < a.d ? sb[j] : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = __fmaf_rn(__fmul_rn(__fsub_rn(f[e], mean), rstd), w[e], b[e]);
+      u[v].put(f);
+      store_unit<T, Wide>(u[v], y, v, t, L, a.d);
+    }
+    if (t == 0) {
+      if (a.mean_out) a.mean_out[r] = mean;
+      if (a.rstd_out) a.rstd_out[r] = rstd;
+    }
+  }
+}
+
+// Rows longer than the registers hold: three passes over the row, the later
+// ones out of the caches.
 template <int T>
-__global__ void __launch_bounds__(kLnThreads) ln_forward_kernel(LnArgs a) {
+__global__ void __launch_bounds__(kLnThreads) ln_forward_long_kernel(LnArgs a) {
   pdl_enter();
   using E = Elem<T>;
   __shared__ float red[kLnThreads / 32];
@@ -72,8 +229,227 @@ __global__ void __launch_bounds__(kLnThreads) ln_forward_kernel(LnArgs a) {
   }
 }
 
+// ---- backward ---------------------------------------------------------------
+// One pass gives dx and the block's share of dweight and dbias: a thread owns
+// the same columns in every row it sees, so it adds their dy xh and dy in
+// registers, and a block writes its sums once, part[block][0 or 1][d]; a
+// second, small launch adds the blocks' sums in block order.
+
+// Adds N per-lane values over the 32 lanes: N / 2 + N / 4 + ... + 1 shuffles
+// halve the values each lane carries, the rest finish the one left. Lane l
+// ends with the total of value many_index<N>(l).
+template <int N>
+__device__ __forceinline__ float many_sum(float (&v)[N]) {
+  const int lane = threadIdx.x % 32;
+  int o = 16;
+#pragma unroll
+  for (int n = N; n > 1; n /= 2) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) {
+      const float send = up ? v[i] : v[i + n / 2];
+      const float keep = up ? v[i + n / 2] : v[i];
+      v[i] = __fadd_rn(keep, __shfl_xor_sync(kAll, send, o));
+    }
+    o >>= 1;
+  }
+  float s = v[0];
+#pragma unroll
+  for (int q = 16 / N; q > 0; q >>= 1) s = __fadd_rn(s, __shfl_xor_sync(kAll, s, q));
+  return s;
+}
+
+// The value whose total lane l holds: the top log2(N) bits of l.
+template <int N>
+__device__ __forceinline__ int many_index(int lane) {
+  return lane / (32 / N);
+}
+
+// Rows of up to 8 * NV * blockDim elements, R rows a round: the loads of the
+// next round are in flight while this one is reduced, with one barrier a
+// round (the warps' sums alternate between two buffers).
+template <int T, bool Wide, int NV, int R, int MaxThreads>
+__global__ void __launch_bounds__(MaxThreads) ln_backward_kernel(LnArgs a, float* part) {
+  pdl_enter();
+  using E = typename Elem<T>::type;
+  constexpr int N = 2 * R;
+  __shared__ float red[2][32][N];
+  const int t = threadIdx.x, L = blockDim.x, lane = t % 32, warp = t / 32, warps = L / 32;
+  const float inv_d = __fdiv_rn(1.0f, static_cast<float>(a.d));
+  const int64_t begin = a.rows * blockIdx.x / gridDim.x, end = a.rows * (blockIdx.x + 1) / gridDim.x;
+  float w[NV][8], dw[NV][8], db[NV][8];
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int64_t j = column<Wide>(v, e, t, L);
+      w[v][e] = j < a.d ? (a.weight ? load_as(a.weight, j, a.weight_type) : 1.0f) : 0.0f;
+      dw[v][e] = db[v][e] = 0.0f;
+    }
+  Pack8<T> x[R][NV], g[R][NV];
+  float mean[R], rstd[R];
+  auto load = [&](int64_t r0) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int64_t r = r0 + i;
+      const bool live = r < end;
+      const int64_t n = live ? a.d : 0, at = live ? r : begin;
+      mean[i] = live ? a.mean[r] : 0.0f;
+      rstd[i] = live ? a.rstd[r] : 0.0f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        load_unit<T, Wide>(x[i][v], static_cast<const E*>(a.x) + at * a.x_stride, v, t, L, n);
+        load_unit<T, Wide>(g[i][v], static_cast<const E*>(a.dy) + at * a.dy_stride, v, t, L, n);
+      }
+    }
+  };
+  if (begin < end) load(begin);
+  int buf = 0;
+  for (int64_t r0 = begin; r0 < end; r0 += R, buf ^= 1) {
+    Pack8<T> cx[R][NV], cg[R][NV];
+    float cm[R], cr[R], sums[N];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      cm[i] = mean[i];
+      cr[i] = rstd[i];
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        cx[i][v] = x[i][v];
+        cg[i][v] = g[i][v];
+      }
+    }
+    if (r0 + R < end) load(r0 + R);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        float fx[8], fg[8];
+        cx[i][v].get(fx);
+        cg[i][v].get(fg);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float gw = __fmul_rn(fg[e], w[v][e]);  // 0 past the row
+          s1 = __fadd_rn(s1, gw);
+          s2 = __fmaf_rn(gw, __fmul_rn(__fsub_rn(fx[e], cm[i]), cr[i]), s2);
+        }
+      }
+      sums[2 * i] = s1;
+      sums[2 * i + 1] = s2;
+    }
+    const float mine = many_sum<N>(sums);
+    if (lane % (32 / N) == 0) red[buf][warp][many_index<N>(lane)] = mine;
+    __syncthreads();
+    float total = 0.0f;
+    for (int q = lane % (32 / N); q < warps; q += 32 / N) total = __fadd_rn(total, red[buf][q][many_index<N>(lane)]);
+#pragma unroll
+    for (int o = 16 / N; o > 0; o >>= 1) total = __fadd_rn(total, __shfl_xor_sync(kAll, total, o));
+    total = __fmul_rn(total, inv_d);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const float c1 = __shfl_sync(kAll, total, (2 * i) * (32 / N));
+      const float c2 = __shfl_sync(kAll, total, (2 * i + 1) * (32 / N));
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        float fx[8], fg[8], o[8];
+        cx[i][v].get(fx);
+        cg[i][v].get(fg);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float xh = __fmul_rn(__fsub_rn(fx[e], cm[i]), cr[i]);
+          const float gw = __fmul_rn(fg[e], w[v][e]);
+          o[e] = __fmul_rn(cr[i], __fmaf_rn(-xh, c2, __fsub_rn(gw, c1)));
+          dw[v][e] = __fmaf_rn(fg[e], xh, dw[v][e]);
+          db[v][e] = __fadd_rn(db[v][e], fg[e]);
+        }
+        if (a.y && r0 + i < end) {
+          Pack8<T> u;
+          u.put(o);
+          store_unit<T, Wide>(u, static_cast<E*>(a.y) + (r0 + i) * a.y_stride, v, t, L, a.d);
+        }
+      }
+    }
+  }
+  if (!part) return;
+  float* pw = part + static_cast<int64_t>(blockIdx.x) * 2 * a.d;
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (in_row<Wide>(v, e, t, L, a.d)) {
+        const int64_t j = column<Wide>(v, e, t, L);
+        pw[j] = dw[v][e];
+        pw[a.d + j] = db[v][e];
+      }
+}
+
+// Rows of up to 8 * L elements, one per L <= 32 lanes, no barrier; the groups
+// of a block join their sums through shared memory at the end.
+template <int T, bool Wide, int L>
+__global__ void __launch_bounds__(kLnThreads) ln_backward_short_kernel(LnArgs a, float* part) {
+  pdl_enter();
+  using E = typename Elem<T>::type;
+  constexpr int G = kLnThreads / L;
+  __shared__ float joined[G][8 * L];
+  const int t = threadIdx.x % L, group = threadIdx.x / L;
+  const float inv_d = __fdiv_rn(1.0f, static_cast<float>(a.d));
+  float w[8], dw[8], db[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int64_t j = column<Wide>(0, e, t, L);
+    w[e] = j < a.d ? (a.weight ? load_as(a.weight, j, a.weight_type) : 1.0f) : 0.0f;
+    dw[e] = db[e] = 0.0f;
+  }
+  const int64_t groups = static_cast<int64_t>(gridDim.x) * G;
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * G; r0 < a.rows; r0 += groups) {
+    const int64_t r = r0 + group;
+    const bool live = r < a.rows;
+    const int64_t at = live ? r : 0, n = live ? a.d : 0;
+    Pack8<T> x, g;
+    load_unit<T, Wide>(x, static_cast<const E*>(a.x) + at * a.x_stride, 0, t, L, n);
+    load_unit<T, Wide>(g, static_cast<const E*>(a.dy) + at * a.dy_stride, 0, t, L, n);
+    const float mean = live ? a.mean[r] : 0.0f, rstd = live ? a.rstd[r] : 0.0f;
+    float fx[8], fg[8], s1 = 0.0f, s2 = 0.0f;
+    x.get(fx);
+    g.get(fg);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      fx[e] = __fmul_rn(__fsub_rn(fx[e], mean), rstd);
+      const float gw = __fmul_rn(fg[e], w[e]);
+      s1 = __fadd_rn(s1, gw);
+      s2 = __fmaf_rn(gw, fx[e], s2);
+      dw[e] = __fmaf_rn(fg[e], fx[e], dw[e]);
+      db[e] = __fadd_rn(db[e], fg[e]);
+    }
+    const float c1 = __fmul_rn(lanes_sum<L>(s1), inv_d), c2 = __fmul_rn(lanes_sum<L>(s2), inv_d);
+    if (a.y && live) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        fx[e] = __fmul_rn(rstd, __fmaf_rn(-fx[e], c2, __fsub_rn(__fmul_rn(fg[e], w[e]), c1)));
+      x.put(fx);
+      store_unit<T, Wide>(x, static_cast<E*>(a.y) + r * a.y_stride, 0, t, L, a.d);
+    }
+  }
+  if (!part) return;
+  float* pw = part + static_cast<int64_t>(blockIdx.x) * 2 * a.d;
+  for (int k = 0; k < 2; ++k) {
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) joined[group][e * L + t] = k ? db[e] : dw[e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 8 * L; i += kLnThreads) {
+      const int64_t j = column<Wide>(0, i / L, i % L, L);
+      if (j >= a.d) continue;
+      float s = 0.0f;
+      for (int q = 0; q < G; ++q) s = __fadd_rn(s, joined[q][i]);
+      pw[k * a.d + j] = s;
+    }
+  }
+}
+
+// Rows longer than the registers hold: dx row by row, in two passes.
 template <int T>
-__global__ void __launch_bounds__(kLnThreads) ln_dx_kernel(LnArgs a) {
+__global__ void __launch_bounds__(kLnThreads) ln_dx_long_kernel(LnArgs a) {
   pdl_enter();
   using E = Elem<T>;
   __shared__ float red[kLnThreads / 32];
@@ -101,63 +477,164 @@ __global__ void __launch_bounds__(kLnThreads) ln_dx_kernel(LnArgs a) {
   }
 }
 
-// Partial sums over a chunk of rows: part[0][chunk][j] for the weight,
-// part[1][chunk][j] for the bias. One column per thread.
-constexpr int kChunks = 64;
-
+// ... and the weight gradients column by column: block (i, c) adds 256 columns
+// over the c-th chunk of rows.
 template <int T>
-__global__ void __launch_bounds__(kLnThreads) ln_dw_kernel(LnArgs a, float* part, int chunks) {
+__global__ void __launch_bounds__(kLnThreads) ln_dw_long_kernel(LnArgs a, float* part) {
   pdl_enter();
   using E = Elem<T>;
-  const int64_t j = static_cast<int64_t>(blockIdx.x) * kLnThreads + threadIdx.x;
+  const int64_t strips = (a.d + kLnThreads - 1) / kLnThreads;
+  const int64_t c = blockIdx.x / strips, chunks = gridDim.x / strips;
+  const int64_t j = (blockIdx.x % strips) * kLnThreads + threadIdx.x;
   if (j >= a.d) return;
-  for (int c = 0; c < chunks; ++c) {
-    const int64_t r0 = a.rows * c / chunks, r1 = a.rows * (c + 1) / chunks;
-    float sw = 0.0f, sb = 0.0f;
-    for (int64_t r = r0; r < r1; ++r) {
-      const float xv = E::get(static_cast<const typename E::type*>(a.x)[r * a.x_stride + j]);
-      const float g = E::get(static_cast<const typename E::type*>(a.dy)[r * a.dy_stride + j]);
-      sw = __fmaf_rn(g, __fmul_rn(__fsub_rn(xv, a.mean[r]), a.rstd[r]), sw);
-      sb = __fadd_rn(sb, g);
-    }
-    part[static_cast<int64_t>(c) * a.d + j] = sw;
-    part[(static_cast<int64_t>(chunks) + c) * a.d + j] = sb;
+  const int64_t r1 = a.rows * (c + 1) / chunks;
+  float sw = 0.0f, sb = 0.0f;
+#pragma unroll 4
+  for (int64_t r = a.rows * c / chunks; r < r1; ++r) {
+    const float xv = E::get(static_cast<const typename E::type*>(a.x)[r * a.x_stride + j]);
+    const float g = E::get(static_cast<const typename E::type*>(a.dy)[r * a.dy_stride + j]);
+    sw = __fmaf_rn(g, __fmul_rn(__fsub_rn(xv, a.mean[r]), a.rstd[r]), sw);
+    sb = __fadd_rn(sb, g);
   }
+  part[c * 2 * a.d + j] = sw;
+  part[(c * 2 + 1) * a.d + j] = sb;
 }
 
-__global__ void __launch_bounds__(kLnThreads) ln_dw_finish_kernel(void* dweight, void* dbias, const float* part,
-                                                                  int64_t d, int chunks, int weight_type) {
+// dweight and dbias from `parts` blocks' sums: 32 columns a block, 16 threads
+// a column, each adding every 16th block's sum.
+constexpr int kFinishSlices = 16;
+
+__global__ void __launch_bounds__(32 * kFinishSlices) ln_finish_kernel(void* dweight, void* dbias, const float* part,
+                                                                       int64_t d, int parts, int weight_type) {
   pdl_enter();
-  const int64_t j = static_cast<int64_t>(blockIdx.x) * kLnThreads + threadIdx.x;
-  if (j >= d) return;
+  __shared__ float red[2][kFinishSlices][33];
+  const int c = threadIdx.x % 32, slice = threadIdx.x / 32;
+  const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + c;
   float sw = 0.0f, sb = 0.0f;
-  for (int c = 0; c < chunks; ++c) {
-    sw = __fadd_rn(sw, part[static_cast<int64_t>(c) * d + j]);
-    sb = __fadd_rn(sb, part[(static_cast<int64_t>(chunks) + c) * d + j]);
+  if (j < d) {
+#pragma unroll 8
+    for (int p = slice; p < parts; p += kFinishSlices) {
+      sw = __fadd_rn(sw, part[static_cast<int64_t>(p) * 2 * d + j]);
+      sb = __fadd_rn(sb, part[(static_cast<int64_t>(p) * 2 + 1) * d + j]);
+    }
   }
-  if (dweight) store_as(dweight, j, weight_type, sw);
-  if (dbias) store_as(dbias, j, weight_type, sb);
+  red[0][slice][c] = sw;
+  red[1][slice][c] = sb;
+  __syncthreads();
+  if (slice >= 2 || j >= d) return;
+  float s = 0.0f;
+#pragma unroll
+  for (int q = 0; q < kFinishSlices; ++q) s = __fadd_rn(s, red[slice][q][c]);
+  if (slice == 0 && dweight) store_as(dweight, j, weight_type, s);
+  if (slice == 1 && dbias) store_as(dbias, j, weight_type, s);
+}
+
+// ---- launches ---------------------------------------------------------------
+
+// Blocks of the backward pass and their threads for rows of d elements. Fewer
+// blocks mean fewer partial sums to write and add; two to four blocks a SM
+// keep enough loads in flight. The sums' order, and so their bits, and the
+// workspace's size follow from rows and d alone.
+constexpr int64_t kSms = 152;
+
+struct LnPlan {
+  int threads, parts;
+};
+
+LnPlan backward_plan(int64_t rows, int64_t d) {
+  LnPlan p;
+  int64_t per_block;  // rows that make a further block worth its partial sum
+  int blocks_per_sm;
+  if (d <= 256) {
+    p.threads = kLnThreads;
+    const int lanes = d <= 64 ? 8 : d <= 128 ? 16 : 32;
+    per_block = kLnThreads / lanes;
+    blocks_per_sm = 4;
+  } else if (d <= 8192) {
+    const int64_t units = (d + 7) / 8;
+    const int64_t nv = units > 512 ? 2 : 1;
+    p.threads = static_cast<int>((units + 32 * nv - 1) / (32 * nv) * 32);
+    per_block = 2;
+    blocks_per_sm = std::max(1, std::min(4, 512 / p.threads));
+  } else {
+    p.threads = kLnThreads;
+    per_block = 32;
+    blocks_per_sm = 1;
+  }
+  const int64_t cap = d <= 8192 ? blocks_per_sm * kSms : 64;
+  p.parts = static_cast<int>(std::max<int64_t>(1, std::min(cap, (rows + per_block - 1) / per_block)));
+  return p;
+}
+
+template <int T, bool Wide, int L, int NV>
+cudaError_t launch_forward(const LnArgs& a, const DeviceInfo& dev, cudaStream_t s) {
+  static std::atomic<bool> ready[64];
+  const size_t smem = (a.d + 7) / 8 * 64;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = allow_shared(ln_forward_kernel<T, Wide, L, NV>, 64 * 1024, ready);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t per_block = kLnThreads / L;
+  const int64_t blocks = std::min<int64_t>((a.rows + per_block - 1) / per_block, (NV >= 8 ? 3 : 4) * dev.sms);
+  return launch_pdl_smem(ln_forward_kernel<T, Wide, L, NV>, static_cast<unsigned>(blocks), kLnThreads, smem, s, a);
+}
+
+template <int T, bool Wide>
+cudaError_t forward_wide(const LnArgs& a, const DeviceInfo& dev, cudaStream_t s) {
+  if (a.d <= 64) return launch_forward<T, Wide, 8, 1>(a, dev, s);
+  if (a.d <= 128) return launch_forward<T, Wide, 16, 1>(a, dev, s);
+  if (a.d <= 256) return launch_forward<T, Wide, 32, 1>(a, dev, s);
+  if (a.d <= 512) return launch_forward<T, Wide, 32, 2>(a, dev, s);
+  if (a.d <= 1024) return launch_forward<T, Wide, 32, 4>(a, dev, s);
+  if (Wide && a.d <= 2048) return launch_forward<T, Wide, 32, 8>(a, dev, s);
+  if (a.d <= 2048) return launch_forward<T, Wide, 256, 1>(a, dev, s);
+  if (a.d <= 4096) return launch_forward<T, Wide, 256, 2>(a, dev, s);
+  if (a.d <= 8192) return launch_forward<T, Wide, 256, 4>(a, dev, s);
+  return launch_pdl(ln_forward_long_kernel<T>, static_cast<unsigned>(std::min<int64_t>(a.rows, 8 * dev.sms)),
+                    kLnThreads, s, a);
 }
 
 template <int T>
 cudaError_t forward(const LnArgs& a, const DeviceInfo& dev, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.rows, 8 * dev.sms));
-  return launch_pdl(ln_forward_kernel<T>, grid, kLnThreads, s, a);
+  const bool wide = wide_rows(a.x, a.d, a.x_stride, a.rows, T) && wide_rows(a.y, a.d, a.y_stride, a.rows, T);
+  return wide ? forward_wide<T, true>(a, dev, s) : forward_wide<T, false>(a, dev, s);
+}
+
+template <int T, bool Wide>
+cudaError_t backward_wide(const LnArgs& a, const LnPlan& p, float* part, cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>(p.parts), threads = static_cast<unsigned>(p.threads);
+  if (a.d <= 64) return launch_pdl(ln_backward_short_kernel<T, Wide, 8>, grid, threads, s, a, part);
+  if (a.d <= 128) return launch_pdl(ln_backward_short_kernel<T, Wide, 16>, grid, threads, s, a, part);
+  if (a.d <= 256) return launch_pdl(ln_backward_short_kernel<T, Wide, 32>, grid, threads, s, a, part);
+  constexpr int R = T == MP_FP32 ? 2 : 4;
+  if (a.d <= 4096) return launch_pdl(ln_backward_kernel<T, Wide, 1, R, 512>, grid, threads, s, a, part);
+  return launch_pdl(ln_backward_kernel<T, Wide, 2, 1, 512>, grid, threads, s, a, part);
 }
 
 template <int T>
 cudaError_t backward(const LnArgs& a, void* dweight, void* dbias, float* part, const DeviceInfo& dev,
                      cudaStream_t s) {
-  const unsigned cols = static_cast<unsigned>((a.d + kLnThreads - 1) / kLnThreads);
+  const bool sums = dweight || dbias;
+  const LnPlan p = backward_plan(a.rows, a.d);
+  const int64_t strips = (a.d + kLnThreads - 1) / kLnThreads;
   cudaError_t e = cudaSuccess;
-  if (dweight || dbias) {  // before dx, which may be written over dy
-    e = launch_pdl(ln_dw_kernel<T>, cols, kLnThreads, s, a, part, kChunks);
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(ln_dw_finish_kernel, cols, kLnThreads, s, dweight, dbias, static_cast<const float*>(part), a.d,
-                   kChunks, a.weight_type);
+  if (a.d <= 8192) {
+    if (a.rows || sums) {
+      const bool wide = wide_rows(a.x, a.d, a.x_stride, a.rows, T) && wide_rows(a.dy, a.d, a.dy_stride, a.rows, T) &&
+                        (!a.y || wide_rows(a.y, a.d, a.y_stride, a.rows, T));
+      float* to = sums ? part : nullptr;
+      e = wide ? backward_wide<T, true>(a, p, to, s) : backward_wide<T, false>(a, p, to, s);
+    }
+  } else {
+    if (sums)  // before dx, which may be written over dy or x
+      e = launch_pdl(ln_dw_long_kernel<T>, static_cast<unsigned>(strips * p.parts), kLnThreads, s, a, part);
+    if (e == cudaSuccess && a.y && a.rows)
+      e = launch_pdl(ln_dx_long_kernel<T>, static_cast<unsigned>(std::min<int64_t>(a.rows, 8 * dev.sms)), kLnThreads,
+                     s, a);
   }
-  if (e == cudaSuccess && a.y && a.rows)
-    e = launch_pdl(ln_dx_kernel<T>, static_cast<unsigned>(std::min<int64_t>(a.rows, 8 * dev.sms)), kLnThreads, s, a);
+  if (e == cudaSuccess && sums)
+    e = launch_pdl(ln_finish_kernel, static_cast<unsigned>((a.d + 31) / 32), 32 * kFinishSlices, s, dweight, dbias,
+                   static_cast<const float*>(part), a.d, p.parts, a.weight_type);
   return e;
 }
 
@@ -204,7 +681,7 @@ extern "C" int mp_layernorm_forward(void* y, float* mean, float* rstd, const voi
 extern "C" size_t mp_layernorm_workspace_bytes(int64_t rows, int64_t d) {
   using namespace mpk;
   if (!shape_ok(rows, d)) return 0;
-  return static_cast<size_t>(2) * kChunks * d * sizeof(float);
+  return static_cast<size_t>(2) * backward_plan(rows, d).parts * d * sizeof(float);
 }
 
 extern "C" int mp_layernorm_backward(void* dx, void* dweight, void* dbias, const void* dy, const void* x,

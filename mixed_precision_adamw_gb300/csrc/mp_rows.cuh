@@ -118,4 +118,105 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// ---- eight elements of a row ------------------------------------------------
+// A thread's unit of a row is eight elements, kept as stored until used. With
+// Wide they are consecutive (16-B loads and stores; the row must start on a
+// 16-B boundary and hold a multiple of eight elements), otherwise `step`
+// apart, so that neighbouring threads read neighbouring elements.
+__device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack2_fp16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <int T>
+struct Pack8 {  // bf16, fp16
+  uint4 v;
+
+  __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = v; }
+  __device__ __forceinline__ void load_stepped(const uint16_t* p, int64_t j, int64_t step, int64_t n) {
+    uint32_t h[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = j + e * step < n ? p[j + e * step] : 0u;
+    v = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
+  }
+  __device__ __forceinline__ void store_stepped(uint16_t* p, int64_t j, int64_t step, int64_t n) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (j + e * step < n) p[j + e * step] = static_cast<uint16_t>(e % 2 ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu);
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (T == MP_BF16) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      } else {
+        const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        f[2 * i] = g.x;
+        f[2 * i + 1] = g.y;
+      }
+    }
+  }
+  __device__ __forceinline__ void put(const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = T == MP_BF16 ? pack2_bf16(f[2 * i], f[2 * i + 1]) : pack2_fp16(f[2 * i], f[2 * i + 1]);
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+template <>
+struct Pack8<MP_FP32> {
+  float4 a, b;
+
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    reinterpret_cast<float4*>(p)[0] = a;
+    reinterpret_cast<float4*>(p)[1] = b;
+  }
+  __device__ __forceinline__ void load_stepped(const float* p, int64_t j, int64_t step, int64_t n) {
+    float h[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = j + e * step < n ? p[j + e * step] : 0.0f;
+    put(h);
+  }
+  __device__ __forceinline__ void store_stepped(float* p, int64_t j, int64_t step, int64_t n) const {
+    float h[8];
+    get(h);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (j + e * step < n) p[j + e * step] = h[e];
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  }
+  __device__ __forceinline__ void put(const float (&f)[8]) {
+    a = make_float4(f[0], f[1], f[2], f[3]);
+    b = make_float4(f[4], f[5], f[6], f[7]);
+  }
+};
+
+// Whether rows of `length` elements, `stride` apart from p on, can be read
+// and written as 16-B vectors of whole units.
+inline bool wide_rows(const void* p, int64_t length, int64_t stride, int64_t rows, int32_t type) {
+  const int64_t unit = type == MP_FP32 ? 4 : 8;
+  return aligned_to(p, 16) && length % 8 == 0 && (rows <= 1 || stride % unit == 0);
+}
+
 }  // namespace mpk
