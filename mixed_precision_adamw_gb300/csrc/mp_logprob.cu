@@ -1,15 +1,31 @@
 // mp_logprob.cu — log probabilities of given tokens with entropy and top
 // alternatives, and their backward pass.
+//
+// Forward: one pass over the logits (mp_softmax.cuh), so 2 B an element from
+// HBM for 16-bit logits is the floor. Few rows are split over the blocks of a
+// cluster, which join their statistics and candidates in the first block's
+// shared memory.
+//
+// Alternatives: the pass keeps the maximum of each chunk (32 or 16 elements)
+// a thread reads. The k-th largest of 32 maxima, each over one lane position
+// of the block's warps, bounds the k-th largest element from below, and only
+// chunks whose maximum reaches it are read again (about k of them): so the
+// pass itself pays one comparison per 32 elements for them.
 #include "mp_device.cuh"
 #include "mp_internal.h"
-#include "mp_rows.cuh"
+#include "mp_softmax.cuh"
 
 namespace mpk {
 namespace {
 
-constexpr int kLpThreads = 256;
+namespace cg = cooperative_groups;
+
+constexpr int kLpThreads = 256;  // at most
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kMaxTop = 32;
+constexpr int kSlots = 16;        // chunk maxima a thread keeps
+constexpr int kCandidates = 512;  // elements a block ranks without the slow form
+constexpr int kLpCluster = 8;     // blocks a row is split over at most
 
 struct LpArgs {
   float* logp;
@@ -32,97 +48,249 @@ struct LpArgs {
   const float* dentropy;
 };
 
-__device__ float block_max(float v, float* red) {
-  v = warp_max(v);
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
-  __syncthreads();
-  float s = red[0];
-  for (int w = 1; w < kLpWarps; ++w) s = max_nan(s, red[w]);
-  return s;
-}
-
-__device__ float block_sum(float v, float* red) {
-  v = warp_sum(v);
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
-  __syncthreads();
-  float s = 0.0f;
-  for (int w = 0; w < kLpWarps; ++w) s = __fadd_rn(s, red[w]);
-  return s;
-}
-
 // (order of the value, complement of the index): its maximum is the largest
-// value, the lowest index among equal ones.
-__device__ __forceinline__ uint64_t top_key(float x, int64_t j) {
-  return (static_cast<uint64_t>(order_of(x)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(j));
+// value, the lowest index among equal ones. 0 is below every element's key.
+__device__ __forceinline__ uint64_t top_key(uint32_t order, int64_t j) {
+  return (static_cast<uint64_t>(order) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(j));
 }
 
-template <int T>
-__global__ void __launch_bounds__(kLpThreads) lp_forward_kernel(LpArgs a) {
-  pdl_enter();
-  using E = Elem<T>;
-  __shared__ float red[kLpWarps];
-  __shared__ uint64_t redk[kLpWarps];
-  const float c = __fmul_rn(a.scale, kLog2E);
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-    const typename E::type* x = static_cast<const typename E::type*>(a.logits) + r * a.stride;
-    float m = -kInf;
-    for (int64_t j = threadIdx.x; j < a.vocab; j += kLpThreads) m = max_nan(m, E::get(x[j]));
-    m = block_max(m, red);
-    const bool empty = m == -kInf;
-    float s = 0.0f, u = 0.0f;
-    if (!empty)
-      for (int64_t j = threadIdx.x; j < a.vocab; j += kLpThreads) {
-        const float t = __fmul_rn(__fsub_rn(E::get(x[j]), m), c);
-        const float e = exp2_fast(t);
-        s = __fadd_rn(s, e);
-        if (e != 0.0f) u = __fmaf_rn(e, t, u);
-      }
-    s = block_sum(s, red);
-    u = block_sum(u, red);
-    const float log_s = logf(s);
-    const float lse = empty ? -kInf : __fadd_rn(__fmul_rn(m, a.scale), log_s);
-    if (threadIdx.x == 0) {
-      if (a.lse) a.lse[r] = lse;
-      if (a.entropy) a.entropy[r] = empty ? 0.0f : __fsub_rn(log_s, __fmul_rn(__fdiv_rn(u, s), kLn2));
-      if (a.logp) {
-        const int64_t t = load_index(a.targets, r, a.index_type);
-        float v = 0.0f;
-        if (t >= a.vocab) {
-          v = __int_as_float(0x7FC00000);
-          if (a.d_status) atomicCAS(a.d_status, 0, MP_ERR_RANGE);
-        } else if (t >= 0) {
-          v = empty ? -kInf : __fmaf_rn(__fsub_rn(E::get(x[t]), m), a.scale, -log_s);
+struct TopShared {
+  uint32_t lane_max[kLpWarps][32];
+  uint64_t keys[kCandidates + kMaxTop];
+  uint64_t warp_key[kLpWarps];
+  int warp_count[kLpWarps];
+  int count;
+};
+
+// Calls f(order, index) for the elements of this thread's chunks whose
+// maximum's order is at least `bound`.
+template <int T, typename F>
+__device__ __forceinline__ void visit_chunks(const RowPart<T>& p, const uint32_t* slots, int per_slot, uint32_t bound,
+                                             F&& f) {
+  constexpr int U = kUnits<T>;
+  const int threads = blockDim.x;
+  for (int slot = 0; slot < kSlots; ++slot) {
+    if (slots[slot * threads + threadIdx.x] < bound) continue;
+    for (int it = slot * per_slot; it < (slot + 1) * per_slot; ++it) {
+      const int64_t unit = p.first + static_cast<int64_t>(it) * U * threads + threadIdx.x;
+      if (unit >= p.last) break;
+      Pack8<T> x[U];
+      load_units(x, p, unit, threads);
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+        if (unit + q * threads >= p.last) continue;
+        float v[8];
+        x[q].get(v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t order = order_of(v[e]);
+          if (order >= bound) f(order, p.head + 8 * (unit + q * threads) + e);
         }
-        a.logp[r] = v;
       }
     }
-    uint64_t last = ~uint64_t{0};
-    for (int k = 0; k < a.top_k; ++k) {
-      uint64_t best = 0;
-      for (int64_t j = threadIdx.x; j < a.vocab; j += kLpThreads) {
-        const uint64_t key = top_key(E::get(x[j]), j);
-        if (key < last && key > best) best = key;
-      }
-      for (int o = 16; o > 0; o >>= 1) {
-        const uint64_t other = __shfl_xor_sync(kAll, best, o);
-        best = other > best ? other : best;
-      }
+  }
+  if (threadIdx.x < p.extra) {
+    const int64_t j = p.extra_index(threadIdx.x);
+    const uint32_t order = order_of(Elem<T>::get(p.row[j]));
+    if (order >= bound) f(order, j);
+  }
+}
+
+// Leaves the keys of the part's k largest elements (and perhaps more) in
+// sh.keys and returns their number, to every thread.
+template <int T>
+__device__ int find_top(const RowPart<T>& p, int k, const uint32_t* slots, int per_slot, uint32_t thread_max,
+                        TopShared& sh) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
+  sh.lane_max[warp][lane] = thread_max;
+  if (threadIdx.x == 0) sh.count = 0;
+  __syncthreads();
+  // the k-th largest of the 32 lane positions' maxima
+  uint32_t mine = 0;
+  for (int w = 0; w < warps; ++w) mine = max(mine, sh.lane_max[w][lane]);
+  int rank = 0;
+#pragma unroll
+  for (int l = 0; l < 32; ++l) {
+    const uint32_t other = __shfl_sync(kAll, mine, l);
+    rank += other > mine || (other == mine && l < lane);
+  }
+  const uint32_t bound = __shfl_sync(kAll, mine, __ffs(__ballot_sync(kAll, rank == k - 1)) - 1);
+  visit_chunks<T>(p, slots, per_slot, bound, [&](uint32_t order, int64_t j) {
+    const int at = atomicAdd(&sh.count, 1);
+    if (at < kCandidates) sh.keys[at] = top_key(order, j);
+  });
+  __syncthreads();
+  int n = sh.count;
+  if (n <= kCandidates) return n;
+  // Many elements equal to the bound (masked rows, equal logits): those above
+  // it, then the first of the equal ones in index order.
+  __syncthreads();
+  if (threadIdx.x == 0) sh.count = 0;
+  __syncthreads();
+  visit_chunks<T>(p, slots, per_slot, bound + 1, [&](uint32_t order, int64_t j) {
+    const int at = atomicAdd(&sh.count, 1);
+    if (at < kCandidates) sh.keys[at] = top_key(order, j);
+  });
+  __syncthreads();
+  n = sh.count;
+  // The part's elements in index order, one per thread and round; the extra
+  // elements before the units belong to it, those after them come last.
+  const int64_t from = p.extra ? 0 : p.head + 8 * p.first;
+  const int64_t body_end = p.head + 8 * p.last;
+  const int64_t tail = p.extra ? p.extra - p.head : 0;
+  const int64_t total = body_end - from + tail;
+  auto element = [&](int64_t i) { return i < body_end - from ? from + i : p.head + 8 * p.units + (i - (body_end - from)); };
+  if (bound != 0xFFFFFFFFu && n <= kCandidates) {
+    for (int64_t base = 0; base < total && n < kCandidates + kMaxTop; base += blockDim.x) {
+      const int64_t i = base + threadIdx.x;
+      const bool equal = i < total && order_of(Elem<T>::get(p.row[element(i)])) == bound;
+      const uint32_t votes = __ballot_sync(kAll, equal);
+      if (lane == 0) sh.warp_count[warp] = __popc(votes);
       __syncthreads();
-      if (threadIdx.x % 32 == 0) redk[threadIdx.x / 32] = best;
+      int at = n + __popc(votes & ((1u << lane) - 1));
+      int sum = 0;
+      for (int w = 0; w < warps; ++w) {
+        if (w < warp) at += sh.warp_count[w];
+        sum += sh.warp_count[w];
+      }
+      if (equal && at < kCandidates + kMaxTop) sh.keys[at] = top_key(bound, element(i));
+      n = min(n + sum, kCandidates + kMaxTop);
       __syncthreads();
-      for (int w = 0; w < kLpWarps; ++w) best = redk[w] > best ? redk[w] : best;
-      last = best;
+      if (n >= k && sh.count + k <= n) break;
+    }
+    return n;
+  }
+  // Very many above the bound (or NaN): the largest key below the last one, k times.
+  uint64_t last = ~uint64_t{0};
+  for (int q = 0; q < k; ++q) {
+    uint64_t best = 0;
+    for (int64_t i = threadIdx.x; i < total; i += blockDim.x) {
+      const uint64_t key = top_key(order_of(Elem<T>::get(p.row[element(i)])), element(i));
+      if (key < last && key > best) best = key;
+    }
+    for (int o = 16; o > 0; o >>= 1) {
+      const uint64_t other = __shfl_xor_sync(kAll, best, o);
+      best = other > best ? other : best;
+    }
+    __syncthreads();
+    if (lane == 0) sh.warp_key[warp] = best;
+    __syncthreads();
+    for (int w = 0; w < warps; ++w) best = sh.warp_key[w] > best ? sh.warp_key[w] : best;
+    if (threadIdx.x == 0) sh.keys[q] = best;
+    last = best;
+  }
+  __syncthreads();
+  return k;
+}
+
+// Calls f(rank, key) for the k largest of n keys (all different, or 0).
+template <typename F>
+__device__ __forceinline__ void rank_keys(const uint64_t* keys, int n, int k, F&& f) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const uint64_t key = keys[i];
+    if (key == 0) continue;
+    int rank = 0;
+    for (int q = 0; q < n; ++q) rank += keys[q] > key;
+    if (rank < k) f(rank, key);
+  }
+}
+
+template <int T, bool Entropy, bool Top>
+__global__ void __launch_bounds__(kLpThreads, 4) lp_forward_kernel(LpArgs a, int per_slot) {
+  pdl_enter();
+  using E = typename Elem<T>::type;
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int parts = cluster.num_blocks(), part = cluster.block_rank();
+  __shared__ RowStats red[kLpWarps];
+  __shared__ RowStats part_stats[kLpCluster];                       // of the first block: every block's
+  __shared__ uint64_t part_keys[Top ? kLpCluster * kMaxTop : 1];    // likewise
+  __shared__ TopShared top;
+  extern __shared__ uint32_t slots[];
+  const float c = __fmul_rn(a.scale, kLog2E), slack = __fdiv_rn(kSlack, c);
+  const int threads = blockDim.x;
+  const int64_t teams = gridDim.x / parts;
+  for (int64_t r = blockIdx.x / parts; r < a.rows; r += teams) {
+    const E* x = static_cast<const E*>(a.logits) + r * a.stride;
+    const RowPart<T> p(x, a.vocab, part, parts);
+    RowStats st;
+    int it = 0;
+    uint32_t slot_max = 0;
+    if (Top)
+      for (int q = 0; q < kSlots; ++q) slots[q * threads + threadIdx.x] = 0;
+    scan_row<T, Entropy>(st, p, c, slack, [&](float m) {
+      if (Top) {
+        const uint32_t order = order_of(m);
+        slot_max = it % per_slot ? max(slot_max, order) : order;
+        slots[it / per_slot * threads + threadIdx.x] = slot_max;
+        ++it;
+      }
+    });
+    const bool some = p.first + threadIdx.x < p.last || threadIdx.x < p.extra;
+    const uint32_t thread_max = some ? order_of(st.m) : 0;
+    st = join_block(st, red);
+    int n = 0;
+    if (Top) n = find_top<T>(p, a.top_k, slots, per_slot, thread_max, top);
+    const uint64_t* keys = top.keys;
+    if (parts > 1) {
+      if (threadIdx.x == 0) *cluster.map_shared_rank(&part_stats[part], 0) = st;
+      if (Top) {
+        uint64_t* to = cluster.map_shared_rank(&part_keys[part * kMaxTop], 0);
+        if (threadIdx.x >= min(n, a.top_k) && threadIdx.x < kMaxTop) to[threadIdx.x] = 0;
+        rank_keys(top.keys, n, a.top_k, [&](int rank, uint64_t key) { to[rank] = key; });
+      }
+      cluster.sync();
+      if (part == 0) {
+        float R = part_stats[0].R;
+        for (int q = 1; q < parts; ++q) R = max_nan(R, part_stats[q].R);
+        st = part_stats[0];
+        rebase(st, R);
+        for (int q = 1; q < parts; ++q) {
+          RowStats b = part_stats[q];
+          rebase(b, R);
+          st.m = max_nan(st.m, b.m);
+          st.s = __fadd_rn(st.s, b.s);
+          st.u = __fadd_rn(st.u, b.u);
+        }
+        st.R = R;
+        keys = part_keys;
+        n = parts * kMaxTop;
+      }
+    }
+    if (part == 0) {
+      const bool plain = out_of_range(st);
+      if (plain) st = plain_stats<T, Entropy>(x, a.vocab, st.m, c, red);
+      const RowLog log(st, plain, c, a.scale);
       if (threadIdx.x == 0) {
-        const uint32_t j = 0xFFFFFFFFu - static_cast<uint32_t>(best);
-        a.top_index[r * a.top_k + k] = static_cast<int32_t>(j);
-        a.top_logp[r * a.top_k + k] = empty ? -kInf : __fmaf_rn(__fsub_rn(E::get(x[j]), m), a.scale, -log_s);
+        if (a.lse) a.lse[r] = log.lse;
+        if (Entropy) a.entropy[r] = log.entropy;
+        if (a.logp) {
+          const int64_t t = load_index(a.targets, r, a.index_type);
+          float v = 0.0f;
+          if (t >= a.vocab) {
+            v = __int_as_float(0x7FC00000);
+            if (a.d_status) atomicCAS(a.d_status, 0, MP_ERR_RANGE);
+          } else if (t >= 0) {
+            v = log.log_p(Elem<T>::get(x[t]));
+          }
+          a.logp[r] = v;
+        }
       }
+      if (Top)
+        rank_keys(keys, n, a.top_k, [&](int rank, uint64_t key) {
+          a.top_index[r * a.top_k + rank] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(key));
+          a.top_logp[r * a.top_k + rank] = log.log_p(value_of_order(static_cast<uint32_t>(key >> 32)));
+        });
+    }
+    if (r + teams < a.rows) {  // before the next row's sums go where this row's were read
+      if (parts > 1)
+        cluster.sync();
+      else
+        __syncthreads();
     }
   }
 }
 
+// ---- backward ---------------------------------------------------------------
 template <int T>
 __global__ void __launch_bounds__(kLpThreads) lp_backward_kernel(LpArgs a) {
   pdl_enter();
@@ -157,10 +325,51 @@ __global__ void __launch_bounds__(kLpThreads) lp_backward_kernel(LpArgs a) {
   }
 }
 
+// Threads of a block and blocks of a row. A thread should have at least one
+// chunk; rows are split over a cluster while that leaves the grid short of
+// two blocks an SM and each block with a chunk a thread.
+struct RowPlan {
+  int threads, parts;
+};
+
+RowPlan row_plan(int64_t rows, int64_t vocab, int type, const DeviceInfo& dev) {
+  const int64_t chunk = type == MP_FP32 ? 16 : 32;
+  RowPlan p;
+  p.threads = static_cast<int>(std::min<int64_t>(kLpThreads, std::max<int64_t>(1, (vocab / chunk + 31) / 32) * 32));
+  p.parts = 1;
+  while (p.parts < kLpCluster && rows * p.parts * 2 <= 2 * dev.sms && vocab / (2 * p.parts) >= chunk * p.threads / 2)
+    p.parts *= 2;
+  return p;
+}
+
+template <int T, bool Entropy, bool Top>
+cudaError_t launch_forward(const LpArgs& a, const DeviceInfo& dev, cudaStream_t s) {
+  const RowPlan p = row_plan(a.rows, a.vocab, T, dev);
+  const int64_t per_part = (a.vocab / 8 + p.parts - 1) / p.parts + 1;
+  const int64_t step = static_cast<int64_t>(kUnits<T>) * p.threads;
+  const int64_t its = (per_part + step - 1) / step;
+  const int per_slot = static_cast<int>((its + kSlots - 1) / kSlots);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.parts;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(a.rows, 1 << 24) * p.parts));
+  cfg.blockDim = dim3(p.threads);
+  cfg.dynamicSmemBytes = Top ? kSlots * p.threads * sizeof(uint32_t) : 0;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, lp_forward_kernel<T, Entropy, Top>, a, per_slot);
+}
+
 template <int T>
 cudaError_t forward(const LpArgs& a, const DeviceInfo& dev, cudaStream_t s) {
-  return launch_pdl(lp_forward_kernel<T>, static_cast<unsigned>(std::min<int64_t>(a.rows, 8 * dev.sms)), kLpThreads,
-                    s, a);
+  if (a.entropy) return a.top_k ? launch_forward<T, true, true>(a, dev, s) : launch_forward<T, true, false>(a, dev, s);
+  return a.top_k ? launch_forward<T, false, true>(a, dev, s) : launch_forward<T, false, false>(a, dev, s);
 }
 
 template <int T>

@@ -44,6 +44,7 @@ struct Elem<MP_BF16> {
   using type = uint16_t;
   static __device__ __forceinline__ float get(uint16_t h) { return __uint_as_float(static_cast<uint32_t>(h) << 16); }
   static __device__ __forceinline__ uint16_t put(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+  static constexpr uint16_t kMinusInf = 0xFF80;
 };
 
 template <>
@@ -51,6 +52,7 @@ struct Elem<MP_FP16> {
   using type = uint16_t;
   static __device__ __forceinline__ float get(uint16_t h) { return __half2float(__ushort_as_half(h)); }
   static __device__ __forceinline__ uint16_t put(float x) { return __half_as_ushort(__float2half_rn(x)); }
+  static constexpr uint16_t kMinusInf = 0xFC00;
 };
 
 template <>
@@ -58,6 +60,7 @@ struct Elem<MP_FP32> {
   using type = float;
   static __device__ __forceinline__ float get(float x) { return x; }
   static __device__ __forceinline__ float put(float x) { return x; }
+  static constexpr float kMinusInf = -kInf;
 };
 
 // One element of a vector whose type is known at run time only (weights:
@@ -140,6 +143,10 @@ struct Pack8 {  // bf16, fp16
   uint4 v;
 
   __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void fill(uint16_t h) {
+    const uint32_t w = h | (static_cast<uint32_t>(h) << 16);
+    v = make_uint4(w, w, w, w);
+  }
   __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = v; }
   __device__ __forceinline__ void load_stepped(const uint16_t* p, int64_t j, int64_t step, int64_t n) {
@@ -182,6 +189,7 @@ struct Pack8<MP_FP32> {
   float4 a, b;
 
   __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+  __device__ __forceinline__ void fill(float f) { a = b = make_float4(f, f, f, f); }
   __device__ __forceinline__ void load(const float* p) {
     a = reinterpret_cast<const float4*>(p)[0];
     b = reinterpret_cast<const float4*>(p)[1];
@@ -211,6 +219,42 @@ struct Pack8<MP_FP32> {
     b = make_float4(f[4], f[5], f[6], f[7]);
   }
 };
+
+// The largest of U units' elements, NaN if one is NaN.
+template <int T, int U>
+__device__ __forceinline__ float max_of(const Pack8<T> (&x)[U]) {
+  if constexpr (T == MP_FP32) {
+    float m = x[0].a.x;
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      float f[8];
+      x[q].get(f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = max_nan(m, f[e]);
+    }
+    return m;
+  } else {
+    uint32_t w[4 * U];
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      w[4 * q] = x[q].v.x;
+      w[4 * q + 1] = x[q].v.y;
+      w[4 * q + 2] = x[q].v.z;
+      w[4 * q + 3] = x[q].v.w;
+    }
+#pragma unroll
+    for (int n = 4 * U; n > 1; n /= 2)
+#pragma unroll
+      for (int i = 0; i < n / 2; ++i) {
+        if (T == MP_BF16)
+          asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(w[i + n / 2]));
+        else
+          asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(w[i + n / 2]));
+      }
+    const uint16_t lo = static_cast<uint16_t>(w[0]), hi = static_cast<uint16_t>(w[0] >> 16);
+    return max_nan(Elem<T>::get(lo), Elem<T>::get(hi));
+  }
+}
 
 // Whether rows of `length` elements, `stride` apart from p on, can be read
 // and written as 16-B vectors of whole units.

@@ -1,0 +1,237 @@
+// mp_softmax.cuh — one pass over a row of logits (or a segment of one): the
+// sum of exponentials relative to a running reference, and with it the sum
+// that gives the entropy.
+//
+// With c = scale * log2(e), a reference R in log2 units and t = c x - R (one
+// FMA, rounded once):
+//   s = sum 2^t,   u = sum t 2^t
+// and with delta = c m - R for the largest element m and L = log2(s / 2^delta)
+//   lse = scale m + L ln 2,   entropy = (delta + L - u / s) ln 2
+//   log p(x) = scale (x - m) - L ln 2
+// (L is exactly 0, and with it the largest element's log p, where one element
+// has all the probability.) R is whatever rounded value is subtracted, so its own rounding costs
+// nothing; the rounding of c is a relative change of the scale by at most
+// 2^-24. R follows the running maximum lazily: it moves only when a chunk's
+// maximum exceeds the one it was taken from by 8 / c, so a rescale is rare and
+// no term grows past 2^8.
+#pragma once
+
+#include <cooperative_groups.h>
+
+#include "mp_rows.cuh"
+
+namespace mpk {
+
+constexpr float kSlack = 8.0f;       // log2 units R may lag behind the maximum
+constexpr float kLowest = -200.0f;   // 2^-200 is 0: t below it counts as it (its product with 2^t is 0)
+
+struct RowStats {
+  float R;    // reference in log2 units; -inf: no element yet
+  float lim;  // a maximum above this moves R
+  float s, u;
+  float m;    // largest element
+
+  __device__ __forceinline__ void clear() {
+    R = lim = m = -kInf;
+    s = u = 0.0f;
+  }
+};
+
+// Moves the reference to the maximum `top`.
+__device__ __forceinline__ void move_reference(RowStats& a, float top, float c, float slack) {
+  const float R = __fmul_rn(top, c);
+  if (a.R == -kInf) {
+    a.s = a.u = 0.0f;
+  } else {
+    const float d = __fsub_rn(a.R, R), f = exp2_fast(d);
+    a.u = __fmul_rn(f, __fmaf_rn(d, a.s, a.u));
+    a.s = __fmul_rn(f, a.s);
+  }
+  a.R = R;
+  a.lim = __fadd_rn(top, slack);
+}
+
+// Adds U units, whose maximum is `top`.
+template <int T, int U, bool Entropy>
+__device__ __forceinline__ void add_units(RowStats& a, const Pack8<T> (&x)[U], float top, float c, float slack) {
+  a.m = max_nan(a.m, top);
+  if (!(top <= a.lim)) move_reference(a, top, c, slack);
+  const float R = a.R;
+#pragma unroll
+  for (int q = 0; q < U; ++q) {
+    float f[8];
+    x[q].get(f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float t = __fmaf_rn(f[e], c, -R);
+      if (Entropy) t = max_nan(t, kLowest);
+      const float p = exp2_fast(t);
+      a.s = __fadd_rn(a.s, p);
+      if (Entropy) a.u = __fmaf_rn(p, t, a.u);
+    }
+  }
+}
+
+// Adds the statistics of disjoint parts: `a` brought to the reference R.
+// Parts without a reference (empty, or below the range of c x) add nothing.
+__device__ __forceinline__ void rebase(RowStats& a, float R) {
+  if (a.R == -kInf) {
+    a.s = a.u = 0.0f;
+  } else {
+    const float d = __fsub_rn(a.R, R), f = exp2_fast(d);
+    a.u = d < kLowest ? 0.0f : __fmul_rn(f, __fmaf_rn(d, a.s, a.u));
+    a.s = __fmul_rn(f, a.s);
+  }
+}
+
+// A row, or the part [first, last) of its units, as the threads of a block
+// read it: whole units on 16-B boundaries, and the fewer than 16 elements
+// before and after them one by one (read by the first part's threads).
+template <int T>
+struct RowPart {
+  using E = typename Elem<T>::type;
+  const E* row;
+  const E* body;        // row + head, 16-B aligned
+  int64_t first, last;  // units
+  int head, extra;      // elements before the units; before and after them (0 unless this is part 0)
+  int64_t units, n;
+
+  __device__ __forceinline__ RowPart(const E* p, int64_t length, int part, int parts) : row(p), n(length) {
+    constexpr int kAlign = 16 / sizeof(E);
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) / sizeof(E) % kAlign);
+    head = off ? kAlign - off : 0;
+    if (head > n) head = static_cast<int>(n);
+    units = (n - head) / 8;
+    body = p + head;
+    first = units * part / parts;
+    last = units * (part + 1) / parts;
+    extra = part == 0 ? static_cast<int>(n - 8 * units) : 0;
+  }
+  // index of the i-th extra element
+  __device__ __forceinline__ int64_t extra_index(int i) const { return i < head ? i : 8 * units + i; }
+};
+
+template <int T, int U>
+__device__ __forceinline__ void load_units(Pack8<T> (&x)[U], const RowPart<T>& p, int64_t unit, int64_t step) {
+#pragma unroll
+  for (int q = 0; q < U; ++q) {
+    const int64_t i = unit + q * step;
+    if (i < p.last)
+      x[q].load(p.body + 8 * i);
+    else
+      x[q].fill(Elem<T>::kMinusInf);
+  }
+}
+
+// Units a thread has in flight: 64 B.
+template <int T>
+constexpr int kUnits = T == MP_FP32 ? 2 : 4;
+
+// The whole part, by all threads of the block. chunk(top) is called with each
+// chunk's maximum, in the order of the chunks (chunk i of thread t: units
+// first + (i U + q) threads + t, q < U).
+template <int T, bool Entropy, typename Chunk>
+__device__ __forceinline__ void scan_row(RowStats& a, const RowPart<T>& p, float c, float slack, Chunk&& chunk) {
+  constexpr int U = kUnits<T>;
+  const int threads = blockDim.x;
+  a.clear();
+  Pack8<T> x[U];
+  int64_t i = p.first;
+  if (i < p.last) load_units(x, p, i + threadIdx.x, threads);
+  while (i < p.last) {
+    Pack8<T> next[U];
+    const int64_t after = i + static_cast<int64_t>(U) * threads;
+    if (after < p.last) load_units(next, p, after + threadIdx.x, threads);
+    const float top = max_of<T, U>(x);
+    chunk(top);
+    add_units<T, U, Entropy>(a, x, top, c, slack);
+#pragma unroll
+    for (int q = 0; q < U; ++q) x[q] = next[q];
+    i = after;
+  }
+  if (threadIdx.x < p.extra) {
+    Pack8<T> one[1];
+    float f[8] = {-kInf, -kInf, -kInf, -kInf, -kInf, -kInf, -kInf, -kInf};
+    f[0] = Elem<T>::get(p.row[p.extra_index(threadIdx.x)]);
+    one[0].put(f);
+    add_units<T, 1, Entropy>(a, one, f[0], c, slack);
+  }
+}
+
+// The block's statistics, to every thread. `red` has one entry per warp.
+__device__ __forceinline__ RowStats join_block(RowStats a, RowStats* red) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
+  const float R = warp_max(a.R);
+  rebase(a, R);
+  a.R = R;
+  a.m = warp_max(a.m);
+  a.s = warp_sum(a.s);
+  a.u = warp_sum(a.u);
+  __syncthreads();
+  if (lane == 0) red[warp] = a;
+  __syncthreads();
+  a = red[0];
+  float top = a.R;
+  for (int w = 1; w < warps; ++w) top = max_nan(top, red[w].R);
+  rebase(a, top);
+  a.R = top;
+  for (int w = 1; w < warps; ++w) {
+    RowStats b = red[w];
+    rebase(b, top);
+    a.m = max_nan(a.m, b.m);
+    a.s = __fadd_rn(a.s, b.s);
+    a.u = __fadd_rn(a.u, b.u);
+  }
+  return a;
+}
+
+// Whether the row's finite maximum left the range of c x: its statistics have
+// to be taken from differences instead (plain_stats).
+__device__ __forceinline__ bool out_of_range(const RowStats& a) {
+  return isfinite(a.m) && !(fabsf(a.R) <= 1e38f);
+}
+
+// The slow form for such rows, by all threads of a block over the whole row:
+// t = (x - m) c. On return R is 0 and t = (x - m) c replaces c x - R.
+template <int T, bool Entropy>
+__device__ __noinline__ RowStats plain_stats(const typename Elem<T>::type* row, int64_t n, float m, float c,
+                                             RowStats* red) {
+  RowStats a;
+  a.R = 0.0f;
+  a.lim = 0.0f;
+  a.s = a.u = 0.0f;
+  a.m = m;
+  for (int64_t j = threadIdx.x; j < n; j += blockDim.x) {
+    const float t = max_nan(__fmul_rn(__fsub_rn(Elem<T>::get(row[j]), m), c), kLowest);
+    const float p = exp2_fast(t);
+    a.s = __fadd_rn(a.s, p);
+    if (Entropy) a.u = __fmaf_rn(p, t, a.u);
+  }
+  return join_block(a, red);
+}
+
+// The logarithms of a row's joined statistics.
+struct RowLog {
+  float m, scale, log_sum, entropy, lse;
+  bool empty;
+
+  __device__ __forceinline__ RowLog(const RowStats& a, bool plain, float c, float scale_)
+      : m(a.m), scale(scale_), empty(a.m == -kInf) {
+    const float delta = plain ? 0.0f : __fmaf_rn(m, c, -a.R);
+    const float p = exp2_fast(delta);
+    const float L = log2f(__fdiv_rn(a.s, p));
+    const float own = __fmul_rn(p, delta);
+    // sums that hold the largest element's terms alone: one token has all the probability
+    entropy = empty || (a.s == p && a.u == own)
+                  ? 0.0f
+                  : __fmul_rn(__fadd_rn(__fsub_rn(delta, __fdiv_rn(a.u, a.s)), L), kLn2);
+    log_sum = __fmul_rn(L, kLn2);
+    lse = empty ? -kInf : __fmaf_rn(m, scale, log_sum);
+  }
+  // log p(x) of an element of the row
+  __device__ __forceinline__ float log_p(float x) const {
+    return empty ? -kInf : __fmaf_rn(__fsub_rn(x, m), scale, -log_sum);
+  }
+};
+
+}  // namespace mpk
