@@ -175,8 +175,9 @@ int mp_token_logprob_backward(void* dlogits, const void* logits, const void* tar
  * A teacher logit of -inf has q = 0 and adds nothing. A row without a listed
  * token of q > 0 has loss 0 and a zero gradient. A listed token of q > 0
  * whose student logit is -inf makes the loss +inf. A student row that is
- * -inf throughout has a zero gradient. NaN in a row's logits or listed
- * teacher logits, or +inf, makes its loss and gradient NaN.
+ * -inf throughout has a zero gradient. NaN or +inf among a row's logits
+ * makes its loss and gradient NaN, among its listed teacher logits the loss
+ * and the gradient of the listed tokens.
  * Errors: MP_ERR_NULL, MP_ERR_ALIGN, MP_ERR_RANGE, MP_ERR_CUDA.
  * ------------------------------------------------------------------------- */
 int mp_distill_topk(float* loss, void* dlogits, const void* logits, const void* teacher, const void* index,

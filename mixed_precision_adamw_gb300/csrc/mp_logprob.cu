@@ -291,14 +291,21 @@ __global__ void __launch_bounds__(kLpThreads, 4) lp_forward_kernel(LpArgs a, int
 }
 
 // ---- backward ---------------------------------------------------------------
+// dx / scale = p (-g - h (entropy + log p)) + g [j = target], for dlogp = g and
+// dentropy = h: elementwise, 4 B an element for 16-bit types. log p =
+// scale x - lse is rounded once, so its error is relative to log p, small
+// where p is large. A row is divided over `parts` blocks.
 template <int T>
-__global__ void __launch_bounds__(kLpThreads) lp_backward_kernel(LpArgs a) {
+__global__ void __launch_bounds__(kLpThreads) lp_backward_kernel(LpArgs a, int parts) {
   pdl_enter();
-  using E = Elem<T>;
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-    const typename E::type* x = static_cast<const typename E::type*>(a.logits) + r * a.stride;
-    typename E::type* dx = static_cast<typename E::type*>(a.dlogits) + r * a.dlogits_stride;
-    const float lse = a.lse_in[r];
+  using E = typename Elem<T>::type;
+  const int part = blockIdx.x % parts;
+  const int64_t teams = gridDim.x / parts;
+  for (int64_t r = blockIdx.x / parts; r < a.rows; r += teams) {
+    const E* x = static_cast<const E*>(a.logits) + r * a.stride;
+    E* dx = static_cast<E*>(a.dlogits) + r * a.dlogits_stride;
+    const RowPart<T> out(dx, a.vocab, part, parts);
+    const float lse = a.lse_in[r], scale = a.scale;
     int64_t t = a.targets ? load_index(a.targets, r, a.index_type) : -1;
     if (t >= a.vocab) {
       if (a.d_status && threadIdx.x == 0) atomicCAS(a.d_status, 0, MP_ERR_RANGE);
@@ -306,22 +313,29 @@ __global__ void __launch_bounds__(kLpThreads) lp_backward_kernel(LpArgs a) {
     }
     const float g = t >= 0 ? a.dlogp[r] : 0.0f;
     const float h = a.dentropy ? a.dentropy[r] : 0.0f;
-    const float ent = a.dentropy ? a.entropy_in[r] : 0.0f;
-    const bool zero = (g == 0.0f && h == 0.0f) || lse == -kInf;
-    // dx / scale = p (-g - h (ent + log p)) + g [j = t]; log p = scale x - lse is
-    // rounded once, so its error is relative to log p, small where p is large
-    const float a0 = __fsub_rn(-g, __fmul_rn(h, ent));
-    for (int64_t j = threadIdx.x; j < a.vocab; j += kLpThreads) {
-      float v = 0.0f;
-      if (!zero) {
-        const float y = __fmaf_rn(E::get(x[j]), a.scale, -lse);
-        const float p = exp2_fast(__fmul_rn(y, kLog2E));
-        v = p == 0.0f ? 0.0f : __fmul_rn(p, __fmaf_rn(-h, y, a0));
-        if (j == t) v = __fadd_rn(v, g);
-        v = __fmul_rn(v, a.scale);
-      }
-      dx[j] = E::put(v);
+    if ((g == 0.0f && h == 0.0f) || lse == -kInf) {
+      zero_row<T>(out, dx);
+      continue;
     }
+    const float a0 = __fmul_rn(-scale, __fmaf_rn(h, a.dentropy ? a.entropy_in[r] : 0.0f, g));
+    const float a1 = __fmul_rn(-scale, h);
+    // the target's element is written by one thread, from the value read before the row is overwritten
+    const float xt = t >= 0 ? Elem<T>::get(x[t]) : 0.0f;
+    __syncthreads();
+    auto of = [&](float v) {
+      const float y = __fmaf_rn(v, scale, -lse);
+      const float p = exp2_fast(__fmul_rn(y, kLog2E));
+      // y is finite where p is not 0 (or NaN)
+      return __fmul_rn(p, __fmaf_rn(a1, max_nan(y, kLowest), a0));
+    };
+    if (h == 0.0f)
+      map_row<T>(out, dx, x, [&](float v) {
+        return __fmul_rn(a0, exp2_fast(__fmul_rn(__fmaf_rn(v, scale, -lse), kLog2E)));
+      });
+    else
+      map_row<T>(out, dx, x, of);
+    __syncthreads();
+    if (t >= 0 && threadIdx.x == 0 && out.holds(t)) dx[t] = Elem<T>::put(__fmaf_rn(g, scale, of(xt)));
   }
 }
 
@@ -374,8 +388,12 @@ cudaError_t forward(const LpArgs& a, const DeviceInfo& dev, cudaStream_t s) {
 
 template <int T>
 cudaError_t backward(const LpArgs& a, const DeviceInfo& dev, cudaStream_t s) {
-  return launch_pdl(lp_backward_kernel<T>, static_cast<unsigned>(std::min<int64_t>(a.rows, 8 * dev.sms)), kLpThreads,
-                    s, a);
+  const int64_t units = a.vocab / 8, step = static_cast<int64_t>(kUnits<T>) * 32;
+  const int threads = static_cast<int>(std::min<int64_t>(kLpThreads, std::max<int64_t>(1, units / step) * 32));
+  int parts = 1;
+  while (parts < 64 && a.rows * parts < 4 * dev.sms && units / (2 * parts) >= kUnits<T> * threads / 2) parts *= 2;
+  return launch_pdl(lp_backward_kernel<T>, static_cast<unsigned>(std::min<int64_t>(a.rows, 1 << 24) * parts),
+                    static_cast<unsigned>(threads), s, a, parts);
 }
 
 }  // namespace

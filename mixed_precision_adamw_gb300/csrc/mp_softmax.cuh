@@ -107,6 +107,11 @@ struct RowPart {
     last = units * (part + 1) / parts;
     extra = part == 0 ? static_cast<int>(n - 8 * units) : 0;
   }
+  // whether element j is this part's
+  __device__ __forceinline__ bool holds(int64_t j) const {
+    if (j < head || j >= head + 8 * units) return extra > 0;
+    return j >= head + 8 * first && j < head + 8 * last;
+  }
   // index of the i-th extra element
   __device__ __forceinline__ int64_t extra_index(int i) const { return i < head ? i : 8 * units + i; }
 };
@@ -126,6 +131,55 @@ __device__ __forceinline__ void load_units(Pack8<T> (&x)[U], const RowPart<T>& p
 // Units a thread has in flight: 64 B.
 template <int T>
 constexpr int kUnits = T == MP_FP32 ? 2 : 4;
+
+// Eight elements of a row from element j on, wherever they lie: one 16-B load
+// (two for fp32) if they start on a 16-B boundary, element by element if not.
+template <int T>
+__device__ __forceinline__ void load_any(Pack8<T>& x, const typename Elem<T>::type* row, int64_t j, bool aligned) {
+  if (aligned)
+    x.load(row + j);
+  else
+    x.load_stepped(row, j, 1, j + 8);
+}
+
+// Writes f(x[j]) for a part of a row: `out` divides dx (its alignment), x is
+// read to match. Each thread reads what it writes, so dx may be x.
+template <int T, typename F>
+__device__ __forceinline__ void map_row(const RowPart<T>& out, typename Elem<T>::type* dx,
+                                        const typename Elem<T>::type* x, F&& f) {
+  using E = typename Elem<T>::type;
+  constexpr int U = kUnits<T>;
+  const int threads = blockDim.x;
+  const bool aligned = reinterpret_cast<uintptr_t>(x + out.head) % 16 == 0;
+  for (int64_t i = out.first + threadIdx.x; i < out.last; i += static_cast<int64_t>(U) * threads) {
+    Pack8<T> u[U];
+#pragma unroll
+    for (int q = 0; q < U; ++q)
+      if (i + q * threads < out.last) load_any<T>(u[q], x, out.head + 8 * (i + q * threads), aligned);
+#pragma unroll
+    for (int q = 0; q < U; ++q)
+      if (i + q * threads < out.last) {
+        float v[8];
+        u[q].get(v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = f(v[e]);
+        u[q].put(v);
+        u[q].store(dx + out.head + 8 * (i + q * threads));
+      }
+  }
+  if (threadIdx.x < out.extra) {
+    const int64_t j = out.extra_index(threadIdx.x);
+    dx[j] = Elem<T>::put(f(Elem<T>::get(x[j])));
+  }
+}
+
+template <int T>
+__device__ __forceinline__ void zero_row(const RowPart<T>& out, typename Elem<T>::type* dx) {
+  Pack8<T> z;
+  z.zero();
+  for (int64_t i = out.first + threadIdx.x; i < out.last; i += blockDim.x) z.store(dx + out.head + 8 * i);
+  if (threadIdx.x < out.extra) dx[out.extra_index(threadIdx.x)] = Elem<T>::put(0.0f);
+}
 
 // The whole part, by all threads of the block. chunk(top) is called with each
 // chunk's maximum, in the order of the chunks (chunk i of thread t: units
