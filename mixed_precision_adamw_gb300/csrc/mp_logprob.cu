@@ -25,6 +25,7 @@ constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kMaxTop = 32;
 constexpr int kSlots = 16;        // chunk maxima a thread keeps
 constexpr int kCandidates = 512;  // elements a block ranks without the slow form
+constexpr int kVisits = 256;      // chunks it reads again without it
 constexpr int kLpCluster = 8;     // blocks a row is split over at most
 
 struct LpArgs {
@@ -59,51 +60,77 @@ struct TopShared {
   uint64_t keys[kCandidates + kMaxTop];
   uint64_t warp_key[kLpWarps];
   int warp_count[kLpWarps];
-  int count;
+  uint32_t visits[kVisits];  // slot * 256 + thread
+  int count, visit_count;
 };
 
-// Calls f(order, index) for the elements of this thread's chunks whose
-// maximum's order is at least `bound`.
-template <int T, typename F>
-__device__ __forceinline__ void visit_chunks(const RowPart<T>& p, const uint32_t* slots, int per_slot, uint32_t bound,
-                                             F&& f) {
-  constexpr int U = kUnits<T>;
-  const int threads = blockDim.x;
-  for (int slot = 0; slot < kSlots; ++slot) {
-    if (slots[slot * threads + threadIdx.x] < bound) continue;
-    for (int it = slot * per_slot; it < (slot + 1) * per_slot; ++it) {
-      const int64_t unit = p.first + static_cast<int64_t>(it) * U * threads + threadIdx.x;
-      if (unit >= p.last) break;
-      Pack8<T> x[U];
-      load_units(x, p, unit, threads);
-#pragma unroll
-      for (int q = 0; q < U; ++q) {
-        if (unit + q * threads >= p.last) continue;
-        float v[8];
-        x[q].get(v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t order = order_of(v[e]);
-          if (order >= bound) f(order, p.head + 8 * (unit + q * threads) + e);
-        }
+// Leaves the keys of the part's elements whose order is at least `bound` in
+// sh.keys and their number in sh.count: above kCandidates if there are more
+// than that, or too many chunks to look through. A warp reads a chunk again
+// with an element per lane, several chunks at a time.
+template <int T>
+__device__ __forceinline__ void collect(const RowPart<T>& p, const float* slots, int per_slot, uint32_t bound,
+                                        uint32_t thread_max, TopShared& sh) {
+  constexpr int U = kUnits<T>, kBatch = 4;
+  const int threads = blockDim.x, lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = threads / 32;
+  __syncthreads();
+  if (threadIdx.x == 0) sh.count = sh.visit_count = 0;
+  __syncthreads();
+  if (thread_max >= bound) {
+    const int64_t step = static_cast<int64_t>(U) * threads * per_slot;
+    const int used = static_cast<int>((p.last - p.first + step - 1) / step);
+    for (int slot = 0; slot < used; ++slot)
+      if (order_of(slots[slot * threads + threadIdx.x]) >= bound) {
+        const int at = atomicAdd(&sh.visit_count, 1);
+        if (at < kVisits) sh.visits[at] = slot * kLpThreads + threadIdx.x;
       }
+    if (threadIdx.x < p.extra) {
+      const int64_t j = p.extra_index(threadIdx.x);
+      const uint32_t order = order_of(Elem<T>::get(p.row[j]));
+      if (order >= bound) sh.keys[atomicAdd(&sh.count, 1)] = top_key(order, j);  // fewer than 16
     }
   }
-  if (threadIdx.x < p.extra) {
-    const int64_t j = p.extra_index(threadIdx.x);
-    const uint32_t order = order_of(Elem<T>::get(p.row[j]));
-    if (order >= bound) f(order, j);
+  __syncthreads();
+  const int n = sh.visit_count;
+  if (n > kVisits) {
+    __syncthreads();
+    if (threadIdx.x == 0) sh.count = kCandidates + 1;
+    __syncthreads();
+    return;
   }
+  const int q = lane / 8, e = lane % 8;
+  for (int v0 = warp; v0 < n; v0 += kBatch * warps) {
+    for (int in = 0; in < per_slot; ++in) {
+      uint32_t order[kBatch];
+      int64_t index[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int v = v0 + b * warps;
+        const uint32_t visit = sh.visits[min(v, n - 1)];
+        const int64_t it = static_cast<int64_t>(visit / kLpThreads) * per_slot + in;
+        const int64_t unit = p.first + (it * U + q) * threads + visit % kLpThreads;
+        order[b] = 0;
+        index[b] = p.head + 8 * unit + e;
+        if (v < n && q < U && unit < p.last) order[b] = order_of(Elem<T>::get(p.body[8 * unit + e]));
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+        if (order[b] >= bound && order[b] != 0) {
+          const int at = atomicAdd(&sh.count, 1);
+          if (at < kCandidates) sh.keys[at] = top_key(order[b], index[b]);
+        }
+    }
+  }
+  __syncthreads();
 }
 
 // Leaves the keys of the part's k largest elements (and perhaps more) in
 // sh.keys and returns their number, to every thread.
 template <int T>
-__device__ int find_top(const RowPart<T>& p, int k, const uint32_t* slots, int per_slot, uint32_t thread_max,
+__device__ int find_top(const RowPart<T>& p, int k, const float* slots, int per_slot, uint32_t thread_max,
                         TopShared& sh) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
   sh.lane_max[warp][lane] = thread_max;
-  if (threadIdx.x == 0) sh.count = 0;
   __syncthreads();
   // the k-th largest of the 32 lane positions' maxima
   uint32_t mine = 0;
@@ -115,24 +142,16 @@ __device__ int find_top(const RowPart<T>& p, int k, const uint32_t* slots, int p
     rank += other > mine || (other == mine && l < lane);
   }
   const uint32_t bound = __shfl_sync(kAll, mine, __ffs(__ballot_sync(kAll, rank == k - 1)) - 1);
-  visit_chunks<T>(p, slots, per_slot, bound, [&](uint32_t order, int64_t j) {
-    const int at = atomicAdd(&sh.count, 1);
-    if (at < kCandidates) sh.keys[at] = top_key(order, j);
-  });
-  __syncthreads();
+  collect<T>(p, slots, per_slot, bound, thread_max, sh);
   int n = sh.count;
   if (n <= kCandidates) return n;
   // Many elements equal to the bound (masked rows, equal logits): those above
   // it, then the first of the equal ones in index order.
-  __syncthreads();
-  if (threadIdx.x == 0) sh.count = 0;
-  __syncthreads();
-  visit_chunks<T>(p, slots, per_slot, bound + 1, [&](uint32_t order, int64_t j) {
-    const int at = atomicAdd(&sh.count, 1);
-    if (at < kCandidates) sh.keys[at] = top_key(order, j);
-  });
-  __syncthreads();
-  n = sh.count;
+  if (bound != 0xFFFFFFFFu) {
+    collect<T>(p, slots, per_slot, bound + 1, thread_max, sh);
+    n = sh.count;
+  }
+  const int above = n;
   // The part's elements in index order, one per thread and round; the extra
   // elements before the units belong to it, those after them come last.
   const int64_t from = p.extra ? 0 : p.head + 8 * p.first;
@@ -156,7 +175,7 @@ __device__ int find_top(const RowPart<T>& p, int k, const uint32_t* slots, int p
       if (equal && at < kCandidates + kMaxTop) sh.keys[at] = top_key(bound, element(i));
       n = min(n + sum, kCandidates + kMaxTop);
       __syncthreads();
-      if (n >= k && sh.count + k <= n) break;
+      if (above + k <= n) break;
     }
     return n;
   }
@@ -205,7 +224,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) lp_forward_kernel(LpArgs a, int
   __shared__ RowStats part_stats[kLpCluster];                       // of the first block: every block's
   __shared__ uint64_t part_keys[Top ? kLpCluster * kMaxTop : 1];    // likewise
   __shared__ TopShared top;
-  extern __shared__ uint32_t slots[];
+  extern __shared__ float slots[];
   const float c = __fmul_rn(a.scale, kLog2E), slack = __fdiv_rn(kSlack, c);
   const int threads = blockDim.x;
   const int64_t teams = gridDim.x / parts;
@@ -213,16 +232,17 @@ __global__ void __launch_bounds__(kLpThreads, 4) lp_forward_kernel(LpArgs a, int
     const E* x = static_cast<const E*>(a.logits) + r * a.stride;
     const RowPart<T> p(x, a.vocab, part, parts);
     RowStats st;
-    int it = 0;
-    uint32_t slot_max = 0;
-    if (Top)
-      for (int q = 0; q < kSlots; ++q) slots[q * threads + threadIdx.x] = 0;
+    float* slot = slots + threadIdx.x;
+    float slot_max = -kInf;
+    int left = per_slot;
     scan_row<T, Entropy>(st, p, c, slack, [&](float m) {
-      if (Top) {
-        const uint32_t order = order_of(m);
-        slot_max = it % per_slot ? max(slot_max, order) : order;
-        slots[it / per_slot * threads + threadIdx.x] = slot_max;
-        ++it;
+      if (!Top) return;
+      slot_max = max_nan(slot_max, m);
+      *slot = slot_max;
+      if (--left == 0) {
+        slot += threads;
+        slot_max = -kInf;
+        left = per_slot;
       }
     });
     const bool some = p.first + threadIdx.x < p.last || threadIdx.x < p.extra;
@@ -373,7 +393,7 @@ cudaError_t launch_forward(const LpArgs& a, const DeviceInfo& dev, cudaStream_t 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(a.rows, 1 << 24) * p.parts));
   cfg.blockDim = dim3(p.threads);
-  cfg.dynamicSmemBytes = Top ? kSlots * p.threads * sizeof(uint32_t) : 0;
+  cfg.dynamicSmemBytes = Top ? kSlots * p.threads * sizeof(float) : 0;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;

@@ -37,8 +37,10 @@ struct RowStats {
   }
 };
 
-// Moves the reference to the maximum `top`.
-__device__ __forceinline__ void move_reference(RowStats& a, float top, float c, float slack) {
+// Takes note of a maximum, and moves the reference to it if it has to.
+__device__ __forceinline__ void note_maximum(RowStats& a, float top, float c, float slack) {
+  a.m = max_nan(a.m, top);
+  if (top <= a.lim) return;
   const float R = __fmul_rn(top, c);
   if (a.R == -kInf) {
     a.s = a.u = 0.0f;
@@ -51,14 +53,13 @@ __device__ __forceinline__ void move_reference(RowStats& a, float top, float c, 
   a.lim = __fadd_rn(top, slack);
 }
 
-// Adds U units, whose maximum is `top`.
+// Adds `n` of U units from the q0-th on; the reference has been moved.
 template <int T, int U, bool Entropy>
-__device__ __forceinline__ void add_units(RowStats& a, const Pack8<T> (&x)[U], float top, float c, float slack) {
-  a.m = max_nan(a.m, top);
-  if (!(top <= a.lim)) move_reference(a, top, c, slack);
+__device__ __forceinline__ void add_units(RowStats& a, const Pack8<T> (&x)[U], int q0, int n, float c) {
   const float R = a.R;
 #pragma unroll
   for (int q = 0; q < U; ++q) {
+    if (q < q0 || q >= q0 + n) continue;
     float f[8];
     x[q].get(f);
 #pragma unroll
@@ -182,33 +183,42 @@ __device__ __forceinline__ void zero_row(const RowPart<T>& out, typename Elem<T>
 }
 
 // The whole part, by all threads of the block. chunk(top) is called with each
-// chunk's maximum, in the order of the chunks (chunk i of thread t: units
-// first + (i U + q) threads + t, q < U).
+// chunk's maximum, in the order of the chunks: chunk i of thread t is the
+// units first + (i U + q) threads + t, q < U.
 template <int T, bool Entropy, typename Chunk>
 __device__ __forceinline__ void scan_row(RowStats& a, const RowPart<T>& p, float c, float slack, Chunk&& chunk) {
   constexpr int U = kUnits<T>;
   const int threads = blockDim.x;
+  const int64_t step = static_cast<int64_t>(U) * threads;
   a.clear();
   Pack8<T> x[U];
   int64_t i = p.first;
   if (i < p.last) load_units(x, p, i + threadIdx.x, threads);
-  while (i < p.last) {
-    Pack8<T> next[U];
-    const int64_t after = i + static_cast<int64_t>(U) * threads;
-    if (after < p.last) load_units(next, p, after + threadIdx.x, threads);
-    const float top = max_of<T, U>(x);
-    chunk(top);
-    add_units<T, U, Entropy>(a, x, top, c, slack);
-#pragma unroll
-    for (int q = 0; q < U; ++q) x[q] = next[q];
-    i = after;
-  }
   if (threadIdx.x < p.extra) {
     Pack8<T> one[1];
     float f[8] = {-kInf, -kInf, -kInf, -kInf, -kInf, -kInf, -kInf, -kInf};
     f[0] = Elem<T>::get(p.row[p.extra_index(threadIdx.x)]);
     one[0].put(f);
-    add_units<T, 1, Entropy>(a, one, f[0], c, slack);
+    note_maximum(a, f[0], c, slack);
+    add_units<T, 1, Entropy>(a, one, 0, 1, c);
+  }
+  for (; i + step < p.last; i += step) {
+    Pack8<T> next[U];
+    load_units(next, p, i + step + threadIdx.x, threads);
+    const float top = max_of<T, U>(x);
+    chunk(top);
+    note_maximum(a, top, c, slack);
+    add_units<T, U, Entropy>(a, x, 0, U, c);
+#pragma unroll
+    for (int q = 0; q < U; ++q) x[q] = next[q];
+  }
+  if (i < p.last) {  // the last chunk, only as many units as the block still has
+    const float top = max_of<T, U>(x);
+    chunk(top);
+    note_maximum(a, top, c, slack);
+#pragma unroll
+    for (int q = 0; q < U; ++q)
+      if (i + q * threads < p.last) add_units<T, U, Entropy>(a, x, q, 1, c);
   }
 }
 
