@@ -115,17 +115,7 @@ __global__ void __launch_bounds__(kDsThreads, 4) distill_kernel(DsArgs a, int sl
     if (parts > 1) {
       if (threadIdx.x == 0) mine = st;
       cluster.sync();
-      float R = -kInf;
-      for (int q = 0; q < parts; ++q) R = max_nan(R, cluster.map_shared_rank(&mine, q)->R);
-      st.clear();
-      for (int q = 0; q < parts; ++q) {
-        RowStats b = *cluster.map_shared_rank(&mine, q);
-        rebase(b, R);
-        st.m = max_nan(st.m, b.m);
-        st.s = __fadd_rn(st.s, b.s);
-      }
-      st.R = R;
-      st.u = 0.0f;
+      st = join_all(parts, [&](int q) { return cluster.map_shared_rank(&mine, q); });
       cluster.sync();  // before `mine`, or a logit another block still reads, is overwritten
     }
     const bool plain = out_of_range(st);

@@ -20,12 +20,12 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kLpThreads = 256;  // at most
+constexpr int kLpThreads = 128;  // at most; see row_plan
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kMaxTop = 32;
 constexpr int kSlots = 16;        // chunk maxima a thread keeps
 constexpr int kCandidates = 512;  // elements a block ranks without the slow form
-constexpr int kVisits = 256;      // chunks it reads again without it
+constexpr int kVisits = 64;       // chunks a warp reads again without it
 constexpr int kLpCluster = 8;     // blocks a row is split over at most
 
 struct LpArgs {
@@ -60,79 +60,14 @@ struct TopShared {
   uint64_t keys[kCandidates + kMaxTop];
   uint64_t warp_key[kLpWarps];
   int warp_count[kLpWarps];
-  uint32_t visits[kVisits];  // slot * 256 + thread
-  int count, visit_count;
+  uint16_t visits[kLpWarps][kVisits];  // slot * 128 + thread
+  int count;
 };
 
-// Leaves the keys of the part's elements whose order is at least `bound` in
-// sh.keys and their number in sh.count: above kCandidates if there are more
-// than that, or too many chunks to look through. A warp reads a chunk again
-// with an element per lane, several chunks at a time.
-template <int T>
-__device__ __forceinline__ void collect(const RowPart<T>& p, const float* slots, int per_slot, uint32_t bound,
-                                        uint32_t thread_max, TopShared& sh) {
-  constexpr int U = kUnits<T>, kBatch = 4;
-  const int threads = blockDim.x, lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = threads / 32;
-  __syncthreads();
-  if (threadIdx.x == 0) sh.count = sh.visit_count = 0;
-  __syncthreads();
-  if (thread_max >= bound) {
-    const int64_t step = static_cast<int64_t>(U) * threads * per_slot;
-    const int used = static_cast<int>((p.last - p.first + step - 1) / step);
-    for (int slot = 0; slot < used; ++slot)
-      if (order_of(slots[slot * threads + threadIdx.x]) >= bound) {
-        const int at = atomicAdd(&sh.visit_count, 1);
-        if (at < kVisits) sh.visits[at] = slot * kLpThreads + threadIdx.x;
-      }
-    if (threadIdx.x < p.extra) {
-      const int64_t j = p.extra_index(threadIdx.x);
-      const uint32_t order = order_of(Elem<T>::get(p.row[j]));
-      if (order >= bound) sh.keys[atomicAdd(&sh.count, 1)] = top_key(order, j);  // fewer than 16
-    }
-  }
-  __syncthreads();
-  const int n = sh.visit_count;
-  if (n > kVisits) {
-    __syncthreads();
-    if (threadIdx.x == 0) sh.count = kCandidates + 1;
-    __syncthreads();
-    return;
-  }
-  const int q = lane / 8, e = lane % 8;
-  for (int v0 = warp; v0 < n; v0 += kBatch * warps) {
-    for (int in = 0; in < per_slot; ++in) {
-      uint32_t order[kBatch];
-      int64_t index[kBatch];
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int v = v0 + b * warps;
-        const uint32_t visit = sh.visits[min(v, n - 1)];
-        const int64_t it = static_cast<int64_t>(visit / kLpThreads) * per_slot + in;
-        const int64_t unit = p.first + (it * U + q) * threads + visit % kLpThreads;
-        order[b] = 0;
-        index[b] = p.head + 8 * unit + e;
-        if (v < n && q < U && unit < p.last) order[b] = order_of(Elem<T>::get(p.body[8 * unit + e]));
-      }
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b)
-        if (order[b] >= bound && order[b] != 0) {
-          const int at = atomicAdd(&sh.count, 1);
-          if (at < kCandidates) sh.keys[at] = top_key(order[b], index[b]);
-        }
-    }
-  }
-  __syncthreads();
-}
-
-// Leaves the keys of the part's k largest elements (and perhaps more) in
-// sh.keys and returns their number, to every thread.
-template <int T>
-__device__ int find_top(const RowPart<T>& p, int k, const float* slots, int per_slot, uint32_t thread_max,
-                        TopShared& sh) {
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
-  sh.lane_max[warp][lane] = thread_max;
-  __syncthreads();
-  // the k-th largest of the 32 lane positions' maxima
+// The k-th largest of the 32 lane positions' maxima, to every thread: at least
+// k elements reach it.
+__device__ __forceinline__ uint32_t lower_bound(const TopShared& sh, int k) {
+  const int lane = threadIdx.x % 32, warps = blockDim.x / 32;
   uint32_t mine = 0;
   for (int w = 0; w < warps; ++w) mine = max(mine, sh.lane_max[w][lane]);
   int rank = 0;
@@ -141,14 +76,81 @@ __device__ int find_top(const RowPart<T>& p, int k, const float* slots, int per_
     const uint32_t other = __shfl_sync(kAll, mine, l);
     rank += other > mine || (other == mine && l < lane);
   }
-  const uint32_t bound = __shfl_sync(kAll, mine, __ffs(__ballot_sync(kAll, rank == k - 1)) - 1);
-  collect<T>(p, slots, per_slot, bound, thread_max, sh);
-  int n = sh.count;
-  if (n <= kCandidates) return n;
-  // Many elements equal to the bound (masked rows, equal logits): those above
-  // it, then the first of the equal ones in index order.
+  return __shfl_sync(kAll, mine, __ffs(__ballot_sync(kAll, rank == k - 1)) - 1);
+}
+
+// Appends the keys of elements whose order is at least `bound` to sh.keys
+// (sh.count of them): one warp, for the chunks that threads t0 .. t0 + nt - 1
+// read. A count above kCandidates says that there are more, or too many chunks
+// to look through. A lane reads a unit of a chunk again, so a warp has eight
+// chunks (16 for fp32) in flight with one load.
+template <int T>
+__device__ __forceinline__ void collect(const RowPart<T>& p, const float* slots, int per_slot, uint32_t bound, int t0,
+                                        int nt, int threads, uint16_t* visits, TopShared& sh) {
+  constexpr int U = kUnits<T>, kAtOnce = 32 / U;
+  const int lane = threadIdx.x % 32;
+  const int64_t step = static_cast<int64_t>(U) * threads * per_slot;
+  const int used = static_cast<int>((p.last - p.first + step - 1) / step);
+  const float least = bound ? value_of_order(bound) : -kInf;  // NaN: only NaN reaches it
+  int n = 0;
+  for (int slot = 0; slot < used; ++slot)
+    for (int t = t0 + lane; t < t0 + nt; t += 32) {
+      const float m = slots[slot * threads + t];
+      const bool pass = m >= least || m != m;
+      const uint32_t votes = __ballot_sync(kAll, pass);
+      const int at = n + __popc(votes & ((1u << lane) - 1));
+      if (pass && at < kVisits) visits[at] = static_cast<uint16_t>(slot * kLpThreads + t);
+      n += __popc(votes);
+    }
+  __syncwarp();
+  if (n > kVisits) {
+    if (lane == 0) atomicAdd(&sh.count, kCandidates + 1);
+    return;
+  }
+  auto append = [&](uint32_t order, int64_t j) {
+    const int at = atomicAdd(&sh.count, 1);
+    if (at < kCandidates) sh.keys[at] = top_key(order, j);
+  };
+  if (t0 == 0 && lane < p.extra) {
+    const int64_t j = p.extra_index(lane);
+    const uint32_t order = order_of(Elem<T>::get(p.row[j]));
+    if (order >= bound) append(order, j);
+  }
+  for (int v0 = 0; v0 < n; v0 += kAtOnce)
+    for (int in = 0; in < per_slot; ++in) {
+      const int v = v0 + lane / U, visit = visits[min(v, n - 1)];
+      const int64_t it = static_cast<int64_t>(visit / kLpThreads) * per_slot + in;
+      const int64_t unit = p.first + (it * U + lane % U) * threads + visit % kLpThreads;
+      Pack8<T> x[1];
+      if (v >= n || unit >= p.last) continue;
+      x[0].load(p.body + 8 * unit);
+      const float top = max_of<T, 1>(x);
+      if (!(top >= least || top != top)) continue;
+      float f[8];
+      x[0].get(f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t order = order_of(f[e]);
+        if (order >= bound) append(order, p.head + 8 * unit + e);
+      }
+    }
+}
+
+// Where too many elements reach the bound (masked rows, equal logits): leaves
+// the keys of the part's k largest elements (and perhaps more) in sh.keys and
+// returns their number, to every thread.
+template <int T>
+__device__ __noinline__ int find_among_many(const RowPart<T>& p, int k, const float* slots, int per_slot,
+                                            uint32_t bound, TopShared& sh) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
+  // those above the bound, then the first of the equal ones in index order
+  int n = kCandidates + 1;
   if (bound != 0xFFFFFFFFu) {
-    collect<T>(p, slots, per_slot, bound + 1, thread_max, sh);
+    __syncthreads();
+    if (threadIdx.x == 0) sh.count = 0;
+    __syncthreads();
+    collect<T>(p, slots, per_slot, bound + 1, 32 * warp, 32, blockDim.x, sh.visits[warp], sh);
+    __syncthreads();
     n = sh.count;
   }
   const int above = n;
@@ -202,6 +204,21 @@ __device__ int find_top(const RowPart<T>& p, int k, const float* slots, int per_
   return k;
 }
 
+// The keys of the part's k largest elements (and perhaps more), in sh.keys;
+// their number, to every thread. sh.lane_max is filled and sh.count 0. Out of
+// line, so that the pass over the row keeps its registers.
+template <int T>
+__device__ __noinline__ int find_top(const typename Elem<T>::type* row, int64_t vocab, int part, int parts, int k,
+                                     const float* slots, int per_slot, TopShared& sh) {
+  const RowPart<T> p(row, vocab, part, parts);
+  const uint32_t bound = lower_bound(sh, k);
+  const int warp = threadIdx.x / 32;
+  collect<T>(p, slots, per_slot, bound, 32 * warp, 32, blockDim.x, sh.visits[warp], sh);
+  __syncthreads();
+  const int n = sh.count;
+  return n <= kCandidates ? n : find_among_many<T>(p, k, slots, per_slot, bound, sh);
+}
+
 // Calls f(rank, key) for the k largest of n keys (all different, or 0).
 template <typename F>
 __device__ __forceinline__ void rank_keys(const uint64_t* keys, int n, int k, F&& f) {
@@ -215,7 +232,7 @@ __device__ __forceinline__ void rank_keys(const uint64_t* keys, int n, int k, F&
 }
 
 template <int T, bool Entropy, bool Top>
-__global__ void __launch_bounds__(kLpThreads, 4) lp_forward_kernel(LpArgs a, int per_slot) {
+__global__ void __launch_bounds__(kLpThreads, 8) lp_forward_kernel(LpArgs a, int per_slot) {
   pdl_enter();
   using E = typename Elem<T>::type;
   const cg::cluster_group cluster = cg::this_cluster();
@@ -232,6 +249,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) lp_forward_kernel(LpArgs a, int
     const E* x = static_cast<const E*>(a.logits) + r * a.stride;
     const RowPart<T> p(x, a.vocab, part, parts);
     RowStats st;
+    if (Top && threadIdx.x == 0) top.count = 0;
     float* slot = slots + threadIdx.x;
     float slot_max = -kInf;
     int left = per_slot;
@@ -247,9 +265,16 @@ __global__ void __launch_bounds__(kLpThreads, 4) lp_forward_kernel(LpArgs a, int
     });
     const bool some = p.first + threadIdx.x < p.last || threadIdx.x < p.extra;
     const uint32_t thread_max = some ? order_of(st.m) : 0;
-    st = join_block(st, red);
+    const int warp = threadIdx.x / 32;
+    st = join_warp(st);
+    if (threadIdx.x % 32 == 0) red[warp] = st;
+    if (Top) top.lane_max[warp][threadIdx.x % 32] = thread_max;
+    __syncthreads();
+    st = join_all(threads / 32, [&](int i) { return red + i; });
     int n = 0;
-    if (Top) n = find_top<T>(p, a.top_k, slots, per_slot, thread_max, top);
+    if (Top) {
+      n = find_top<T>(x, a.vocab, part, parts, a.top_k, slots, per_slot, top);
+    }
     const uint64_t* keys = top.keys;
     if (parts > 1) {
       if (threadIdx.x == 0) *cluster.map_shared_rank(&part_stats[part], 0) = st;
@@ -260,18 +285,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) lp_forward_kernel(LpArgs a, int
       }
       cluster.sync();
       if (part == 0) {
-        float R = part_stats[0].R;
-        for (int q = 1; q < parts; ++q) R = max_nan(R, part_stats[q].R);
-        st = part_stats[0];
-        rebase(st, R);
-        for (int q = 1; q < parts; ++q) {
-          RowStats b = part_stats[q];
-          rebase(b, R);
-          st.m = max_nan(st.m, b.m);
-          st.s = __fadd_rn(st.s, b.s);
-          st.u = __fadd_rn(st.u, b.u);
-        }
-        st.R = R;
+        st = join_all(parts, [&](int q) { return part_stats + q; });
         keys = part_keys;
         n = parts * kMaxTop;
       }
@@ -302,10 +316,8 @@ __global__ void __launch_bounds__(kLpThreads, 4) lp_forward_kernel(LpArgs a, int
         });
     }
     if (r + teams < a.rows) {  // before the next row's sums go where this row's were read
-      if (parts > 1)
-        cluster.sync();
-      else
-        __syncthreads();
+      if (parts > 1) cluster.sync();
+      __syncthreads();
     }
   }
 }
@@ -360,8 +372,12 @@ __global__ void __launch_bounds__(kLpThreads) lp_backward_kernel(LpArgs a, int p
 }
 
 // Threads of a block and blocks of a row. A thread should have at least one
-// chunk; rows are split over a cluster while that leaves the grid short of
-// two blocks an SM and each block with a chunk a thread.
+// chunk. Blocks of 128 threads, eight an SM, hide the end of a row (joining
+// and ranking, all latency) behind other rows better than fewer larger ones,
+// and pay it less often than more smaller ones: 8192 x 50304 bf16 with entropy
+// and 20 alternatives took 222 us with 128 threads, 252 with 256, 339 with 64.
+// Rows are split over a cluster while that leaves the grid short of four
+// blocks an SM and each block with half a chunk a thread.
 struct RowPlan {
   int threads, parts;
 };
@@ -371,7 +387,7 @@ RowPlan row_plan(int64_t rows, int64_t vocab, int type, const DeviceInfo& dev) {
   RowPlan p;
   p.threads = static_cast<int>(std::min<int64_t>(kLpThreads, std::max<int64_t>(1, (vocab / chunk + 31) / 32) * 32));
   p.parts = 1;
-  while (p.parts < kLpCluster && rows * p.parts * 2 <= 2 * dev.sms && vocab / (2 * p.parts) >= chunk * p.threads / 2)
+  while (p.parts < kLpCluster && rows * p.parts * 2 <= 4 * dev.sms && vocab / (2 * p.parts) >= chunk * p.threads / 2)
     p.parts *= 2;
   return p;
 }

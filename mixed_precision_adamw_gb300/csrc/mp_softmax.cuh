@@ -222,31 +222,42 @@ __device__ __forceinline__ void scan_row(RowStats& a, const RowPart<T>& p, float
   }
 }
 
-// The block's statistics, to every thread. `red` has one entry per warp.
-__device__ __forceinline__ RowStats join_block(RowStats a, RowStats* red) {
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
+// Sum of a warp's statistics, to each lane.
+__device__ __forceinline__ RowStats join_warp(RowStats a) {
   const float R = warp_max(a.R);
   rebase(a, R);
   a.R = R;
   a.m = warp_max(a.m);
   a.s = warp_sum(a.s);
   a.u = warp_sum(a.u);
-  __syncthreads();
-  if (lane == 0) red[warp] = a;
-  __syncthreads();
-  a = red[0];
-  float top = a.R;
-  for (int w = 1; w < warps; ++w) top = max_nan(top, red[w].R);
-  rebase(a, top);
-  a.R = top;
-  for (int w = 1; w < warps; ++w) {
-    RowStats b = red[w];
-    rebase(b, top);
+  return a;
+}
+
+// Sum of `n` joined statistics at at(i).
+template <typename At>
+__device__ __forceinline__ RowStats join_all(int n, At&& at) {
+  float R = at(0)->R;
+  for (int i = 1; i < n; ++i) R = max_nan(R, at(i)->R);
+  RowStats a = *at(0);
+  rebase(a, R);
+  a.R = R;
+  for (int i = 1; i < n; ++i) {
+    RowStats b = *at(i);
+    rebase(b, R);
     a.m = max_nan(a.m, b.m);
     a.s = __fadd_rn(a.s, b.s);
     a.u = __fadd_rn(a.u, b.u);
   }
   return a;
+}
+
+// The block's statistics, to every thread. `red` has one entry per warp.
+__device__ __forceinline__ RowStats join_block(RowStats a, RowStats* red) {
+  a = join_warp(a);
+  __syncthreads();
+  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = a;
+  __syncthreads();
+  return join_all(blockDim.x / 32, [&](int i) { return red + i; });
 }
 
 // Whether the row's finite maximum left the range of c x: its statistics have
