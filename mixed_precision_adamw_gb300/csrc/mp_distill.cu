@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kDsThreads, 4) distill_kernel(DsArgs a, int sl
     }
     const bool plain = out_of_range(st);
     if (plain) {
-      st = plain_stats<T, false>(x, a.vocab, st.m, c, red);
+      st = plain_stats<T, false, BlockTeam>(x, a.vocab, st.m, c, red);
       if (parts > 1) cluster.sync();
     }
     const RowLog log(st, plain, c, a.scale);

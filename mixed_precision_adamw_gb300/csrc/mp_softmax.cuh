@@ -182,29 +182,35 @@ __device__ __forceinline__ void zero_row(const RowPart<T>& out, typename Elem<T>
   if (threadIdx.x < out.extra) dx[out.extra_index(threadIdx.x)] = Elem<T>::put(0.0f);
 }
 
-// The whole part, by all threads of the block. chunk(top) is called with each
-// chunk's maximum, in the order of the chunks: chunk i of thread t is the
-// units first + (i U + q) threads + t, q < U.
-template <int T, bool Entropy, typename Chunk>
-__device__ __forceinline__ void scan_row(RowStats& a, const RowPart<T>& p, float c, float slack, Chunk&& chunk) {
+// A part's first chunk, to be loaded before scan_row.
+template <int T>
+__device__ __forceinline__ void first_chunk(Pack8<T> (&x)[kUnits<T>], const RowPart<T>& p, int t, int threads) {
+  load_units(x, p, p.first + t, threads);
+}
+
+// The whole part, by `threads` threads, of which this is the t-th; x holds its
+// first chunk. chunk(top) is called with each chunk's maximum, in the order of the
+// chunks: chunk i of the thread is the units first + (i U + q) threads + t,
+// q < U. ahead(x) is called once, before the last chunk is added, to load what
+// comes after the part.
+template <int T, bool Entropy, typename Chunk, typename Ahead>
+__device__ __forceinline__ void scan_row(RowStats& a, Pack8<T> (&x)[kUnits<T>], const RowPart<T>& p, int t, int threads,
+                                         float c, float slack, Chunk&& chunk, Ahead&& ahead) {
   constexpr int U = kUnits<T>;
-  const int threads = blockDim.x;
   const int64_t step = static_cast<int64_t>(U) * threads;
   a.clear();
-  Pack8<T> x[U];
-  int64_t i = p.first;
-  if (i < p.last) load_units(x, p, i + threadIdx.x, threads);
-  if (threadIdx.x < p.extra) {
+  if (t < p.extra) {
     Pack8<T> one[1];
     float f[8] = {-kInf, -kInf, -kInf, -kInf, -kInf, -kInf, -kInf, -kInf};
-    f[0] = Elem<T>::get(p.row[p.extra_index(threadIdx.x)]);
+    f[0] = Elem<T>::get(p.row[p.extra_index(t)]);
     one[0].put(f);
     note_maximum(a, f[0], c, slack);
     add_units<T, 1, Entropy>(a, one, 0, 1, c);
   }
+  Pack8<T> next[U];
+  int64_t i = p.first;
   for (; i + step < p.last; i += step) {
-    Pack8<T> next[U];
-    load_units(next, p, i + step + threadIdx.x, threads);
+    load_units(next, p, i + step + t, threads);
     const float top = max_of<T, U>(x);
     chunk(top);
     note_maximum(a, top, c, slack);
@@ -212,6 +218,7 @@ __device__ __forceinline__ void scan_row(RowStats& a, const RowPart<T>& p, float
 #pragma unroll
     for (int q = 0; q < U; ++q) x[q] = next[q];
   }
+  ahead(next);
   if (i < p.last) {  // the last chunk, only as many units as the block still has
     const float top = max_of<T, U>(x);
     chunk(top);
@@ -220,6 +227,15 @@ __device__ __forceinline__ void scan_row(RowStats& a, const RowPart<T>& p, float
     for (int q = 0; q < U; ++q)
       if (i + q * threads < p.last) add_units<T, U, Entropy>(a, x, q, 1, c);
   }
+#pragma unroll
+  for (int q = 0; q < U; ++q) x[q] = next[q];
+}
+
+template <int T, bool Entropy, typename Chunk>
+__device__ __forceinline__ void scan_row(RowStats& a, const RowPart<T>& p, float c, float slack, Chunk&& chunk) {
+  Pack8<T> x[kUnits<T>];
+  first_chunk(x, p, threadIdx.x, blockDim.x);
+  scan_row<T, Entropy>(a, x, p, threadIdx.x, blockDim.x, c, slack, chunk, [](auto&) {});
 }
 
 // Sum of a warp's statistics, to each lane.
@@ -266,9 +282,24 @@ __device__ __forceinline__ bool out_of_range(const RowStats& a) {
   return isfinite(a.m) && !(fabsf(a.R) <= 1e38f);
 }
 
-// The slow form for such rows, by all threads of a block over the whole row:
-// t = (x - m) c. On return R is 0 and t = (x - m) c replaces c x - R.
-template <int T, bool Entropy>
+// The threads that finish a row: a whole block, or one warp of it.
+struct BlockTeam {
+  __device__ __forceinline__ static int thread() { return threadIdx.x; }
+  __device__ __forceinline__ static int threads() { return blockDim.x; }
+  __device__ __forceinline__ static void sync() { __syncthreads(); }
+  __device__ __forceinline__ static RowStats join(const RowStats& a, RowStats* red) { return join_block(a, red); }
+};
+
+struct WarpTeam {
+  __device__ __forceinline__ static int thread() { return threadIdx.x % 32; }
+  __device__ __forceinline__ static int threads() { return 32; }
+  __device__ __forceinline__ static void sync() { __syncwarp(); }
+  __device__ __forceinline__ static RowStats join(const RowStats& a, RowStats*) { return join_warp(a); }
+};
+
+// The slow form for such rows, by a team over the whole row: t = (x - m) c.
+// On return R is 0 and t = (x - m) c replaces c x - R.
+template <int T, bool Entropy, typename Team>
 __device__ __noinline__ RowStats plain_stats(const typename Elem<T>::type* row, int64_t n, float m, float c,
                                              RowStats* red) {
   RowStats a;
@@ -276,13 +307,13 @@ __device__ __noinline__ RowStats plain_stats(const typename Elem<T>::type* row, 
   a.lim = 0.0f;
   a.s = a.u = 0.0f;
   a.m = m;
-  for (int64_t j = threadIdx.x; j < n; j += blockDim.x) {
+  for (int64_t j = Team::thread(); j < n; j += Team::threads()) {
     const float t = max_nan(__fmul_rn(__fsub_rn(Elem<T>::get(row[j]), m), c), kLowest);
     const float p = exp2_fast(t);
     a.s = __fadd_rn(a.s, p);
     if (Entropy) a.u = __fmaf_rn(p, t, a.u);
   }
-  return join_block(a, red);
+  return Team::join(a, red);
 }
 
 // The logarithms of a row's joined statistics.
