@@ -111,19 +111,14 @@ __global__ void __launch_bounds__(kDsThreads, 4) distill_kernel(DsArgs a, int sl
     }
     RowStats st;
     scan_row<T, false>(st, RowPart<T>(x, a.vocab, part, parts), c, slack, [](float) {});
-    st = join_block(st, red);
+    st = join_block(st, red, c);
     if (parts > 1) {
       if (threadIdx.x == 0) mine = st;
       cluster.sync();
-      st = join_all(parts, [&](int q) { return cluster.map_shared_rank(&mine, q); });
+      st = join_all(parts, c, [&](int q) { return cluster.map_shared_rank(&mine, q); });
       cluster.sync();  // before `mine`, or a logit another block still reads, is overwritten
     }
-    const bool plain = out_of_range(st);
-    if (plain) {
-      st = plain_stats<T, false, BlockTeam>(x, a.vocab, st.m, c, red);
-      if (parts > 1) cluster.sync();
-    }
-    const RowLog log(st, plain, c, a.scale);
+    const RowLog log(st, c, a.scale);
     // the teacher's distribution and the loss
     tm = block_reduce(tm, redf, true);
     const bool none = tm == -kInf;
@@ -162,10 +157,7 @@ __global__ void __launch_bounds__(kDsThreads, 4) distill_kernel(DsArgs a, int sl
       continue;
     }
     const float ws = __fmul_rn(w, a.scale), A = __fdiv_rn(ws, st.s);
-    if (plain)
-      map_row<T>(out, dx, x, [&](float v) { return __fmul_rn(exp2_fast(__fmul_rn(__fsub_rn(v, st.m), c)), A); });
-    else
-      map_row<T>(out, dx, x, [&](float v) { return __fmul_rn(exp2_fast(__fmaf_rn(v, c, -st.R)), A); });
+    map_row<T>(out, dx, x, [&](float v) { return __fmul_rn(exp2_fast(__fmul_rn(__fsub_rn(v, st.ref), c)), A); });
     __syncthreads();
     for (int i = threadIdx.x; i < a.k; i += threads) {
       const int32_t token = l.token[i];
@@ -178,7 +170,7 @@ __global__ void __launch_bounds__(kDsThreads, 4) distill_kernel(DsArgs a, int sl
         for (int j = i + 1; j < a.k; ++j)
           if (l.token[j] == token) q = __fadd_rn(q, l.q[j]);
       }
-      const float t = plain ? __fmul_rn(__fsub_rn(l.z[i], st.m), c) : __fmaf_rn(l.z[i], c, -st.R);
+      const float t = __fmul_rn(__fsub_rn(l.z[i], st.ref), c);
       dx[token] = Elem<T>::put(__fmul_rn(ws, __fsub_rn(__fdiv_rn(exp2_fast(t), st.s), q)));
     }
   }
