@@ -11,6 +11,7 @@
 #include "mp_device.cuh"
 #include "mp_internal.h"
 #include "mp_softmax.cuh"
+#include "mp_tma.cuh"
 
 namespace mpk {
 namespace {
@@ -57,7 +58,7 @@ __device__ __forceinline__ float block_reduce(float v, float* red, bool maximum)
 }
 
 // Enters token into the table; true if it was there.
-__device__ __forceinline__ bool enter(const List& l, int32_t token) {
+__device__ __forceinline__ bool enter(const List& l, int32_t token) {  // the table is at most half full
   const uint32_t mask = l.slots - 1;
   uint32_t at = (static_cast<uint32_t>(token) * 0x9E3779B1u) >> 16;
   for (int i = 0; i < l.slots; ++i, ++at) {
@@ -176,8 +177,508 @@ __global__ void __launch_bounds__(kDsThreads, 4) distill_kernel(DsArgs a, int sl
   }
 }
 
+// ---- many long rows -----------------------------------------------------------
+// One block an SM streams rows through a ring of shared-memory tiles, so that
+// HBM never waits for a row to be finished. A row's tiles are loaded by the TMA
+// engine (1D bulk copies) and read once for the sum; the last `resident` of
+// them stay, are turned into the gradient in place and stored from there by
+// bulk copies, the others are freed at once and loaded a second time, out of
+// L2. Meanwhile the loads of the following rows fill what is free.
+//
+// Warps: 0 loads tiles, 1 patches the listed tokens and stores tiles, 2 reads
+// the teacher's lists a row or two ahead, the other 16 compute. mbarriers:
+// full (tile has landed), freed (its slot may be loaded again: by each computing
+// warp, or sixteenfold by the storing thread), done (its gradient is written),
+// listed and taken (the two list buffers), joined (the row's sums). Every wait
+// gives up after a second and records MP_ERR_CUDA; nothing waits without that
+// limit, and the loads and stores in flight are waited for before a block ends.
+constexpr int kRingWarps = 16;
+constexpr int kRingThreads = 32 * kRingWarps;         // that compute
+constexpr int kRingBlock = kRingThreads + 96;
+constexpr uint32_t kTileBytes = 2 * 16 * kRingThreads;  // two vectors a thread
+constexpr int kTileVectors = kTileBytes / 16;
+constexpr uint32_t kRingSlots = 13;
+constexpr int kRingResident = 11;                     // tiles of a row kept between its passes, at most
+constexpr int kRingTeacher = 128;                     // list length, at most
+constexpr int kRingOwn = kRingTeacher / 32;           // list entries a lane holds
+
+struct RingList {
+  int32_t token[kRingTeacher];  // -1: unused; below: -2 - token of a later entry of a token listed twice
+  float q[kRingTeacher];
+  float q_sum[kRingTeacher];    // over a token's entries
+  float z[kRingTeacher];
+  float w, kl0;                 // row weight; sum q log q
+  int none, bad;
+};
+
+struct RingShared {
+  RingList list[2];
+  RowStats stats[2][kRingWarps];
+  int32_t table[2 * kRingTeacher];
+  unsigned long long full[kRingSlots], freed[kRingSlots], done[kRingSlots], listed[2], taken[2], joined;
+};
+
+constexpr size_t kRingBytes = kRingSlots * kTileBytes + sizeof(RingShared);
+static_assert(kRingBytes <= 227 * 1024, "one block's shared memory");
+
+// A row in the ring: its body's tiles and their places in the stream of loads.
+template <int T>
+struct RingRow {
+  RowPart<T> part;
+  int tiles, resident;
+  int64_t vectors;
+
+  __device__ __forceinline__ RingRow(const DsArgs& a, int64_t r)
+      : part(static_cast<const typename Elem<T>::type*>(a.logits) + r * a.stride, a.vocab, 0, 1) {
+    vectors = part.units * (T == MP_FP32 ? 2 : 1);
+    tiles = static_cast<int>((vectors + kTileVectors - 1) / kTileVectors);
+    resident = min(tiles, kRingResident);
+  }
+  __device__ __forceinline__ int loads() const { return 2 * tiles - resident; }
+  // the j-th load's tile; tiles are in pass-two order from load tiles - resident on
+  __device__ __forceinline__ int tile_of(int load) const { return load < tiles ? load : load - tiles; }
+  __device__ __forceinline__ uint32_t bytes(int tile) const {
+    return static_cast<uint32_t>(min(static_cast<int64_t>(kTileVectors), vectors - static_cast<int64_t>(tile) * kTileVectors)) * 16;
+  }
+};
+
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  return __all_sync(kAll, mbar_wait(bar, parity));
+}
+
+__device__ __forceinline__ float row_weight(const DsArgs& a, int64_t r) { return a.row_weight ? a.row_weight[r] : 1.0f; }
+
+// The slot and phase of the stream's next load or tile.
+struct RingPlace {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void next(uint32_t n = 1) {
+    slot += n;
+    while (slot >= kRingSlots) {
+      slot -= kRingSlots;
+      phase ^= 1;
+    }
+  }
+};
+
+template <int T>
+__device__ __noinline__ bool ring_load(const DsArgs& a, uint32_t tiles, const RingShared& sh) {
+  RingPlace at;
+  const uint64_t once = l2_evict_first();
+  float w = blockIdx.x < a.rows ? row_weight(a, blockIdx.x) : 0.0f;
+  int64_t loads = 0;
+  bool ok = true;
+  for (int64_t r = blockIdx.x; ok && r < a.rows; r += gridDim.x) {
+    const float w_next = r + gridDim.x < a.rows ? row_weight(a, r + gridDim.x) : 0.0f;
+    if (w != 0.0f) {
+      const RingRow<T> row(a, r);
+      for (int i = 0; i < row.loads(); ++i, ++loads, at.next()) {
+        if (loads >= kRingSlots && !mbar_wait(smem_u32(&sh.freed[at.slot]), at.phase ^ 1)) {
+          ok = false;
+          break;
+        }
+        const int tile = row.tile_of(i);
+        const uint32_t bar = smem_u32(&sh.full[at.slot]), bytes = row.bytes(tile);
+        const void* src = reinterpret_cast<const char*>(row.part.body) + static_cast<int64_t>(tile) * kTileBytes;
+        mbar_expect_tx(bar, bytes);
+        if (i < row.tiles - row.resident)  // to be loaded again
+          bulk_load(tiles + at.slot * kTileBytes, src, bytes, bar);
+        else
+          bulk_load(tiles + at.slot * kTileBytes, src, bytes, bar, once);
+      }
+    }
+    w = w_next;
+  }
+  // the last loads land before the block ends
+  if (loads < kRingSlots) at = RingPlace{0, 1};
+  for (int64_t q = min(loads, static_cast<int64_t>(kRingSlots)); q > 0; --q, at.next())
+    ok = mbar_wait(smem_u32(&sh.full[at.slot]), at.phase ^ 1) && ok;
+  return ok;
+}
+
+// The teacher's list of each row: q, the loss's share that the student has no
+// part in, the student's logits, entries of one token joined. The index, the
+// teacher's logits and the weight of the next row are on their way while a row
+// is worked on.
+template <int T>
+__device__ __noinline__ bool ring_list(const DsArgs& a, RingShared& sh) {
+  using E = typename Elem<T>::type;
+  const int lane = threadIdx.x % 32;
+  const float c = __fmul_rn(a.scale, kLog2E);
+  uint32_t slots = 2;
+  while (slots < 2u * a.k) slots *= 2;
+  int64_t index[kRingOwn];
+  typename Elem<T>::type teacher[kRingOwn];
+  float w = 0.0f;
+  auto fetch = [&](int64_t r) {
+    if (r >= a.rows) return;
+    w = row_weight(a, r);
+#pragma unroll
+    for (int u = 0; u < kRingOwn; ++u) {
+      const int i = 32 * u + lane;
+      index[u] = -1;
+      if (i < a.k) {
+        index[u] = load_index(a.index, r * a.index_stride + i, a.index_type);
+        teacher[u] = (static_cast<const E*>(a.teacher) + r * a.teacher_stride)[i];
+      }
+    }
+  };
+  fetch(blockIdx.x);
+  int round = 0;
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, ++round) {
+    const int set = round & 1;
+    RingList& l = sh.list[set];
+    const E* x = static_cast<const E*>(a.logits) + r * a.stride;
+    const float weight = w;
+    int32_t token[kRingOwn];
+    float q[kRingOwn], z[kRingOwn];
+    float tm = -kInf;
+    bool bad = false;
+#pragma unroll
+    for (int u = 0; u < kRingOwn; ++u) {
+      const bool use = index[u] >= 0 && index[u] < a.vocab;
+      bad = bad || index[u] >= a.vocab;
+      token[u] = use ? static_cast<int32_t>(index[u]) : -1;
+      q[u] = use ? Elem<T>::get(teacher[u]) : -kInf;
+      z[u] = use && weight != 0.0f ? Elem<T>::get(x[index[u]]) : 0.0f;
+      tm = max_nan(tm, q[u]);
+    }
+    fetch(r + gridDim.x);
+    if (round >= 2 && !warp_wait(smem_u32(&sh.taken[set]), (round / 2 - 1) & 1)) return false;
+    if (weight != 0.0f) {
+      tm = warp_max(tm);
+      bad = __any_sync(kAll, bad);
+      const bool none = tm == -kInf;
+      float ts = 0.0f;
+#pragma unroll
+      for (int u = 0; u < kRingOwn; ++u)
+        if (!none) ts = __fadd_rn(ts, exp2_fast(__fmul_rn(__fsub_rn(q[u], tm), c)));
+      ts = warp_sum(ts);
+      const float inv_ts = __fdiv_rn(1.0f, ts), log_ts = logf(ts);
+      float kl0 = 0.0f;
+#pragma unroll 1
+      for (int i = lane; i < static_cast<int>(slots); i += 32) sh.table[i] = -1;
+      __syncwarp();
+      uint32_t twice = 0;  // bit u: entry u's token was in the table
+#pragma unroll
+      for (int u = 0; u < kRingOwn; ++u) {
+        float p = 0.0f;
+        if (!none) {
+          const float d = __fsub_rn(q[u], tm);
+          p = __fmul_rn(exp2_fast(__fmul_rn(d, c)), inv_ts);
+          if (p != 0.0f) kl0 = __fmaf_rn(p, __fmaf_rn(d, a.scale, -log_ts), kl0);
+        }
+        q[u] = p;
+        if (token[u] >= 0) {
+          uint32_t at = (static_cast<uint32_t>(token[u]) * 0x9E3779B1u) >> 16;
+          for (uint32_t n = 0; n < slots; ++n, ++at) {
+            const int32_t was = atomicCAS(&sh.table[at & (slots - 1)], -1, token[u]);
+            if (was == token[u]) twice |= 1u << u;
+            if (was == -1 || was == token[u]) break;
+          }
+        }
+      }
+      kl0 = warp_sum(kl0);
+#pragma unroll
+      for (int u = 0; u < kRingOwn; ++u)
+        if (32 * u + lane < a.k) {
+          l.q[32 * u + lane] = l.q_sum[32 * u + lane] = q[u];
+          l.z[32 * u + lane] = z[u];
+        }
+      // tokens listed twice: the first entry carries the sum, in the list's order
+      if (__any_sync(kAll, twice)) {
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < kRingOwn; ++u)
+          for (uint32_t left = __ballot_sync(kAll, twice >> u & 1); left; left &= left - 1) {
+            const int32_t again = __shfl_sync(kAll, token[u], __ffs(left) - 1);
+            if (again < 0) continue;  // joined before
+            int owner = -1;
+            float sum = 0.0f;
+#pragma unroll
+            for (int v = 0; v < kRingOwn; ++v)
+              for (uint32_t with = __ballot_sync(kAll, token[v] == again); with; with &= with - 1) {
+                const int from = __ffs(with) - 1;
+                sum = __fadd_rn(sum, __shfl_sync(kAll, q[v], from));
+                if (owner >= 0 && lane == from) token[v] = -2 - again;
+                owner = owner < 0 ? 32 * v + from : owner;
+              }
+            if (lane == 0) l.q_sum[owner] = sum;
+          }
+      }
+#pragma unroll
+      for (int u = 0; u < kRingOwn; ++u)
+        if (32 * u + lane < a.k) l.token[32 * u + lane] = token[u];
+      if (lane == 0) {
+        l.kl0 = kl0;
+        l.none = none;
+        l.bad = bad;
+      }
+    }
+    if (lane == 0) l.w = weight;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh.listed[set]));
+  }
+  return true;
+}
+
+// Loss, listed tokens and stores.
+template <int T>
+__device__ __noinline__ bool ring_store(const DsArgs& a, uint8_t* tiles, RingShared& sh) {
+  using E = typename Elem<T>::type;
+  const int lane = threadIdx.x % 32;
+  const float c = __fmul_rn(a.scale, kLog2E);
+  RingPlace at;
+  uint32_t done_phase = 0;  // bit s: the parity of slot s's next use of `done`
+  int round = 0;
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, ++round) {
+    const int set = round & 1;
+    if (!warp_wait(smem_u32(&sh.listed[set]), (round / 2) & 1)) return false;
+    RingList& l = sh.list[set];
+    if (l.w == 0.0f) {
+      if (lane == 0) a.loss[r] = 0.0f;
+    } else {
+      const RingRow<T> row(a, r);
+      const E* x = row.part.row;
+      E* dx = static_cast<E*>(a.dlogits) + r * a.dlogits_stride;
+      at.next(row.tiles - row.resident);
+      RowStats st;
+      bool zero = true;
+      int32_t token[kRingOwn];
+      E grad[kRingOwn];
+#pragma unroll 1
+      for (int i = 0; i < row.tiles; ++i, at.next()) {
+        const int tile = row.tile_of(row.tiles - row.resident + i);
+        const uint32_t done = smem_u32(&sh.done[at.slot]);
+        if (!warp_wait(done, done_phase >> at.slot & 1)) return false;
+        done_phase ^= 1u << at.slot;
+        if (i == 0) {  // every computing warp has left its sums
+          st.clear();
+          if (lane < kRingWarps) st = sh.stats[set][lane];
+          st = join_warp(st, c);
+          zero = l.none || st.m == -kInf;
+          const float ws = __fmul_rn(l.w, a.scale);
+#pragma unroll
+          for (int u = 0; u < kRingOwn; ++u) {  // the listed tokens' gradients
+            const int j = 32 * u + lane;
+            token[u] = -1;
+            if (j >= a.k) continue;
+            const float p = __fdiv_rn(exp2_fast(__fmul_rn(__fsub_rn(l.z[j], st.ref), c)), st.s);
+            token[u] = l.token[j];
+            grad[u] = Elem<T>::put(zero ? 0.0f : __fmul_rn(ws, __fsub_rn(p, l.q_sum[j])));
+          }
+          if (row.part.extra) {  // the elements before and after the tiles
+            if (lane < row.part.extra) {
+              const int64_t j = row.part.extra_index(lane);
+              const float p = exp2_fast(__fmul_rn(__fsub_rn(Elem<T>::get(x[j]), st.ref), c));
+              dx[j] = Elem<T>::put(zero ? 0.0f : __fmul_rn(p, __fdiv_rn(ws, st.s)));
+            }
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < kRingOwn; ++u)
+              if (token[u] >= 0 && (token[u] < row.part.head || token[u] >= row.part.head + 8 * row.part.units))
+                dx[token[u]] = grad[u];
+          }
+        }
+        constexpr int kTileElems = kTileBytes / sizeof(E);
+        const int64_t first = row.part.head + static_cast<int64_t>(tile) * kTileElems;
+        const int64_t end = min(first + kTileElems, row.part.head + 8 * row.part.units);
+        E* data = reinterpret_cast<E*>(tiles + at.slot * kTileBytes);
+#pragma unroll
+        for (int u = 0; u < kRingOwn; ++u)
+          if (token[u] >= first && token[u] < end) data[token[u] - first] = grad[u];
+        fence_to_bulk();
+        __syncwarp();
+        if (lane == 0) {
+          bulk_store(dx + first, smem_u32(data), row.bytes(tile));
+          bulk_commit();
+          if (i > 0) {  // the tile before has been read
+            bulk_wait_read<1>();
+            mbar_arrive_n(smem_u32(&sh.freed[at.slot == 0 ? kRingSlots - 1 : at.slot - 1]), kRingWarps);
+          }
+        }
+      }
+      if (lane == 0) {
+        bulk_wait_read<0>();
+        mbar_arrive_n(smem_u32(&sh.freed[at.slot == 0 ? kRingSlots - 1 : at.slot - 1]), kRingWarps);
+      }
+      const RowLog log(st, c, a.scale);
+      float kl = 0.0f;
+#pragma unroll 1
+      for (int j = lane; j < a.k; j += 32)
+        if (l.q[j] != 0.0f) kl = __fmaf_rn(-l.q[j], log.log_p(l.z[j]), kl);
+      kl = __fadd_rn(warp_sum(kl), l.kl0);
+      if (lane == 0) {
+        a.loss[r] = l.bad ? __int_as_float(0x7FC00000) : l.none ? 0.0f : __fmul_rn(l.w, kl);
+        if (l.bad && a.d_status) atomicCAS(a.d_status, 0, MP_ERR_RANGE);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh.taken[set]));
+  }
+  return true;
+}
+
+template <int T>
+__global__ void __launch_bounds__(kRingBlock, 1) distill_ring_kernel(DsArgs a) {
+  pdl_enter();
+  using E = typename Elem<T>::type;
+  using V = Vec16<T>;
+  extern __shared__ __align__(128) uint8_t tiles[];
+  RingShared& sh = *reinterpret_cast<RingShared*>(tiles + kRingSlots * kTileBytes);
+  if (threadIdx.x == 0) {
+    for (uint32_t i = 0; i < kRingSlots; ++i) {
+      mbar_init(smem_u32(&sh.full[i]), 1);
+      mbar_init(smem_u32(&sh.freed[i]), kRingWarps);
+      mbar_init(smem_u32(&sh.done[i]), kRingWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sh.listed[i]), 1);
+      mbar_init(smem_u32(&sh.taken[i]), 1 + kRingWarps);
+    }
+    mbar_init(smem_u32(&sh.joined), kRingWarps);
+    mbar_init_fence();
+  }
+  __syncthreads();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  bool ok = true;
+  if (warp == 0) {
+    if (lane == 0) ok = ring_load<T>(a, smem_u32(tiles), sh);
+  } else if (warp == 1) {
+    ok = ring_store<T>(a, tiles, sh);
+    if (lane == 0) bulk_wait_all();
+  } else if (warp == 2) {
+    ok = ring_list<T>(a, sh);
+  } else {
+    const int t = threadIdx.x - 96;
+    const float c = __fmul_rn(a.scale, kLog2E), slack = __fdiv_rn(kSlack, c);
+    RingPlace at;
+    uint32_t joined = 0;
+    int round = 0;
+    for (int64_t r = blockIdx.x; ok && r < a.rows; r += gridDim.x, ++round) {
+      const int set = round & 1;
+      ok = warp_wait(smem_u32(&sh.listed[set]), (round / 2) & 1);
+      if (!ok) break;
+      E* dx = static_cast<E*>(a.dlogits) + r * a.dlogits_stride;
+      const RingRow<T> row(a, r);
+      if (sh.list[set].w == 0.0f) {
+        const RowPart<T>& p = row.part;  // dx divides alike
+        const V zero = {make_uint4(0u, 0u, 0u, 0u)};
+        for (int64_t i = t; i < row.vectors; i += kRingThreads)
+          reinterpret_cast<uint4*>(dx + p.head)[i] = zero.v;
+        if (t < p.extra) dx[p.extra_index(t)] = Elem<T>::put(0.0f);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.taken[set]));
+        continue;
+      }
+      RowStats st;
+      st.clear();
+      auto add = [&](const V& v) {
+        float f[V::N];
+        v.get(f);
+#pragma unroll
+        for (int e = 0; e < V::N; ++e) st.s = __fadd_rn(st.s, exp2_fast(__fmul_rn(__fsub_rn(f[e], st.ref), c)));
+      };
+      for (int i = 0; i < row.tiles; ++i, at.next()) {
+        ok = warp_wait(smem_u32(&sh.full[at.slot]), at.phase);
+        if (!ok) break;
+        const uint4* data = reinterpret_cast<const uint4*>(tiles + at.slot * kTileBytes);
+        const int n = row.bytes(i) / 16;
+        V v[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          if (t + q * kRingThreads < n)
+            v[q].v = data[t + q * kRingThreads];
+          else
+            v[q].fill_minus_inf();
+        if (i < row.tiles - row.resident) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh.freed[at.slot]));
+        }
+        note_maximum(st, max_nan(v[0].max(), v[1].max()), c, slack);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) add(v[q]);
+      }
+      if (!ok) break;
+      if (t < row.part.extra) {
+        const float x = Elem<T>::get(row.part.row[row.part.extra_index(t)]);
+        note_maximum(st, x, c, slack);
+        st.s = __fadd_rn(st.s, exp2_fast(__fmul_rn(__fsub_rn(x, st.ref), c)));
+      }
+      st.u = 0.0f;
+      st = join_warp(st, c);
+      if (lane == 0) {
+        sh.stats[set][warp - 3] = st;
+        mbar_arrive(smem_u32(&sh.joined));
+      }
+      ok = warp_wait(smem_u32(&sh.joined), joined);
+      if (!ok) break;
+      joined ^= 1;
+      st.clear();
+      if (lane < kRingWarps) st = sh.stats[set][lane];
+      st = join_warp(st, c);
+      const bool zero = sh.list[set].none || st.m == -kInf;
+      const float A = __fdiv_rn(__fmul_rn(sh.list[set].w, a.scale), st.s), ref = st.ref;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.taken[set]));
+      // pass two: from the first resident tile on
+      RingPlace two = at;
+      two.slot += kRingSlots - row.resident;
+      two.phase ^= 1;
+      if (two.slot >= kRingSlots) {
+        two.slot -= kRingSlots;
+        two.phase ^= 1;
+      }
+      for (int i = 0; i < row.tiles; ++i, two.next()) {
+        if (i >= row.resident) {
+          ok = warp_wait(smem_u32(&sh.full[two.slot]), two.phase);
+          if (!ok) break;
+        }
+        uint4* data = reinterpret_cast<uint4*>(tiles + two.slot * kTileBytes);
+        const int n = row.bytes(row.tile_of(row.tiles - row.resident + i)) / 16;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          if (t + q * kRingThreads < n) {
+            V v;
+            float f[V::N];
+            v.v = data[t + q * kRingThreads];
+            v.get(f);
+#pragma unroll
+            for (int e = 0; e < V::N; ++e)
+              f[e] = __fmul_rn(exp2_fast(__fmul_rn(__fsub_rn(f[e], ref), c)), A);
+            if (zero) {
+#pragma unroll
+              for (int e = 0; e < V::N; ++e) f[e] = 0.0f;
+            }
+            v.put(f);
+            data[t + q * kRingThreads] = v.v;
+          }
+        fence_to_bulk();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.done[two.slot]));
+      }
+      at = two;
+    }
+  }
+  if (!ok && lane == 0 && a.d_status) atomicCAS(a.d_status, 0, MP_ERR_CUDA);
+}
+
+// Whether the ring takes these rows: logits and gradient divide into 16-B
+// vectors alike, and the rows are long and many enough.
+bool ring_takes(const DsArgs& a, int type, const DeviceInfo& dev) {
+  const int64_t size = type == MP_FP32 ? 4 : 2;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.logits), dx = reinterpret_cast<uintptr_t>(a.dlogits);
+  return a.dlogits && a.k <= kRingTeacher && (x - dx) % 16 == 0 && (a.stride - a.dlogits_stride) * size % 16 == 0 &&
+         a.rows >= 2 * dev.sms && a.vocab * size >= 4 * kTileBytes;
+}
+
 template <int T>
 cudaError_t launch(const DsArgs& a, const DeviceInfo& dev, cudaStream_t s) {
+  if (ring_takes(a, T, dev)) {
+    static std::atomic<bool> ready[64];
+    const cudaError_t e = allow_shared(distill_ring_kernel<T>, static_cast<int>(kRingBytes), ready);
+    if (e != cudaSuccess) return e;
+    return launch_pdl_smem(distill_ring_kernel<T>, static_cast<unsigned>(dev.sms), kRingBlock, kRingBytes, s, a);
+  }
   const int64_t units = a.vocab / 8, step = static_cast<int64_t>(kUnits<T>) * 32;
   const int threads = static_cast<int>(std::min<int64_t>(kDsThreads, std::max<int64_t>(1, units / step) * 32));
   int parts = 1;

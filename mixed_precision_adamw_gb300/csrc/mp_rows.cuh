@@ -220,6 +220,56 @@ struct Pack8<MP_FP32> {
   }
 };
 
+// Sixteen bytes of a row in shared memory.
+template <int T>
+struct Vec16 {
+  static constexpr int N = T == MP_FP32 ? 4 : 8;
+  uint4 v;
+
+  __device__ __forceinline__ void get(float (&f)[N]) const {
+    if constexpr (T == MP_FP32) {
+      f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y);
+      f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+    } else {
+      Pack8<T> p;
+      p.v = v;
+      p.get(f);
+    }
+  }
+  __device__ __forceinline__ void put(const float (&f)[N]) {
+    if constexpr (T == MP_FP32) {
+      v = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    } else {
+      Pack8<T> p;
+      p.put(f);
+      v = p.v;
+    }
+  }
+  __device__ __forceinline__ void fill_minus_inf() {
+    constexpr uint32_t w = T == MP_BF16 ? 0xFF80FF80u : T == MP_FP16 ? 0xFC00FC00u : 0xFF800000u;
+    v = make_uint4(w, w, w, w);
+  }
+  __device__ __forceinline__ float max() const {
+    if constexpr (T == MP_FP32) {
+      float f[4];
+      get(f);
+      return max_nan(max_nan(f[0], f[1]), max_nan(f[2], f[3]));
+    } else {
+      uint32_t a = v.x, b = v.z;
+      if (T == MP_BF16) {
+        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(v.y));
+        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(b) : "r"(v.w));
+        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+      } else {
+        asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(a) : "r"(v.y));
+        asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(b) : "r"(v.w));
+        asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+      }
+      return max_nan(Elem<T>::get(static_cast<uint16_t>(a)), Elem<T>::get(static_cast<uint16_t>(a >> 16)));
+    }
+  }
+};
+
 // The largest of U units' elements, NaN if one is NaN.
 template <int T, int U>
 __device__ __forceinline__ float max_of(const Pack8<T> (&x)[U]) {

@@ -510,6 +510,37 @@ def test_distill_masks_and_extremes(mp, dtype, vocab):
     assert torch.isnan(loss[9:12]).all()
 
 
+@pytest.mark.parametrize("dtype,vocab,pad", [(BF, 32768, 0), (BF, 50304, 24), (HF, 50261, 3), (BF, 128256, 0),
+                                             (FF, 60001, 0), (FF, 128256, 4), (BF, 180007, 1)])
+def test_distill_many_long_rows(mp, dtype, vocab, pad):
+    g = gen(25)
+    rows = 470
+    x = placed(randn((rows, vocab), g, 2.0, dtype), pad, 8)
+    t, idx = teacher_for(x, 40, g)
+    low = torch.finfo(dtype).min
+    w = torch.rand(rows, generator=g, device="cuda") + 0.5
+    w[5:9] = 0.0                       # rows of weight 0, several in one block's turn too
+    w[150:460:152] = 0.0
+    w[151:460:152] = 0.0
+    w[7] = -1.5
+    idx[10] = -1
+    t[11] = -INF
+    x[12] = -INF
+    x[13, idx[13, 1]] = -INF
+    x[14] = low
+    idx[15] = 11
+    idx[16, :6] = idx[16, 6:12]
+    x[17, vocab // 2] = math.nan
+    t[18, 2] = math.nan
+    x[19, : vocab // 2] = -INF
+    idx[20, 0], idx[20, 1], idx[20, 2] = 0, vocab - 1, vocab - 2  # the ends of the row
+    x[21] = torch.sort(x[21].float()).values.to(dtype)
+    x[6, 3] = math.nan                 # of weight 0
+    distill_case(mp, x, t, idx, w, scale=0.75)
+    big_t, big_i = teacher_for(x, 256, g)
+    distill_case(mp, x, big_t, big_i.int(), None)
+
+
 def test_distill_index_out_of_range(mp):
     g = gen(22)
     x = randn((3, 500), g, 2.0, BF)
@@ -595,6 +626,10 @@ def test_other_stream(mp):
     tgt = torch.randint(0, 5000, (300,), generator=g, device="cuda")
     torch.cuda.synchronize()
     lp_case(mp, x, tgt, k=3, stream=s)
+    distill_case(mp, x, t, idx, stream=s)
+    x = randn((400, 40000), g, 2.0, BF)
+    t, idx = teacher_for(x, 9, g)
+    torch.cuda.synchronize()
     distill_case(mp, x, t, idx, stream=s)
     ln_case(mp, 300, 768, BF, BF, stream=s)
 
