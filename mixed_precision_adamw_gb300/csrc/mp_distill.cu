@@ -211,9 +211,23 @@ struct RingList {
   int none, bad;
 };
 
+// A row's sum: s = sum 2^((x - ref) c); ref is -inf where nothing is above it.
+struct RingSum {
+  float ref, s;
+
+  // of a warp's lanes, to each of them
+  __device__ __forceinline__ RingSum join(float c) const {
+    RingSum a;
+    a.ref = warp_max(ref);
+    const float f = exp2_fast(__fmul_rn(__fsub_rn(ref, a.ref), c));
+    a.s = warp_sum(ref == -kInf ? 0.0f : __fmul_rn(s, f));
+    return a;
+  }
+};
+
 struct RingShared {
   RingList list[2];
-  RowStats stats[2][kRingWarps];
+  RingSum sums[2][kRingWarps];
   int32_t table[2 * kRingTeacher];
   unsigned long long full[kRingSlots], freed[kRingSlots], done[kRingSlots], listed[2], taken[2], joined;
 };
@@ -441,7 +455,7 @@ __device__ __noinline__ bool ring_store(const DsArgs& a, uint8_t* tiles, RingSha
       const E* x = row.part.row;
       E* dx = static_cast<E*>(a.dlogits) + r * a.dlogits_stride;
       at.next(row.tiles - row.resident);
-      RowStats st;
+      RingSum st;
       bool zero = true;
       int32_t token[kRingOwn];
       E grad[kRingOwn];
@@ -452,10 +466,10 @@ __device__ __noinline__ bool ring_store(const DsArgs& a, uint8_t* tiles, RingSha
         if (!warp_wait(done, done_phase >> at.slot & 1)) return false;
         done_phase ^= 1u << at.slot;
         if (i == 0) {  // every computing warp has left its sums
-          st.clear();
-          if (lane < kRingWarps) st = sh.stats[set][lane];
-          st = join_warp(st, c);
-          zero = l.none || st.m == -kInf;
+          st = sh.sums[set][lane % kRingWarps];
+          if (lane >= kRingWarps) st.ref = -kInf;
+          st = st.join(c);
+          zero = l.none || st.ref == -kInf;
           const float ws = __fmul_rn(l.w, a.scale);
 #pragma unroll
           for (int u = 0; u < kRingOwn; ++u) {  // the listed tokens' gradients
@@ -501,11 +515,14 @@ __device__ __noinline__ bool ring_store(const DsArgs& a, uint8_t* tiles, RingSha
         bulk_wait_read<0>();
         mbar_arrive_n(smem_u32(&sh.freed[at.slot == 0 ? kRingSlots - 1 : at.slot - 1]), kRingWarps);
       }
-      const RowLog log(st, c, a.scale);
+      const float log_s = logf(st.s);
       float kl = 0.0f;
 #pragma unroll 1
       for (int j = lane; j < a.k; j += 32)
-        if (l.q[j] != 0.0f) kl = __fmaf_rn(-l.q[j], log.log_p(l.z[j]), kl);
+        if (l.q[j] != 0.0f) {
+          const float log_p = st.ref == -kInf ? -kInf : __fmaf_rn(__fsub_rn(l.z[j], st.ref), a.scale, -log_s);
+          kl = __fmaf_rn(-l.q[j], log_p, kl);
+        }
       kl = __fadd_rn(warp_sum(kl), l.kl0);
       if (lane == 0) {
         a.loss[r] = l.bad ? __int_as_float(0x7FC00000) : l.none ? 0.0f : __fmul_rn(l.w, kl);
@@ -570,13 +587,13 @@ __global__ void __launch_bounds__(kRingBlock, 1) distill_ring_kernel(DsArgs a) {
         if (lane == 0) mbar_arrive(smem_u32(&sh.taken[set]));
         continue;
       }
-      RowStats st;
-      st.clear();
-      auto add = [&](const V& v) {
-        float f[V::N];
-        v.get(f);
-#pragma unroll
-        for (int e = 0; e < V::N; ++e) st.s = __fadd_rn(st.s, exp2_fast(__fmul_rn(__fsub_rn(f[e], st.ref), c)));
+      RingSum st = {-kInf, 0.0f};
+      float lim = -kInf;
+      auto note = [&](float top) {
+        if (top <= lim) return;
+        st.s = st.ref == -kInf ? 0.0f : __fmul_rn(st.s, exp2_fast(__fmul_rn(__fsub_rn(st.ref, top), c)));
+        st.ref = top;
+        lim = __fadd_rn(top, slack);
       };
       for (int i = 0; i < row.tiles; ++i, at.next()) {
         ok = warp_wait(smem_u32(&sh.full[at.slot]), at.phase);
@@ -594,30 +611,41 @@ __global__ void __launch_bounds__(kRingBlock, 1) distill_ring_kernel(DsArgs a) {
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh.freed[at.slot]));
         }
-        note_maximum(st, max_nan(v[0].max(), v[1].max()), c, slack);
+        note(max_nan(v[0].max(), v[1].max()));
 #pragma unroll
-        for (int q = 0; q < 2; ++q) add(v[q]);
+        for (int q = 0; q < 2; ++q) {
+          float f[V::N];
+          v[q].get(f);
+#pragma unroll
+          for (int e = 0; e < V::N; ++e)
+            st.s = __fadd_rn(st.s, exp2_fast(__fmul_rn(__fsub_rn(f[e], st.ref), c)));
+        }
       }
       if (!ok) break;
       if (t < row.part.extra) {
         const float x = Elem<T>::get(row.part.row[row.part.extra_index(t)]);
-        note_maximum(st, x, c, slack);
+        note(x);
         st.s = __fadd_rn(st.s, exp2_fast(__fmul_rn(__fsub_rn(x, st.ref), c)));
       }
-      st.u = 0.0f;
-      st = join_warp(st, c);
+      st = st.join(c);
       if (lane == 0) {
-        sh.stats[set][warp - 3] = st;
+        sh.sums[set][warp - 3] = st;
         mbar_arrive(smem_u32(&sh.joined));
       }
       ok = warp_wait(smem_u32(&sh.joined), joined);
       if (!ok) break;
       joined ^= 1;
-      st.clear();
-      if (lane < kRingWarps) st = sh.stats[set][lane];
-      st = join_warp(st, c);
-      const bool zero = sh.list[set].none || st.m == -kInf;
+      st = sh.sums[set][lane % kRingWarps];
+      if (lane >= kRingWarps) st.ref = -kInf;
+      st = st.join(c);
       const float A = __fdiv_rn(__fmul_rn(sh.list[set].w, a.scale), st.s), ref = st.ref;
+      const bool zero = sh.list[set].none || ref == -kInf;
+      // A 2^((x - ref) c) as 2^(c x + B): two operations fewer an element. The
+      // rounding of B, where |B| < 64, is a relative error below 2^-19 of the
+      // gradient; 16-bit types round it by 2^-12 or more. Other rows, and fp32,
+      // take the difference first.
+      const float B = __fsub_rn(log2f(A), __fmul_rn(ref, c));
+      const bool folded = T != MP_FP32 && fabsf(B) < 64.0f && fabsf(__fmul_rn(ref, c)) < 64.0f;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.taken[set]));
       // pass two: from the first resident tile on
@@ -642,14 +670,15 @@ __global__ void __launch_bounds__(kRingBlock, 1) distill_ring_kernel(DsArgs a) {
             float f[V::N];
             v.v = data[t + q * kRingThreads];
             v.get(f);
+            if (folded) {
 #pragma unroll
-            for (int e = 0; e < V::N; ++e)
-              f[e] = __fmul_rn(exp2_fast(__fmul_rn(__fsub_rn(f[e], ref), c)), A);
-            if (zero) {
+              for (int e = 0; e < V::N; ++e) f[e] = exp2_fast(__fmaf_rn(f[e], c, B));
+            } else {
 #pragma unroll
-              for (int e = 0; e < V::N; ++e) f[e] = 0.0f;
+              for (int e = 0; e < V::N; ++e) f[e] = __fmul_rn(exp2_fast(__fmul_rn(__fsub_rn(f[e], ref), c)), A);
             }
             v.put(f);
+            if (zero) v.v = make_uint4(0u, 0u, 0u, 0u);
             data[t + q * kRingThreads] = v.v;
           }
         fence_to_bulk();
