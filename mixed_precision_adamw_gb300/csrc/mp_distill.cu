@@ -185,16 +185,20 @@ __global__ void __launch_bounds__(kDsThreads, 4) distill_kernel(DsArgs a, int sl
 // bulk copies, the others are freed at once and loaded a second time, out of
 // L2. Meanwhile the loads of the following rows fill what is free.
 //
-// Warps: 0 loads tiles, 1 patches the listed tokens and stores tiles, 2 reads
-// the teacher's lists a row or two ahead, the other 16 compute. mbarriers:
+// Warps: 0 loads tiles, 1 and 2 patch the listed tokens and store tiles, 3 and 4
+// read the teacher's lists a row or two ahead (every second row each: what they
+// do is all latency), the other 16 compute. mbarriers:
 // full (tile has landed), freed (its slot may be loaded again: by each computing
-// warp, or sixteenfold by the storing thread), done (its gradient is written),
-// listed and taken (the two list buffers), joined (the row's sums). Every wait
+// warp, or sixteenfold by the storing thread), done (its gradient is written;
+// one set for each storing warp, because a wait tells phases apart by their
+// parity alone and may not begin before the one before last is over), listed
+// and taken (the two list buffers), joined (the row's sums). Every wait
 // gives up after a second and records MP_ERR_CUDA; nothing waits without that
 // limit, and the loads and stores in flight are waited for before a block ends.
 constexpr int kRingWarps = 16;
 constexpr int kRingThreads = 32 * kRingWarps;         // that compute
-constexpr int kRingBlock = kRingThreads + 96;
+constexpr int kRingHelpers = 5;                       // warps that do not compute
+constexpr int kRingBlock = kRingThreads + 32 * kRingHelpers;
 constexpr uint32_t kTileBytes = 2 * 16 * kRingThreads;  // two vectors a thread
 constexpr int kTileVectors = kTileBytes / 16;
 constexpr uint32_t kRingSlots = 13;
@@ -228,8 +232,8 @@ struct RingSum {
 struct RingShared {
   RingList list[2];
   RingSum sums[2][kRingWarps];
-  int32_t table[2 * kRingTeacher];
-  unsigned long long full[kRingSlots], freed[kRingSlots], done[kRingSlots], listed[2], taken[2], joined;
+  int32_t table[2][2 * kRingTeacher];
+  unsigned long long full[kRingSlots], freed[kRingSlots], done[2][kRingSlots], listed[2], taken[2], joined;
 };
 
 constexpr size_t kRingBytes = kRingSlots * kTileBytes + sizeof(RingShared);
@@ -314,7 +318,7 @@ __device__ __noinline__ bool ring_load(const DsArgs& a, uint32_t tiles, const Ri
 // teacher's logits and the weight of the next row are on their way while a row
 // is worked on.
 template <int T>
-__device__ __noinline__ bool ring_list(const DsArgs& a, RingShared& sh) {
+__device__ __noinline__ bool ring_list(const DsArgs& a, RingShared& sh, int set) {
   using E = typename Elem<T>::type;
   const int lane = threadIdx.x % 32;
   const float c = __fmul_rn(a.scale, kLog2E);
@@ -336,11 +340,11 @@ __device__ __noinline__ bool ring_list(const DsArgs& a, RingShared& sh) {
       }
     }
   };
-  fetch(blockIdx.x);
-  int round = 0;
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, ++round) {
-    const int set = round & 1;
-    RingList& l = sh.list[set];
+  const int64_t step = 2 * static_cast<int64_t>(gridDim.x);
+  RingList& l = sh.list[set];
+  fetch(blockIdx.x + set * gridDim.x);
+  uint32_t round = 0;  // of this set
+  for (int64_t r = blockIdx.x + set * gridDim.x; r < a.rows; r += step, ++round) {
     const E* x = static_cast<const E*>(a.logits) + r * a.stride;
     const float weight = w;
     int32_t token[kRingOwn];
@@ -356,8 +360,8 @@ __device__ __noinline__ bool ring_list(const DsArgs& a, RingShared& sh) {
       z[u] = use && weight != 0.0f ? Elem<T>::get(x[index[u]]) : 0.0f;
       tm = max_nan(tm, q[u]);
     }
-    fetch(r + gridDim.x);
-    if (round >= 2 && !warp_wait(smem_u32(&sh.taken[set]), (round / 2 - 1) & 1)) return false;
+    fetch(r + step);
+    if (round >= 1 && !warp_wait(smem_u32(&sh.taken[set]), (round - 1) & 1)) return false;
     if (weight != 0.0f) {
       tm = warp_max(tm);
       bad = __any_sync(kAll, bad);
@@ -370,7 +374,7 @@ __device__ __noinline__ bool ring_list(const DsArgs& a, RingShared& sh) {
       const float inv_ts = __fdiv_rn(1.0f, ts), log_ts = logf(ts);
       float kl0 = 0.0f;
 #pragma unroll 1
-      for (int i = lane; i < static_cast<int>(slots); i += 32) sh.table[i] = -1;
+      for (int i = lane; i < static_cast<int>(slots); i += 32) sh.table[set][i] = -1;
       __syncwarp();
       uint32_t twice = 0;  // bit u: entry u's token was in the table
 #pragma unroll
@@ -385,7 +389,7 @@ __device__ __noinline__ bool ring_list(const DsArgs& a, RingShared& sh) {
         if (token[u] >= 0) {
           uint32_t at = (static_cast<uint32_t>(token[u]) * 0x9E3779B1u) >> 16;
           for (uint32_t n = 0; n < slots; ++n, ++at) {
-            const int32_t was = atomicCAS(&sh.table[at & (slots - 1)], -1, token[u]);
+            const int32_t was = atomicCAS(&sh.table[set][at & (slots - 1)], -1, token[u]);
             if (was == token[u]) twice |= 1u << u;
             if (was == -1 || was == token[u]) break;
           }
@@ -437,7 +441,7 @@ __device__ __noinline__ bool ring_list(const DsArgs& a, RingShared& sh) {
 
 // Loss, listed tokens and stores.
 template <int T>
-__device__ __noinline__ bool ring_store(const DsArgs& a, uint8_t* tiles, RingShared& sh) {
+__device__ __noinline__ bool ring_store(const DsArgs& a, uint8_t* tiles, RingShared& sh, int mine) {
   using E = typename Elem<T>::type;
   const int lane = threadIdx.x % 32;
   const float c = __fmul_rn(a.scale, kLog2E);
@@ -448,7 +452,10 @@ __device__ __noinline__ bool ring_store(const DsArgs& a, uint8_t* tiles, RingSha
     const int set = round & 1;
     if (!warp_wait(smem_u32(&sh.listed[set]), (round / 2) & 1)) return false;
     RingList& l = sh.list[set];
-    if (l.w == 0.0f) {
+    const float w = l.w;
+    if (set != mine) {  // the other warp's row
+      if (w != 0.0f) at.next(RingRow<T>(a, r).loads());
+    } else if (w == 0.0f) {
       if (lane == 0) a.loss[r] = 0.0f;
     } else {
       const RingRow<T> row(a, r);
@@ -462,7 +469,7 @@ __device__ __noinline__ bool ring_store(const DsArgs& a, uint8_t* tiles, RingSha
 #pragma unroll 1
       for (int i = 0; i < row.tiles; ++i, at.next()) {
         const int tile = row.tile_of(row.tiles - row.resident + i);
-        const uint32_t done = smem_u32(&sh.done[at.slot]);
+        const uint32_t done = smem_u32(&sh.done[set][at.slot]);
         if (!warp_wait(done, done_phase >> at.slot & 1)) return false;
         done_phase ^= 1u << at.slot;
         if (i == 0) {  // every computing warp has left its sums
@@ -470,7 +477,7 @@ __device__ __noinline__ bool ring_store(const DsArgs& a, uint8_t* tiles, RingSha
           if (lane >= kRingWarps) st.ref = -kInf;
           st = st.join(c);
           zero = l.none || st.ref == -kInf;
-          const float ws = __fmul_rn(l.w, a.scale);
+          const float ws = __fmul_rn(w, a.scale);
 #pragma unroll
           for (int u = 0; u < kRingOwn; ++u) {  // the listed tokens' gradients
             const int j = 32 * u + lane;
@@ -525,7 +532,7 @@ __device__ __noinline__ bool ring_store(const DsArgs& a, uint8_t* tiles, RingSha
         }
       kl = __fadd_rn(warp_sum(kl), l.kl0);
       if (lane == 0) {
-        a.loss[r] = l.bad ? __int_as_float(0x7FC00000) : l.none ? 0.0f : __fmul_rn(l.w, kl);
+        a.loss[r] = l.bad ? __int_as_float(0x7FC00000) : l.none ? 0.0f : __fmul_rn(w, kl);
         if (l.bad && a.d_status) atomicCAS(a.d_status, 0, MP_ERR_RANGE);
       }
     }
@@ -546,11 +553,12 @@ __global__ void __launch_bounds__(kRingBlock, 1) distill_ring_kernel(DsArgs a) {
     for (uint32_t i = 0; i < kRingSlots; ++i) {
       mbar_init(smem_u32(&sh.full[i]), 1);
       mbar_init(smem_u32(&sh.freed[i]), kRingWarps);
-      mbar_init(smem_u32(&sh.done[i]), kRingWarps);
+      mbar_init(smem_u32(&sh.done[0][i]), kRingWarps);
+      mbar_init(smem_u32(&sh.done[1][i]), kRingWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sh.listed[i]), 1);
-      mbar_init(smem_u32(&sh.taken[i]), 1 + kRingWarps);
+      mbar_init(smem_u32(&sh.taken[i]), 2 + kRingWarps);
     }
     mbar_init(smem_u32(&sh.joined), kRingWarps);
     mbar_init_fence();
@@ -560,13 +568,13 @@ __global__ void __launch_bounds__(kRingBlock, 1) distill_ring_kernel(DsArgs a) {
   bool ok = true;
   if (warp == 0) {
     if (lane == 0) ok = ring_load<T>(a, smem_u32(tiles), sh);
-  } else if (warp == 1) {
-    ok = ring_store<T>(a, tiles, sh);
+  } else if (warp <= 2) {
+    ok = ring_store<T>(a, tiles, sh, warp - 1);
     if (lane == 0) bulk_wait_all();
-  } else if (warp == 2) {
-    ok = ring_list<T>(a, sh);
+  } else if (warp <= 4) {
+    ok = ring_list<T>(a, sh, warp - 3);
   } else {
-    const int t = threadIdx.x - 96;
+    const int t = threadIdx.x - 32 * kRingHelpers;
     const float c = __fmul_rn(a.scale, kLog2E), slack = __fdiv_rn(kSlack, c);
     RingPlace at;
     uint32_t joined = 0;
@@ -629,7 +637,7 @@ __global__ void __launch_bounds__(kRingBlock, 1) distill_ring_kernel(DsArgs a) {
       }
       st = st.join(c);
       if (lane == 0) {
-        sh.sums[set][warp - 3] = st;
+        sh.sums[set][warp - kRingHelpers] = st;
         mbar_arrive(smem_u32(&sh.joined));
       }
       ok = warp_wait(smem_u32(&sh.joined), joined);
@@ -683,7 +691,7 @@ __global__ void __launch_bounds__(kRingBlock, 1) distill_ring_kernel(DsArgs a) {
           }
         fence_to_bulk();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.done[two.slot]));
+        if (lane == 0) mbar_arrive(smem_u32(&sh.done[set][two.slot]));
       }
       at = two;
     }
