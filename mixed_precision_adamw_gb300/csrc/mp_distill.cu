@@ -187,22 +187,27 @@ __global__ void __launch_bounds__(kDsThreads, 4) distill_kernel(DsArgs a, int sl
 //
 // Warps: 0 loads tiles, 1 and 2 patch the listed tokens and store tiles, 3 and 4
 // read the teacher's lists a row or two ahead (every second row each: what they
-// do is all latency), the other 16 compute. mbarriers:
+// do is all latency), the others compute. mbarriers:
 // full (tile has landed), freed (its slot may be loaded again: by each computing
-// warp, or sixteenfold by the storing thread), done (its gradient is written;
+// warp, or as often by the storing thread), done (its gradient is written;
 // one set for each storing warp, because a wait tells phases apart by their
 // parity alone and may not begin before the one before last is over), listed
 // and taken (the two list buffers), joined (the row's sums). Every wait
 // gives up after a second and records MP_ERR_CUDA; nothing waits without that
 // limit, and the loads and stores in flight are waited for before a block ends.
-constexpr int kRingWarps = 16;
+// Measured on 8192 rows of 50304 and of 128256 bf16 (us), computing warps x
+// vectors a thread x slots: 12 x 3 x 12 338 and 688, 16 x 2 x 13 356 and 738,
+// 8 x 4 x 13 373 and 775, 14 x 3 x 10 334 and 691, 16 x 3 x 9 340 and 687,
+// 10 x 4 x 10 331 and 735, 20 x 2 x 10 339 and 723.
+constexpr int kRingWarps = 12;
+constexpr int kRingVectors = 3;                       // 16-B vectors of a tile a thread takes
 constexpr int kRingThreads = 32 * kRingWarps;         // that compute
 constexpr int kRingHelpers = 5;                       // warps that do not compute
 constexpr int kRingBlock = kRingThreads + 32 * kRingHelpers;
-constexpr uint32_t kTileBytes = 2 * 16 * kRingThreads;  // two vectors a thread
+constexpr uint32_t kTileBytes = 16 * kRingVectors * kRingThreads;
 constexpr int kTileVectors = kTileBytes / 16;
-constexpr uint32_t kRingSlots = 13;
-constexpr int kRingResident = 11;                     // tiles of a row kept between its passes, at most
+constexpr uint32_t kRingSlots = 12;
+constexpr int kRingResident = 10;                     // tiles of a row kept between its passes, at most
 constexpr int kRingTeacher = 128;                     // list length, at most
 constexpr int kRingOwn = kRingTeacher / 32;           // list entries a lane holds
 
@@ -473,7 +478,7 @@ __device__ __noinline__ bool ring_store(const DsArgs& a, uint8_t* tiles, RingSha
         if (!warp_wait(done, done_phase >> at.slot & 1)) return false;
         done_phase ^= 1u << at.slot;
         if (i == 0) {  // every computing warp has left its sums
-          st = sh.sums[set][lane % kRingWarps];
+          st = sh.sums[set][lane < kRingWarps ? lane : 0];
           if (lane >= kRingWarps) st.ref = -kInf;
           st = st.join(c);
           zero = l.none || st.ref == -kInf;
@@ -606,28 +611,36 @@ __global__ void __launch_bounds__(kRingBlock, 1) distill_ring_kernel(DsArgs a) {
       for (int i = 0; i < row.tiles; ++i, at.next()) {
         ok = warp_wait(smem_u32(&sh.full[at.slot]), at.phase);
         if (!ok) break;
-        const uint4* data = reinterpret_cast<const uint4*>(tiles + at.slot * kTileBytes);
-        const int n = row.bytes(i) / 16;
-        V v[2];
+        const uint4* data = reinterpret_cast<const uint4*>(tiles + at.slot * kTileBytes) + t;
+        V v[kRingVectors];
+        if (i + 1 < row.tiles || row.vectors % kTileVectors == 0) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-          if (t + q * kRingThreads < n)
-            v[q].v = data[t + q * kRingThreads];
-          else
+          for (int q = 0; q < kRingVectors; ++q) v[q].v = data[q * kRingThreads];
+        } else {
+          const int n = static_cast<int>(row.vectors % kTileVectors);
+#pragma unroll
+          for (int q = 0; q < kRingVectors; ++q) {
             v[q].fill_minus_inf();
+            if (t + q * kRingThreads < n) v[q].v = data[q * kRingThreads];
+          }
+        }
         if (i < row.tiles - row.resident) {
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh.freed[at.slot]));
         }
-        note(max_nan(v[0].max(), v[1].max()));
+        note(V::max_of(v));
+        float sum[kRingVectors];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < kRingVectors; ++q) {
           float f[V::N];
           v[q].get(f);
+          sum[q] = 0.0f;
 #pragma unroll
           for (int e = 0; e < V::N; ++e)
-            st.s = __fadd_rn(st.s, exp2_fast(__fmul_rn(__fsub_rn(f[e], st.ref), c)));
+            sum[q] = __fadd_rn(sum[q], exp2_fast(__fmul_rn(__fsub_rn(f[e], st.ref), c)));
         }
+#pragma unroll
+        for (int q = 0; q < kRingVectors; ++q) st.s = __fadd_rn(st.s, sum[q]);
       }
       if (!ok) break;
       if (t < row.part.extra) {
@@ -643,7 +656,7 @@ __global__ void __launch_bounds__(kRingBlock, 1) distill_ring_kernel(DsArgs a) {
       ok = warp_wait(smem_u32(&sh.joined), joined);
       if (!ok) break;
       joined ^= 1;
-      st = sh.sums[set][lane % kRingWarps];
+      st = sh.sums[set][lane < kRingWarps ? lane : 0];
       if (lane >= kRingWarps) st.ref = -kInf;
       st = st.join(c);
       const float A = __fdiv_rn(__fmul_rn(sh.list[set].w, a.scale), st.s), ref = st.ref;
@@ -669,26 +682,29 @@ __global__ void __launch_bounds__(kRingBlock, 1) distill_ring_kernel(DsArgs a) {
           ok = warp_wait(smem_u32(&sh.full[two.slot]), two.phase);
           if (!ok) break;
         }
-        uint4* data = reinterpret_cast<uint4*>(tiles + two.slot * kTileBytes);
-        const int n = row.bytes(row.tile_of(row.tiles - row.resident + i)) / 16;
+        uint4* data = reinterpret_cast<uint4*>(tiles + two.slot * kTileBytes) + t;
+        const int tile = row.tile_of(row.tiles - row.resident + i);
+        const int n = tile + 1 < row.tiles ? kTileVectors : static_cast<int>(row.vectors - static_cast<int64_t>(tile) * kTileVectors);
+        V v[kRingVectors];
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-          if (t + q * kRingThreads < n) {
-            V v;
-            float f[V::N];
-            v.v = data[t + q * kRingThreads];
-            v.get(f);
-            if (folded) {
+        for (int q = 0; q < kRingVectors; ++q) v[q].v = data[q * kRingThreads];  // past the row: not stored
 #pragma unroll
-              for (int e = 0; e < V::N; ++e) f[e] = exp2_fast(__fmaf_rn(f[e], c, B));
-            } else {
+        for (int q = 0; q < kRingVectors; ++q) {
+          float f[V::N];
+          v[q].get(f);
+          if (folded) {
 #pragma unroll
-              for (int e = 0; e < V::N; ++e) f[e] = __fmul_rn(exp2_fast(__fmul_rn(__fsub_rn(f[e], ref), c)), A);
-            }
-            v.put(f);
-            if (zero) v.v = make_uint4(0u, 0u, 0u, 0u);
-            data[t + q * kRingThreads] = v.v;
+            for (int e = 0; e < V::N; ++e) f[e] = exp2_fast(__fmaf_rn(f[e], c, B));
+          } else {
+#pragma unroll
+            for (int e = 0; e < V::N; ++e) f[e] = __fmul_rn(exp2_fast(__fmul_rn(__fsub_rn(f[e], ref), c)), A);
           }
+          v[q].put(f);
+          if (zero) v[q].v = make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int q = 0; q < kRingVectors; ++q)
+          if (t + q * kRingThreads < n) data[q * kRingThreads] = v[q].v;
         fence_to_bulk();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.done[set][two.slot]));

@@ -249,21 +249,32 @@ struct Vec16 {
     constexpr uint32_t w = T == MP_BF16 ? 0xFF80FF80u : T == MP_FP16 ? 0xFC00FC00u : 0xFF800000u;
     v = make_uint4(w, w, w, w);
   }
-  __device__ __forceinline__ float max() const {
+  // the largest of n vectors' elements, NaN if one is NaN
+  template <int n>
+  static __device__ __forceinline__ float max_of(const Vec16 (&x)[n]) {
     if constexpr (T == MP_FP32) {
-      float f[4];
-      get(f);
-      return max_nan(max_nan(f[0], f[1]), max_nan(f[2], f[3]));
+      float m = -kInf;
+#pragma unroll
+      for (int q = 0; q < n; ++q) {
+        float f[4];
+        x[q].get(f);
+        m = max_nan(m, max_nan(max_nan(f[0], f[1]), max_nan(f[2], f[3])));
+      }
+      return m;
     } else {
-      uint32_t a = v.x, b = v.z;
-      if (T == MP_BF16) {
-        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(v.y));
-        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(b) : "r"(v.w));
-        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
-      } else {
-        asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(a) : "r"(v.y));
-        asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(b) : "r"(v.w));
-        asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+      uint32_t a = x[0].v.x;
+      auto take = [&](uint32_t w) {
+        if (T == MP_BF16)
+          asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(w));
+        else
+          asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(a) : "r"(w));
+      };
+#pragma unroll
+      for (int q = 0; q < n; ++q) {
+        if (q) take(x[q].v.x);
+        take(x[q].v.y);
+        take(x[q].v.z);
+        take(x[q].v.w);
       }
       return max_nan(Elem<T>::get(static_cast<uint16_t>(a)), Elem<T>::get(static_cast<uint16_t>(a >> 16)));
     }
