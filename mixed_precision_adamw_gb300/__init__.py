@@ -177,8 +177,15 @@ def _ptr(t: Optional[torch.Tensor], dtypes, name: str, n: Optional[int] = None) 
     return t.data_ptr()
 
 
+# The handle of a device's current stream without a Stream object around it
+# (building one costs more than a kernel launch).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream

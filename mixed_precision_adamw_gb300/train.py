@@ -51,15 +51,50 @@ def _on(t, name: str, dev: int) -> None:
         raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
 
 
-def _matrix(t, name: str, dev: int, dtype=None, shape=None):
-    """(pointer, row stride) of a 2-D tensor with contiguous rows."""
+# The checks below run on every call, in front of kernels of a few
+# microseconds: the common case is one condition, and what is wrong with the
+# others is found out afterwards.
+
+def _matrix(t, name: str, dev: int, like=None):
+    """(pointer, row stride, code of the element type) of a 2-D tensor with
+    contiguous rows, of the shape and type of the tensor `like` if given."""
+    if isinstance(t, torch.Tensor) and t.get_device() == dev:
+        code = _TYPES.get(t.dtype)
+        shape = t.shape
+        if code is not None and len(shape) == 2 and (like is None or (shape == like.shape and t.dtype == like.dtype)):
+            stride, last = t.stride()
+            if last == 1 and stride >= shape[1]:
+                return t.data_ptr(), stride, code
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    code = _TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(_TYPES)}")
     _on(t, name, dev)
+    return _rows(t, name, like) + (code,)
+
+
+def _index_matrix(t, name: str, dev: int, like):
+    """The same of an int32 or int64 matrix of the shape of `like`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    code = _INDEX_TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(_INDEX_TYPES)}")
+    _on(t, name, dev)
+    if t.shape != like.shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(like.shape)}")
+    return _rows(t, name, None) + (code,)
+
+
+def _rows(t, name: str, like):
     if t.dim() != 2:
         raise ValueError(f"{name}: {t.dim()}-D, expected [rows, length]")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if like is not None:
+        if t.dtype != like.dtype:
+            raise TypeError(f"{name}: dtype {t.dtype}, expected {like.dtype}")
+        if t.shape != like.shape:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(like.shape)}")
     stride, last = t.stride()
     rows, cols = t.shape
     if last != 1 and cols > 1:
@@ -75,40 +110,32 @@ def _vector(t, name: str, dev: int, n: int, dtypes):
     """Pointer of a contiguous tensor of n elements; None stays None."""
     if t is None:
         return None
+    if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype in dtypes and t.numel() == n
+            and t.is_contiguous()):
+        return t.data_ptr()
     _on(t, name, dev)
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(dtypes)}")
     if t.numel() != n:
         raise ValueError(f"{name}: {t.numel()} elements, expected {n}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name}: must be contiguous")
 
 
-_F32 = (torch.float32,)
-_I32 = (torch.int32,)
+_F32 = frozenset((torch.float32,))
+_I32 = frozenset((torch.int32,))
+_U8 = frozenset((torch.uint8,))
 
 
-def _type_of(t, name: str) -> int:
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor")
-    code = _TYPES.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(_TYPES)}")
-    return code
-
-
-def _weight_type(*named) -> int:
+def _weight_type(*weights) -> int:
     """The common type of the given weight tensors (float32 if none is given)."""
-    code = None
-    for t, name in named:
-        if t is None:
-            continue
-        c = _type_of(t, name)
-        if code is not None and c != code:
-            raise TypeError(f"{name}: weight, bias and their gradients must have one dtype")
-        code = c
-    return MP_FP32 if code is None else code
+    dtype = None
+    for t in weights:
+        if t is not None:
+            if dtype is None:
+                dtype = t.dtype
+            elif t.dtype != dtype:
+                raise TypeError("weight, bias and their gradients must have one dtype")
+    return MP_FP32 if dtype is None else _TYPES[dtype]
 
 
 def mp_layernorm_forward(y: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor] = None,
@@ -119,15 +146,15 @@ def mp_layernorm_forward(y: torch.Tensor, x: torch.Tensor, weight: Optional[torc
     bias if given; mean and rstd (float32 [rows]) are kept for the backward
     pass. y may be x itself."""
     dev = torch.cuda.current_device()
-    code = _type_of(x, "x")
-    xp, xs = _matrix(x, "x", dev)
-    yp, ys = _matrix(y, "y", dev, x.dtype, x.shape)
+    xp, xs, code = _matrix(x, "x", dev)
+    yp, ys, _ = _matrix(y, "y", dev, x)
     rows, d = x.shape
-    wcode = _weight_type((weight, "weight"), (bias, "bias"))
-    _check(_lib.mp_layernorm_forward(
+    st = _lib.mp_layernorm_forward(
         yp, _vector(mean, "mean", dev, rows, _F32), _vector(rstd, "rstd", dev, rows, _F32), xp,
         _vector(weight, "weight", dev, d, _TYPES), _vector(bias, "bias", dev, d, _TYPES), rows, d, ys, xs, eps, code,
-        wcode, _stream(stream)), "mp_layernorm_forward")
+        _weight_type(weight, bias), _stream(stream))
+    if st:
+        _check(st, "mp_layernorm_forward")
 
 
 def mp_layernorm_workspace_bytes(rows: int, d: int) -> int:
@@ -144,21 +171,21 @@ def mp_layernorm_backward(dx: Optional[torch.Tensor], dweight: Optional[torch.Te
     three may be None). dx may be dy itself. workspace: uint8 of
     mp_layernorm_workspace_bytes(rows, d) bytes, when dweight or dbias is given."""
     dev = torch.cuda.current_device()
-    code = _type_of(x, "x")
-    xp, xs = _matrix(x, "x", dev)
+    xp, xs, code = _matrix(x, "x", dev)
     rows, d = x.shape
-    dyp, dys = _matrix(dy, "dy", dev, x.dtype, x.shape)
-    dxp, dxs = (None, 0) if dx is None else _matrix(dx, "dx", dev, x.dtype, x.shape)
-    wcode = _weight_type((weight, "weight"), (dweight, "dweight"), (dbias, "dbias"))
+    dyp, dys, _ = _matrix(dy, "dy", dev, x)
+    dxp, dxs, _ = (None, 0, 0) if dx is None else _matrix(dx, "dx", dev, x)
     wsp, wsn = None, 0
     if workspace is not None:
         wsn = workspace.numel()
-        wsp = _vector(workspace, "workspace", dev, wsn, (torch.uint8,))
-    _check(_lib.mp_layernorm_backward(
+        wsp = _vector(workspace, "workspace", dev, wsn, _U8)
+    st = _lib.mp_layernorm_backward(
         dxp, _vector(dweight, "dweight", dev, d, _TYPES), _vector(dbias, "dbias", dev, d, _TYPES), dyp, xp,
         _vector(weight, "weight", dev, d, _TYPES), _vector(mean, "mean", dev, rows, _F32),
-        _vector(rstd, "rstd", dev, rows, _F32), rows, d, dxs, dys, xs, code, wcode, wsp, wsn, _stream(stream)),
-        "mp_layernorm_backward")
+        _vector(rstd, "rstd", dev, rows, _F32), rows, d, dxs, dys, xs, code, _weight_type(weight, dweight, dbias), wsp,
+        wsn, _stream(stream))
+    if st:
+        _check(st, "mp_layernorm_backward")
 
 
 def _index_type(t, name: str) -> int:
@@ -180,8 +207,7 @@ def mp_token_logprob_forward(logits: torch.Tensor, targets: Optional[torch.Tenso
     (top_logp float32 and top_index int32, both [rows, k], k <= 32; largest
     first, equal ones by rising index). Negative targets: no given token."""
     dev = torch.cuda.current_device()
-    code = _type_of(logits, "logits")
-    lp, ls = _matrix(logits, "logits", dev)
+    lp, ls, code = _matrix(logits, "logits", dev)
     rows, vocab = logits.shape
     icode = MP_INT64 if targets is None else _index_type(targets, "targets")
     k, tlp, tip = 0, None, None
@@ -193,11 +219,12 @@ def mp_token_logprob_forward(logits: torch.Tensor, targets: Optional[torch.Tenso
         k = top_logp.shape[1]
         tlp = _vector(top_logp, "top_logp", dev, rows * k, _F32)
         tip = _vector(top_index, "top_index", dev, rows * k, _I32)
-    _check(_lib.mp_token_logprob_forward(
+    st = _lib.mp_token_logprob_forward(
         _vector(logp, "logp", dev, rows, _F32), _vector(lse, "lse", dev, rows, _F32),
         _vector(entropy, "entropy", dev, rows, _F32), tlp, tip, lp, _vector(targets, "targets", dev, rows, _INDEX_TYPES),
-        rows, vocab, ls, scale, k, code, icode, _vector(d_status, "d_status", dev, 1, _I32), _stream(stream)),
-        "mp_token_logprob_forward")
+        rows, vocab, ls, scale, k, code, icode, _vector(d_status, "d_status", dev, 1, _I32), _stream(stream))
+    if st:
+        _check(st, "mp_token_logprob_forward")
 
 
 def mp_token_logprob_backward(dlogits: torch.Tensor, logits: torch.Tensor, targets: Optional[torch.Tensor], *,
@@ -208,18 +235,19 @@ def mp_token_logprob_backward(dlogits: torch.Tensor, logits: torch.Tensor, targe
     probabilities and dentropy of the entropies (with the forward pass's lse
     and entropy). dlogits may be logits itself."""
     dev = torch.cuda.current_device()
-    code = _type_of(logits, "logits")
-    lp, ls = _matrix(logits, "logits", dev)
+    lp, ls, code = _matrix(logits, "logits", dev)
     rows, vocab = logits.shape
-    dp, ds = _matrix(dlogits, "dlogits", dev, logits.dtype, logits.shape)
+    dp, ds, _ = _matrix(dlogits, "dlogits", dev, logits)
     icode = MP_INT64 if targets is None else _index_type(targets, "targets")
     if dentropy is None:
         entropy = None  # only its own gradient needs it
-    _check(_lib.mp_token_logprob_backward(
+    st = _lib.mp_token_logprob_backward(
         dp, lp, _vector(targets, "targets", dev, rows, _INDEX_TYPES), _vector(lse, "lse", dev, rows, _F32),
         _vector(entropy, "entropy", dev, rows, _F32), _vector(dlogp, "dlogp", dev, rows, _F32),
         _vector(dentropy, "dentropy", dev, rows, _F32), rows, vocab, ds, ls, scale, code, icode,
-        _vector(d_status, "d_status", dev, 1, _I32), _stream(stream)), "mp_token_logprob_backward")
+        _vector(d_status, "d_status", dev, 1, _I32), _stream(stream))
+    if st:
+        _check(st, "mp_token_logprob_backward")
 
 
 def mp_distill_topk(loss: torch.Tensor, dlogits: Optional[torch.Tensor], logits: torch.Tensor,
@@ -231,19 +259,21 @@ def mp_distill_topk(loss: torch.Tensor, dlogits: Optional[torch.Tensor], logits:
     index: [rows, k], k <= 1024, negative indices unused. dlogits may be logits
     itself."""
     dev = torch.cuda.current_device()
-    code = _type_of(logits, "logits")
-    lp, ls = _matrix(logits, "logits", dev)
+    lp, ls, code = _matrix(logits, "logits", dev)
     rows, vocab = logits.shape
-    dp, ds = (None, 0) if dlogits is None else _matrix(dlogits, "dlogits", dev, logits.dtype, logits.shape)
-    tp, ts = _matrix(teacher, "teacher", dev, logits.dtype)
-    icode = _index_type(index, "index")
-    ip, istride = _matrix(index, "index", dev, shape=teacher.shape)
+    dp, ds, _ = (None, 0, 0) if dlogits is None else _matrix(dlogits, "dlogits", dev, logits)
+    tp, ts, tcode = _matrix(teacher, "teacher", dev)
+    if tcode != code:
+        raise TypeError(f"teacher: dtype {teacher.dtype}, expected {logits.dtype}")
+    ip, istride, icode = _index_matrix(index, "index", dev, teacher)
     if teacher.shape[0] != rows:
         raise ValueError(f"teacher: {teacher.shape[0]} rows, expected {rows}")
-    _check(_lib.mp_distill_topk(
+    st = _lib.mp_distill_topk(
         _vector(loss, "loss", dev, rows, _F32), dp, lp, tp, ip, _vector(row_weight, "row_weight", dev, rows, _F32),
         rows, vocab, teacher.shape[1], ds, ls, ts, istride, scale, code, icode,
-        _vector(d_status, "d_status", dev, 1, _I32), _stream(stream)), "mp_distill_topk")
+        _vector(d_status, "d_status", dev, 1, _I32), _stream(stream))
+    if st:
+        _check(st, "mp_distill_topk")
 
 
 __all__ = [
