@@ -10,6 +10,7 @@
 #include "mp_device.cuh"
 #include "mp_internal.h"
 #include "mp_rows.cuh"
+#include "mp_tma.cuh"
 
 namespace mpk {
 namespace {
@@ -88,12 +89,51 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   return s;
 }
 
+// ---- rows staged through shared memory ------------------------------------------
+// The TMA engine copies rows into shared memory ahead of their use (1D bulk
+// copies, two stages), so that loads stay in flight without registers or
+// resident warps to hold them. A copy moves the whole 16-B pieces of a row; the
+// fewer than 8 elements before and after them (rows that do not start or end on
+// a 16-B boundary) are loaded by threads and put beside them. A row lies in its
+// buffer at the offset that its address has from a 16-B boundary.
+template <int T>
+struct StagedRow {
+  using E = typename Elem<T>::type;
+  const E* row;
+  uint32_t offset;  // bytes of the row's first element in the buffer
+  int head, tail;   // elements before and after the whole pieces
+  uint32_t bytes;   // of the whole pieces
+
+  __device__ __forceinline__ StagedRow(const E* p, int64_t d) : row(p) {
+    constexpr int kAlign = 16 / sizeof(E);
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) / sizeof(E) % kAlign);
+    offset = off * sizeof(E);
+    head = off ? kAlign - off : 0;
+    if (head > d) head = static_cast<int>(d);
+    tail = static_cast<int>((d - head) % kAlign);
+    bytes = static_cast<uint32_t>(d - head - tail) * sizeof(E);
+  }
+  __device__ __forceinline__ void copy(uint32_t buffer, uint32_t bar) const {
+    if (bytes) bulk_load(buffer + offset + head * sizeof(E), row + head, bytes, bar);
+  }
+  // the i-th of the elements that the copy leaves out
+  __device__ __forceinline__ int edge(int i, int64_t d) const {
+    return i < head ? i : static_cast<int>(d) - tail + (i - head);
+  }
+};
+
+constexpr int kStages = 2;
+
+// Bytes of a row's buffer.
+inline uint32_t staged_pitch(int64_t d, int type) {
+  return static_cast<uint32_t>((d * (type == MP_FP32 ? 4 : 2) + 15) / 16 * 16 + 16);
+}
+
 // ---- forward ----------------------------------------------------------------
-// Groups of L threads take a row each: L <= 32 lanes of a warp (no barrier in
-// the loop), or L = 256, a whole block. Weight and bias are widened into
-// shared memory once a block: at most 8 B a column are read there for 4 B or
-// more of memory traffic, and neither their type nor their alignment (they
-// may sit anywhere in a flat buffer) matters afterwards.
+// Weight and bias are widened into shared memory once a block: at most 8 B a
+// column are read there for 4 B or more of memory traffic, and neither their
+// type nor their alignment (they may sit anywhere in a flat buffer) matters
+// afterwards.
 //
 // Eight weights of a unit lie in two planes of four, so that the lanes of a
 // warp read 16 consecutive bytes each.
@@ -110,89 +150,196 @@ __device__ __forceinline__ void stage_weights(float* sw, const LnArgs& a, int64_
   }
 }
 
-template <int T, bool Wide, int L, int NV>
-__global__ void __launch_bounds__(kLnThreads, NV >= 8 ? 3 : 4) ln_forward_kernel(LnArgs a) {
+// y of a unit of a row from its x.
+template <int T, bool Wide>
+__device__ __forceinline__ void normalise_unit(Pack8<T>& u, const float* sw, const float* sb, float mean, float rstd,
+                                               int v, int t, int L, int64_t units, int64_t d) {
+  float f[8], w[8], b[8];
+  u.get(f);
+  if (Wide) {
+    const int64_t unit = min(static_cast<int64_t>(v) * L + t, units - 1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float4 p = *reinterpret_cast<const float4*>(sw + (h * units + unit) * 4);
+      const float4 q = *reinterpret_cast<const float4*>(sb + (h * units + unit) * 4);
+      w[4 * h] = p.x, w[4 * h + 1] = p.y, w[4 * h + 2] = p.z, w[4 * h + 3] = p.w;
+      b[4 * h] = q.x, b[4 * h + 1] = q.y, b[4 * h + 2] = q.z, b[4 * h + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int64_t j = min(column<Wide>(v, e, t, L), d - 1);
+      w[e] = sw[j];
+      b[e] = sb[j];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = __fmaf_rn(__fmul_rn(__fsub_rn(f[e], mean), rstd), w[e], b[e]);
+  u.put(f);
+}
+
+// Short rows, up to 8 * L elements: L lanes of a warp take a row each, four
+// rows a round so that enough loads are in flight, no barrier.
+template <int T, bool Wide, int L>
+__global__ void __launch_bounds__(kLnThreads, 4) ln_forward_short_kernel(LnArgs a) {
   pdl_enter();
   using E = typename Elem<T>::type;
-  constexpr bool kBlock = L > 32;
-  __shared__ float red[kLnThreads / 32];
-  extern __shared__ float sw[];
+  constexpr int R = T == MP_FP32 ? 2 : 4;
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* sw = reinterpret_cast<float*>(smem);
   const int t = threadIdx.x % L;
   const int64_t units = (a.d + 7) / 8;
-  const float* sb = sw + 8 * units;
-  const int64_t groups = static_cast<int64_t>(gridDim.x) * (kLnThreads / L);
   const float n = static_cast<float>(a.d);
-  // every lane of a warp runs the same number of rounds (the shuffles are whole-warp)
+  const int64_t groups = static_cast<int64_t>(gridDim.x) * (kLnThreads / L);
   const int64_t first = static_cast<int64_t>(blockIdx.x) * (kLnThreads / L) + threadIdx.x / L;
-  for (int64_t r0 = 0; r0 < a.rows; r0 += groups) {
-    const int64_t r = r0 + first;
-    const bool live = r < a.rows;
-    const E* x = static_cast<const E*>(a.x) + (live ? r : 0) * a.x_stride;
-    Pack8<T> u[NV];
+  stage_weights<Wide>(sw, a, units, kLnThreads);
+  __syncthreads();
+  // every lane of a warp runs the same number of rounds (the shuffles are whole-warp)
+  for (int64_t r0 = 0; r0 < a.rows; r0 += R * groups) {
+    Pack8<T> u[R];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) load_unit<T, Wide>(u[v], x, v, t, L, live ? a.d : 0);
-    if (r0 == 0) {  // with the first rows on their way
-      stage_weights<Wide>(sw, a, units, kLnThreads);
-      __syncthreads();
+    for (int i = 0; i < R; ++i) {
+      const int64_t r = r0 + i * groups + first;
+      const bool live = r < a.rows;
+      load_unit<T, Wide>(u[i], static_cast<const E*>(a.x) + (live ? r : 0) * a.x_stride, 0, t, L, live ? a.d : 0);
     }
-    if (kBlock && !live) break;
-    float s = 0.0f;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      float f[8];
-      u[v].get(f);
+    for (int i = 0; i < R; ++i) {
+      const int64_t r = r0 + i * groups + first;
+      float f[8], s = 0.0f, q = 0.0f;
+      u[i].get(f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) s = __fadd_rn(s, f[e]);  // elements past the row are 0
-    }
-    const float mean = __fdiv_rn(kBlock ? block_sum(s, red) : lanes_sum<kBlock ? 32 : L>(s), n);
-    float q = 0.0f;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      float f[8];
-      u[v].get(f);
+      const float mean = __fdiv_rn(lanes_sum<L>(s), n);
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (in_row<Wide>(v, e, t, L, a.d)) {
+        if (in_row<Wide>(0, e, t, L, a.d)) {
           const float c = __fsub_rn(f[e], mean);
           q = __fmaf_rn(c, c, q);
         }
-    }
-    const float var = __fdiv_rn(kBlock ? block_sum(q, red) : lanes_sum<kBlock ? 32 : L>(q), n);
-    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(var, a.eps)));
-    if (!live) continue;
-    E* y = static_cast<E*>(a.y) + r * a.y_stride;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      float f[8], w[8], b[8];
-      u[v].get(f);
-      if (Wide) {
-        const int64_t unit = static_cast<int64_t>(v) * L + t;
-        if (unit >= units) continue;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float4 p = *reinterpret_cast<const float4*>(sw + (h * units + unit) * 4);
-          const float4 q4 = *reinterpret_cast<const float4*>(sb + (h * units + unit) * 4);
-          w[4 * h] = p.x, w[4 * h + 1] = p.y, w[4 * h + 2] = p.z, w[4 * h + 3] = p.w;
-          b[4 * h] = q4.x, b[4 * h + 1] = q4.y, b[4 * h + 2] = q4.z, b[4 * h + 3] = q4.w;
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int64_t j = column<Wide>(v, e, t, L);
-          w[e] = j < a.d ? sw[j] : 0.0f;
-          b[e] = j < a.d ? sb[j] : 0.0f;
-        }
+      const float var = __fdiv_rn(lanes_sum<L>(q), n);
+      const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(var, a.eps)));
+      if (r >= a.rows) continue;
+      normalise_unit<T, Wide>(u[i], sw, sw + 8 * units, mean, rstd, 0, t, L, units, a.d);
+      store_unit<T, Wide>(u[i], static_cast<E*>(a.y) + r * a.y_stride, 0, t, L, a.d);
+      if (t == 0) {
+        if (a.mean_out) a.mean_out[r] = mean;
+        if (a.rstd_out) a.rstd_out[r] = rstd;
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = __fmaf_rn(__fmul_rn(__fsub_rn(f[e], mean), rstd), w[e], b[e]);
-      u[v].put(f);
-      store_unit<T, Wide>(u[v], y, v, t, L, a.d);
-    }
-    if (t == 0) {
-      if (a.mean_out) a.mean_out[r] = mean;
-      if (a.rstd_out) a.rstd_out[r] = rstd;
     }
   }
+}
+
+// Longer rows: groups of G warps (1, 2, 4 or 8 of a block's 8) take a row each
+// from two staged buffers of their own, NV units a thread in registers. A
+// group's warps meet at a named barrier of their own for each of the two sums.
+template <int T, bool Wide, int NV>
+__global__ void __launch_bounds__(kLnThreads, NV >= 8 ? 2 : NV >= 4 ? 3 : 4) ln_forward_kernel(LnArgs a, int G, uint32_t pitch) {
+  pdl_enter();
+  using E = typename Elem<T>::type;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float red[2][kLnThreads / 32];
+  __shared__ unsigned long long full[kStages * kLnThreads / 32];
+  const int64_t units = (a.d + 7) / 8;
+  float* sw = reinterpret_cast<float*>(smem);
+  const int L = 32 * G, t = threadIdx.x % L, group = threadIdx.x / L, count = kLnThreads / L;
+  uint8_t* buffers = smem + 64 * units + static_cast<size_t>(group) * kStages * pitch;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * count;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * count + group;
+  if (threadIdx.x < kStages * count) mbar_init(smem_u32(&full[threadIdx.x]), 1);
+  if (threadIdx.x == 0) mbar_init_fence();
+  __syncthreads();
+  E edge[kStages] = {};
+  auto fetch = [&](int64_t r, int stage) {  // by the group's first warp
+    if (r >= a.rows || t >= 32) return;
+    const StagedRow<T> row(static_cast<const E*>(a.x) + r * a.x_stride, a.d);
+    if (t == 0) {
+      const uint32_t bar = smem_u32(&full[group * kStages + stage]);
+      mbar_expect_tx(bar, row.bytes);
+      row.copy(smem_u32(buffers + stage * pitch), bar);
+    }
+    if (!Wide && t < row.head + row.tail) edge[stage] = row.row[row.edge(t, a.d)];
+  };
+#pragma unroll
+  for (int stage = 0; stage < kStages; ++stage) fetch(first + stage * step, stage);
+  stage_weights<Wide>(sw, a, units, kLnThreads);
+  __syncthreads();
+  const float n = static_cast<float>(a.d);
+  auto meet = [&]() {
+    if (G == 1)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(L) : "memory");
+  };
+  auto group_sum = [&](float v, int which) {
+    v = warp_sum(v);
+    if (G == 1) return v;
+    if (t % 32 == 0) red[which][threadIdx.x / 32] = v;
+    meet();
+    float s = 0.0f;
+    for (int w = 0; w < G; ++w) s = __fadd_rn(s, red[which][group * G + w]);
+    return s;
+  };
+  bool ok = true;
+  uint32_t phase = 0;
+  for (int64_t r0 = first; r0 < a.rows; r0 += kStages * step, phase ^= 1) {
+#pragma unroll
+    for (int stage = 0; stage < kStages; ++stage) {
+      const int64_t r = r0 + stage * step;
+      if (r >= a.rows) break;
+      // a wait that gives up (only a fault can cause that) makes what follows NaN
+      ok = ok && mbar_wait(smem_u32(&full[group * kStages + stage]), phase);
+      const StagedRow<T> row(static_cast<const E*>(a.x) + r * a.x_stride, a.d);
+      E* data = reinterpret_cast<E*>(buffers + stage * pitch + (Wide ? 0 : row.offset));
+      if (!Wide) {
+        if (t < row.head + row.tail) data[row.edge(t, a.d)] = edge[stage];
+        meet();
+      }
+      Pack8<T> u[NV];
+#pragma unroll
+      for (int v = 0; v < NV; ++v) load_unit<T, Wide>(u[v], data, v, t, L, a.d);
+      float s = 0.0f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        float f[8];
+        u[v].get(f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = __fadd_rn(s, f[e]);  // elements past the row are 0
+      }
+      float mean = __fdiv_rn(group_sum(s, 0), n);
+      if (G == 1) __syncwarp();
+      if (ok) fetch(r + kStages * step, stage);  // every thread of the group has read the buffer
+      if (!ok) mean = __int_as_float(0x7FC00000);
+      float q = 0.0f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        float f[8];
+        u[v].get(f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (in_row<Wide>(v, e, t, L, a.d)) {
+            const float c = __fsub_rn(f[e], mean);
+            q = __fmaf_rn(c, c, q);
+          }
+      }
+      const float var = __fdiv_rn(group_sum(q, 1), n);
+      const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(var, a.eps)));
+      E* y = static_cast<E*>(a.y) + r * a.y_stride;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        if (!in_row<Wide>(v, 0, t, L, a.d)) continue;
+        normalise_unit<T, Wide>(u[v], sw, sw + 8 * units, mean, rstd, v, t, L, units, a.d);
+        store_unit<T, Wide>(u[v], y, v, t, L, a.d);
+      }
+      if (t == 0) {
+        if (a.mean_out) a.mean_out[r] = mean;
+        if (a.rstd_out) a.rstd_out[r] = rstd;
+      }
+    }
+  }
+  // copies in flight land before the block ends
+  if (!ok && t == 0)
+    for (int stage = 0; stage < kStages; ++stage) mbar_wait(smem_u32(&full[group * kStages + stage]), phase ^ 1);
 }
 
 // Rows longer than the registers hold: three passes over the row, the later
@@ -265,18 +412,61 @@ __device__ __forceinline__ int many_index(int lane) {
   return lane / (32 / N);
 }
 
-// Rows of up to 8 * NV * blockDim elements, R rows a round: the loads of the
-// next round are in flight while this one is reduced, with one barrier a
-// round (the warps' sums alternate between two buffers).
-template <int T, bool Wide, int NV, int R, int MaxThreads>
-__global__ void __launch_bounds__(MaxThreads) ln_backward_kernel(LnArgs a, float* part) {
+// Rows of up to 8 * NV * blockDim elements, R rows a round: a round's rows of x
+// and dy are staged two rounds ahead. One barrier a round joins the warps' sums
+// (which alternate between two buffers) and says that the stage has been read.
+// For 16-bit types xh is one FMA, x rstd - mean rstd: the second product's
+// rounding is below what the input's own rounding leaves of the difference.
+template <int T, bool Wide, int NV, int R>
+__global__ void __launch_bounds__(512) ln_backward_kernel(LnArgs a, float* part, uint32_t pitch) {
   pdl_enter();
   using E = typename Elem<T>::type;
   constexpr int N = 2 * R;
-  __shared__ float red[2][32][N];
+  __shared__ float red[2][16][N];
+  __shared__ float stats[kStages][N];  // mean and rstd of a stage's rows
+  __shared__ unsigned long long full[kStages];
+  extern __shared__ __align__(128) uint8_t smem[];
   const int t = threadIdx.x, L = blockDim.x, lane = t % 32, warp = t / 32, warps = L / 32;
   const float inv_d = __fdiv_rn(1.0f, static_cast<float>(a.d));
   const int64_t begin = a.rows * blockIdx.x / gridDim.x, end = a.rows * (blockIdx.x + 1) / gridDim.x;
+  if (t < kStages) mbar_init(smem_u32(&full[t]), 1);
+  if (t == 0) mbar_init_fence();
+  __syncthreads();
+  // buffer of row i of x (which = 0) or dy (1) in a stage
+  auto buffer = [&](int stage, int i, int which) { return smem + ((stage * R + i) * 2 + which) * pitch; };
+  auto source = [&](int64_t r, int which) {
+    return which ? static_cast<const E*>(a.dy) + r * a.dy_stride : static_cast<const E*>(a.x) + r * a.x_stride;
+  };
+  // Every thread of the first R warps holds an element that the copies leave
+  // out: of row t / 32, x or dy by t / 16, the t % 16-th. The first 2 R threads
+  // hold a mean or rstd, and put it into `stats` a round before its use.
+  E edge[kStages] = {};
+  float stat[kStages] = {};
+  auto fetch = [&](int64_t r0, int stage) {
+    if (r0 >= end) return;
+    if (t == 0) {
+      const uint32_t bar = smem_u32(&full[stage]);
+      uint32_t bytes = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (r0 + i / 2 < end) bytes += StagedRow<T>(source(r0 + i / 2, i % 2), a.d).bytes;
+      mbar_expect_tx(bar, bytes);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (r0 + i / 2 < end) StagedRow<T>(source(r0 + i / 2, i % 2), a.d).copy(smem_u32(buffer(stage, i / 2, i % 2)), bar);
+    }
+    if (!Wide && t < 32 * R && r0 + t / 32 < end) {
+      const StagedRow<T> row(source(r0 + t / 32, t / 16 % 2), a.d);
+      if (t % 16 < row.head + row.tail) edge[stage] = row.row[row.edge(t % 16, a.d)];
+    }
+    if (t < N) stat[stage] = r0 + t / 2 < end ? (t % 2 ? a.rstd : a.mean)[r0 + t / 2] : 0.0f;
+  };
+#pragma unroll
+  for (int stage = 0; stage < kStages; ++stage) {
+    fetch(begin + stage * R, stage);
+    if (t < N) stats[stage][t] = stat[stage];
+  }
+  __syncthreads();
   float w[NV][8], dw[NV][8], db[NV][8];
 #pragma unroll
   for (int v = 0; v < NV; ++v)
@@ -286,90 +476,95 @@ __global__ void __launch_bounds__(MaxThreads) ln_backward_kernel(LnArgs a, float
       w[v][e] = j < a.d ? (a.weight ? load_as(a.weight, j, a.weight_type) : 1.0f) : 0.0f;
       dw[v][e] = db[v][e] = 0.0f;
     }
-  Pack8<T> x[R][NV], g[R][NV];
-  float mean[R], rstd[R];
-  auto load = [&](int64_t r0) {
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int64_t r = r0 + i;
-      const bool live = r < end;
-      const int64_t n = live ? a.d : 0, at = live ? r : begin;
-      mean[i] = live ? a.mean[r] : 0.0f;
-      rstd[i] = live ? a.rstd[r] : 0.0f;
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        load_unit<T, Wide>(x[i][v], static_cast<const E*>(a.x) + at * a.x_stride, v, t, L, n);
-        load_unit<T, Wide>(g[i][v], static_cast<const E*>(a.dy) + at * a.dy_stride, v, t, L, n);
-      }
-    }
+  auto hat = [](float x, float mean, float rstd, float shift) {
+    return T == MP_FP32 ? __fmul_rn(__fsub_rn(x, mean), rstd) : __fmaf_rn(x, rstd, shift);
   };
-  if (begin < end) load(begin);
-  int buf = 0;
-  for (int64_t r0 = begin; r0 < end; r0 += R, buf ^= 1) {
-    Pack8<T> cx[R][NV], cg[R][NV];
-    float cm[R], cr[R], sums[N];
+  bool ok = true;
+  uint32_t phase = 0;
+  for (int64_t r1 = begin; r1 < end; r1 += kStages * R, phase ^= 1) {
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      cm[i] = mean[i];
-      cr[i] = rstd[i];
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        cx[i][v] = x[i][v];
-        cg[i][v] = g[i][v];
-      }
-    }
-    if (r0 + R < end) load(r0 + R);
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        float fx[8], fg[8];
-        cx[i][v].get(fx);
-        cg[i][v].get(fg);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float gw = __fmul_rn(fg[e], w[v][e]);  // 0 past the row
-          s1 = __fadd_rn(s1, gw);
-          s2 = __fmaf_rn(gw, __fmul_rn(__fsub_rn(fx[e], cm[i]), cr[i]), s2);
+    for (int stage = 0; stage < kStages; ++stage) {
+      const int64_t r0 = r1 + stage * R;
+      if (r0 >= end) break;
+      // a wait that gives up (only a fault can cause that) makes the sums NaN
+      ok = ok && mbar_wait(smem_u32(&full[stage]), phase);
+      if (!Wide) {
+        if (t < 32 * R && r0 + t / 32 < end) {
+          const StagedRow<T> row(source(r0 + t / 32, t / 16 % 2), a.d);
+          if (t % 16 < row.head + row.tail)
+            reinterpret_cast<E*>(buffer(stage, t / 32, t / 16 % 2) + row.offset)[row.edge(t % 16, a.d)] = edge[stage];
         }
+        __syncthreads();
       }
-      sums[2 * i] = s1;
-      sums[2 * i + 1] = s2;
-    }
-    const float mine = many_sum<N>(sums);
-    if (lane % (32 / N) == 0) red[buf][warp][many_index<N>(lane)] = mine;
-    __syncthreads();
-    float total = 0.0f;
-    for (int q = lane % (32 / N); q < warps; q += 32 / N) total = __fadd_rn(total, red[buf][q][many_index<N>(lane)]);
+      Pack8<T> x[R][NV], g[R][NV];
+      float mean[R], rstd[R], shift[R], sums[N];
 #pragma unroll
-    for (int o = 16 / N; o > 0; o >>= 1) total = __fadd_rn(total, __shfl_xor_sync(kAll, total, o));
-    total = __fmul_rn(total, inv_d);
+      for (int i = 0; i < R; ++i) {
+        mean[i] = stats[stage][2 * i];
+        rstd[i] = stats[stage][2 * i + 1];
+        shift[i] = -__fmul_rn(mean[i], rstd[i]);
+        const bool live = r0 + i < end;
+        const int64_t n = live ? a.d : 0;
+        const uint32_t ox = Wide || !live ? 0 : StagedRow<T>(source(r0 + i, 0), a.d).offset;
+        const uint32_t og = Wide || !live ? 0 : StagedRow<T>(source(r0 + i, 1), a.d).offset;
+        float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const float c1 = __shfl_sync(kAll, total, (2 * i) * (32 / N));
-      const float c2 = __shfl_sync(kAll, total, (2 * i + 1) * (32 / N));
+        for (int v = 0; v < NV; ++v) {
+          load_unit<T, Wide>(x[i][v], reinterpret_cast<const E*>(buffer(stage, i, 0) + ox), v, t, L, n);
+          load_unit<T, Wide>(g[i][v], reinterpret_cast<const E*>(buffer(stage, i, 1) + og), v, t, L, n);
+          float fx[8], fg[8];
+          x[i][v].get(fx);
+          g[i][v].get(fg);
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        float fx[8], fg[8], o[8];
-        cx[i][v].get(fx);
-        cg[i][v].get(fg);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float xh = __fmul_rn(__fsub_rn(fx[e], cm[i]), cr[i]);
-          const float gw = __fmul_rn(fg[e], w[v][e]);
-          o[e] = __fmul_rn(cr[i], __fmaf_rn(-xh, c2, __fsub_rn(gw, c1)));
-          dw[v][e] = __fmaf_rn(fg[e], xh, dw[v][e]);
-          db[v][e] = __fadd_rn(db[v][e], fg[e]);
+          for (int e = 0; e < 8; ++e) {
+            const float gw = __fmul_rn(fg[e], w[v][e]);  // 0 past the row
+            s1 = __fadd_rn(s1, gw);
+            s2 = __fmaf_rn(gw, hat(fx[e], mean[i], rstd[i], shift[i]), s2);
+          }
         }
-        if (a.y && r0 + i < end) {
-          Pack8<T> u;
-          u.put(o);
-          store_unit<T, Wide>(u, static_cast<E*>(a.y) + (r0 + i) * a.y_stride, v, t, L, a.d);
+        sums[2 * i] = ok ? s1 : __int_as_float(0x7FC00000);
+        sums[2 * i + 1] = s2;
+      }
+      const float mine = many_sum<N>(sums);
+      if (lane % (32 / N) == 0) red[stage][warp][many_index<N>(lane)] = mine;
+      if (t < N) stats[stage ^ 1][t] = stat[stage ^ 1];
+      __syncthreads();
+      if (ok) fetch(r0 + kStages * R, stage);
+      float total = 0.0f;
+      for (int q = lane % (32 / N); q < warps; q += 32 / N)
+        total = __fadd_rn(total, red[stage][q][many_index<N>(lane)]);
+#pragma unroll
+      for (int o = 16 / N; o > 0; o >>= 1) total = __fadd_rn(total, __shfl_xor_sync(kAll, total, o));
+      total = __fmul_rn(total, inv_d);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        // dx = g rstd + (xh (-c2 rstd) - c1 rstd)
+        const float c1 = -__fmul_rn(__shfl_sync(kAll, total, (2 * i) * (32 / N)), rstd[i]);
+        const float c2 = -__fmul_rn(__shfl_sync(kAll, total, (2 * i + 1) * (32 / N)), rstd[i]);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          float fx[8], fg[8], o[8];
+          x[i][v].get(fx);
+          g[i][v].get(fg);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float xh = hat(fx[e], mean[i], rstd[i], shift[i]);
+            o[e] = __fmaf_rn(__fmul_rn(fg[e], w[v][e]), rstd[i], __fmaf_rn(xh, c2, c1));
+            dw[v][e] = __fmaf_rn(fg[e], xh, dw[v][e]);
+            db[v][e] = __fadd_rn(db[v][e], fg[e]);
+          }
+          if (a.y && r0 + i < end) {
+            Pack8<T> u;
+            u.put(o);
+            store_unit<T, Wide>(u, static_cast<E*>(a.y) + (r0 + i) * a.y_stride, v, t, L, a.d);
+          }
         }
       }
     }
   }
+  // copies in flight land before the block ends
+  if (!ok && t == 0)
+    for (int stage = 0; stage < kStages; ++stage) mbar_wait(smem_u32(&full[stage]), phase ^ 1);
   if (!part) return;
   float* pw = part + static_cast<int64_t>(blockIdx.x) * 2 * a.d;
 #pragma unroll
@@ -378,7 +573,7 @@ __global__ void __launch_bounds__(MaxThreads) ln_backward_kernel(LnArgs a, float
     for (int e = 0; e < 8; ++e)
       if (in_row<Wide>(v, e, t, L, a.d)) {
         const int64_t j = column<Wide>(v, e, t, L);
-        pw[j] = dw[v][e];
+        pw[j] = ok ? dw[v][e] : __int_as_float(0x7FC00000);
         pw[a.d + j] = db[v][e];
       }
 }
@@ -537,6 +732,9 @@ __global__ void __launch_bounds__(32 * kFinishSlices) ln_finish_kernel(void* dwe
 // workspace's size follow from rows and d alone.
 constexpr int64_t kSms = 152;
 
+constexpr int kLnShared = 227 * 1024;  // an SM's shared memory for blocks
+constexpr int64_t kStagedD = 8192;     // longer rows take the long kernels
+
 struct LnPlan {
   int threads, parts;
 };
@@ -550,7 +748,7 @@ LnPlan backward_plan(int64_t rows, int64_t d) {
     const int lanes = d <= 64 ? 8 : d <= 128 ? 16 : 32;
     per_block = kLnThreads / lanes;
     blocks_per_sm = 4;
-  } else if (d <= 8192) {
+  } else if (d <= kStagedD) {
     const int64_t units = (d + 7) / 8;
     const int64_t nv = units > 512 ? 2 : 1;
     p.threads = static_cast<int>((units + 32 * nv - 1) / (32 * nv) * 32);
@@ -561,37 +759,54 @@ LnPlan backward_plan(int64_t rows, int64_t d) {
     per_block = 32;
     blocks_per_sm = 1;
   }
-  const int64_t cap = d <= 8192 ? blocks_per_sm * kSms : 64;
+  const int64_t cap = d <= kStagedD ? blocks_per_sm * kSms : 64;
   p.parts = static_cast<int>(std::max<int64_t>(1, std::min(cap, (rows + per_block - 1) / per_block)));
   return p;
 }
 
-template <int T, bool Wide, int L, int NV>
-cudaError_t launch_forward(const LnArgs& a, const DeviceInfo& dev, cudaStream_t s) {
+template <int T, bool Wide, int L>
+cudaError_t forward_short(const LnArgs& a, const DeviceInfo& dev, cudaStream_t s) {
+  const int64_t per_block = kLnThreads / L * (T == MP_FP32 ? 2 : 4);
+  const int64_t blocks = std::min<int64_t>((a.rows + per_block - 1) / per_block, 4 * dev.sms);
+  return launch_pdl_smem(ln_forward_short_kernel<T, Wide, L>, static_cast<unsigned>(blocks), kLnThreads,
+                         (a.d + 7) / 8 * 64, s, a);
+}
+
+template <int T, bool Wide, int NV>
+cudaError_t forward_staged(const LnArgs& a, int G, const DeviceInfo& dev, cudaStream_t s) {
   static std::atomic<bool> ready[64];
-  const size_t smem = (a.d + 7) / 8 * 64;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = allow_shared(ln_forward_kernel<T, Wide, L, NV>, 64 * 1024, ready);
-    if (e != cudaSuccess) return e;
-  }
-  const int64_t per_block = kLnThreads / L;
-  const int64_t blocks = std::min<int64_t>((a.rows + per_block - 1) / per_block, (NV >= 8 ? 3 : 4) * dev.sms);
-  return launch_pdl_smem(ln_forward_kernel<T, Wide, L, NV>, static_cast<unsigned>(blocks), kLnThreads, smem, s, a);
+  const int64_t groups = 8 / G;
+  const uint32_t pitch = staged_pitch(a.d, T);
+  const size_t smem = (a.d + 7) / 8 * 64 + groups * kStages * pitch;
+  const cudaError_t e = allow_shared(ln_forward_kernel<T, Wide, NV>, kLnShared - 4096, ready);
+  if (e != cudaSuccess) return e;
+  const int64_t per_sm = std::max<int64_t>(1, std::min<int64_t>(NV >= 8 ? 2 : NV >= 4 ? 3 : 4, kLnShared / (smem + 2048)));
+  const int64_t blocks = std::min((a.rows + groups - 1) / groups, per_sm * dev.sms);
+  return launch_pdl_smem(ln_forward_kernel<T, Wide, NV>, static_cast<unsigned>(blocks), kLnThreads, smem, s, a, G,
+                         pitch);
 }
 
 template <int T, bool Wide>
 cudaError_t forward_wide(const LnArgs& a, const DeviceInfo& dev, cudaStream_t s) {
-  if (a.d <= 64) return launch_forward<T, Wide, 8, 1>(a, dev, s);
-  if (a.d <= 128) return launch_forward<T, Wide, 16, 1>(a, dev, s);
-  if (a.d <= 256) return launch_forward<T, Wide, 32, 1>(a, dev, s);
-  if (a.d <= 512) return launch_forward<T, Wide, 32, 2>(a, dev, s);
-  if (a.d <= 1024) return launch_forward<T, Wide, 32, 4>(a, dev, s);
-  if (Wide && a.d <= 2048) return launch_forward<T, Wide, 32, 8>(a, dev, s);
-  if (a.d <= 2048) return launch_forward<T, Wide, 256, 1>(a, dev, s);
-  if (a.d <= 4096) return launch_forward<T, Wide, 256, 2>(a, dev, s);
-  if (a.d <= 8192) return launch_forward<T, Wide, 256, 4>(a, dev, s);
-  return launch_pdl(ln_forward_long_kernel<T>, static_cast<unsigned>(std::min<int64_t>(a.rows, 8 * dev.sms)),
-                    kLnThreads, s, a);
+  if (a.d > kStagedD)
+    return launch_pdl(ln_forward_long_kernel<T>, static_cast<unsigned>(std::min<int64_t>(a.rows, 8 * dev.sms)),
+                      kLnThreads, s, a);
+  if (a.d <= 64) return forward_short<T, Wide, 8>(a, dev, s);
+  if (a.d <= 128) return forward_short<T, Wide, 16>(a, dev, s);
+  if (a.d <= 256) return forward_short<T, Wide, 32>(a, dev, s);
+  // Warps of a row: few enough that the units fit the registers (8 a thread
+  // of aligned 16-bit rows, 4 of others), more where there are too few rows to fill
+  // the GPU with as many warps.
+  constexpr int kMost = T == MP_FP32 || !Wide ? 4 : 8;
+  const int64_t units = (a.d + 7) / 8;
+  int G = 1;
+  while (G < 8 && (units > 32 * G * kMost || (a.rows * G < 8 * dev.sms && units > 32 * G))) G *= 2;
+  const int64_t nv = (units + 32 * G - 1) / (32 * G);
+  if (nv == 1) return forward_staged<T, Wide, 1>(a, G, dev, s);
+  if (nv == 2) return forward_staged<T, Wide, 2>(a, G, dev, s);
+  if (nv <= 4) return forward_staged<T, Wide, 4>(a, G, dev, s);
+  if constexpr (kMost == 8) return forward_staged<T, Wide, 8>(a, G, dev, s);
+  return cudaErrorInvalidValue;  // not reached: 8 warps of 4 units hold kStagedD
 }
 
 template <int T>
@@ -600,15 +815,29 @@ cudaError_t forward(const LnArgs& a, const DeviceInfo& dev, cudaStream_t s) {
   return wide ? forward_wide<T, true>(a, dev, s) : forward_wide<T, false>(a, dev, s);
 }
 
+template <int T, bool Wide, int NV, int R>
+cudaError_t backward_staged(const LnArgs& a, const LnPlan& p, float* part, uint32_t pitch, cudaStream_t s) {
+  static std::atomic<bool> ready[64];
+  const cudaError_t e = allow_shared(ln_backward_kernel<T, Wide, NV, R>, kLnShared - 4096, ready);
+  if (e != cudaSuccess) return e;
+  return launch_pdl_smem(ln_backward_kernel<T, Wide, NV, R>, static_cast<unsigned>(p.parts),
+                         static_cast<unsigned>(p.threads), static_cast<size_t>(kStages) * 2 * R * pitch, s, a, part,
+                         pitch);
+}
+
 template <int T, bool Wide>
 cudaError_t backward_wide(const LnArgs& a, const LnPlan& p, float* part, cudaStream_t s) {
   const unsigned grid = static_cast<unsigned>(p.parts), threads = static_cast<unsigned>(p.threads);
   if (a.d <= 64) return launch_pdl(ln_backward_short_kernel<T, Wide, 8>, grid, threads, s, a, part);
   if (a.d <= 128) return launch_pdl(ln_backward_short_kernel<T, Wide, 16>, grid, threads, s, a, part);
   if (a.d <= 256) return launch_pdl(ln_backward_short_kernel<T, Wide, 32>, grid, threads, s, a, part);
-  constexpr int R = T == MP_FP32 ? 2 : 4;
-  if (a.d <= 4096) return launch_pdl(ln_backward_kernel<T, Wide, 1, R, 512>, grid, threads, s, a, part);
-  return launch_pdl(ln_backward_kernel<T, Wide, 2, 1, 512>, grid, threads, s, a, part);
+  // Rows a round: as many as the registers hold, one for each of the first
+  // warps (which hold the elements between the copies).
+  const uint32_t pitch = staged_pitch(a.d, T);
+  if (a.d > 4096) return backward_staged<T, Wide, 2, 1>(a, p, part, pitch, s);
+  if (T == MP_FP32 || p.threads < 128) return backward_staged<T, Wide, 1, 2>(a, p, part, pitch, s);
+  if constexpr (T != MP_FP32) return backward_staged<T, Wide, 1, 4>(a, p, part, pitch, s);
+  return cudaErrorInvalidValue;  // not reached
 }
 
 template <int T>
@@ -618,7 +847,7 @@ cudaError_t backward(const LnArgs& a, void* dweight, void* dbias, float* part, c
   const LnPlan p = backward_plan(a.rows, a.d);
   const int64_t strips = (a.d + kLnThreads - 1) / kLnThreads;
   cudaError_t e = cudaSuccess;
-  if (a.d <= 8192) {
+  if (a.d <= kStagedD) {
     if (a.rows || sums) {
       const bool wide = wide_rows(a.x, a.d, a.x_stride, a.rows, T) && wide_rows(a.dy, a.d, a.dy_stride, a.rows, T) &&
                         (!a.y || wide_rows(a.y, a.d, a.y_stride, a.rows, T));
