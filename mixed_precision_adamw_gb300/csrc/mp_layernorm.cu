@@ -96,7 +96,7 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 // fewer than 8 elements before and after them (rows that do not start or end on
 // a 16-B boundary) are loaded by threads and put beside them. A row lies in its
 // buffer at the offset that its address has from a 16-B boundary.
-template <int T>
+template <int T, bool Wide>
 struct StagedRow {
   using E = typename Elem<T>::type;
   const E* row;
@@ -106,6 +106,12 @@ struct StagedRow {
 
   __device__ __forceinline__ StagedRow(const E* p, int64_t d) : row(p) {
     constexpr int kAlign = 16 / sizeof(E);
+    if (Wide) {
+      offset = 0;
+      head = tail = 0;
+      bytes = static_cast<uint32_t>(d) * sizeof(E);
+      return;
+    }
     const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) / sizeof(E) % kAlign);
     offset = off * sizeof(E);
     head = off ? kAlign - off : 0;
@@ -122,7 +128,8 @@ struct StagedRow {
   }
 };
 
-constexpr int kStages = 2;
+constexpr int kStages = 2;      // of the forward pass
+constexpr int kMaxStages = 4;   // of the backward pass
 
 // Bytes of a row's buffer.
 inline uint32_t staged_pitch(int64_t d, int type) {
@@ -249,19 +256,19 @@ __global__ void __launch_bounds__(kLnThreads, NV >= 8 ? 2 : NV >= 4 ? 3 : 4) ln_
   if (threadIdx.x < kStages * count) mbar_init(smem_u32(&full[threadIdx.x]), 1);
   if (threadIdx.x == 0) mbar_init_fence();
   __syncthreads();
-  E edge[kStages] = {};
+  E edge0 = {}, edge1 = {};  // of the two stages
   auto fetch = [&](int64_t r, int stage) {  // by the group's first warp
     if (r >= a.rows || t >= 32) return;
-    const StagedRow<T> row(static_cast<const E*>(a.x) + r * a.x_stride, a.d);
+    const StagedRow<T, Wide> row(static_cast<const E*>(a.x) + r * a.x_stride, a.d);
     if (t == 0) {
       const uint32_t bar = smem_u32(&full[group * kStages + stage]);
       mbar_expect_tx(bar, row.bytes);
       row.copy(smem_u32(buffers + stage * pitch), bar);
     }
-    if (!Wide && t < row.head + row.tail) edge[stage] = row.row[row.edge(t, a.d)];
+    if (!Wide && t < row.head + row.tail) (stage ? edge1 : edge0) = row.row[row.edge(t, a.d)];
   };
-#pragma unroll
-  for (int stage = 0; stage < kStages; ++stage) fetch(first + stage * step, stage);
+  fetch(first, 0);
+  fetch(first + step, 1);
   stage_weights<Wide>(sw, a, units, kLnThreads);
   __syncthreads();
   const float n = static_cast<float>(a.d);
@@ -281,18 +288,18 @@ __global__ void __launch_bounds__(kLnThreads, NV >= 8 ? 2 : NV >= 4 ? 3 : 4) ln_
     return s;
   };
   bool ok = true;
-  uint32_t phase = 0;
-  for (int64_t r0 = first; r0 < a.rows; r0 += kStages * step, phase ^= 1) {
-#pragma unroll
-    for (int stage = 0; stage < kStages; ++stage) {
-      const int64_t r = r0 + stage * step;
-      if (r >= a.rows) break;
+  uint32_t stage = 0, phase = 0;
+  // One copy of the body: with the stages unrolled the loop outgrows the
+  // instruction caches (32768 x 1600 bf16: 43 us twice over, 82 us four times).
+#pragma unroll 1
+  for (int64_t r = first; r < a.rows; r += step, phase ^= stage, stage ^= 1) {
+    {
       // a wait that gives up (only a fault can cause that) makes what follows NaN
       ok = ok && mbar_wait(smem_u32(&full[group * kStages + stage]), phase);
-      const StagedRow<T> row(static_cast<const E*>(a.x) + r * a.x_stride, a.d);
+      const StagedRow<T, Wide> row(static_cast<const E*>(a.x) + r * a.x_stride, a.d);
       E* data = reinterpret_cast<E*>(buffers + stage * pitch + (Wide ? 0 : row.offset));
       if (!Wide) {
-        if (t < row.head + row.tail) data[row.edge(t, a.d)] = edge[stage];
+        if (t < row.head + row.tail) data[row.edge(t, a.d)] = stage ? edge1 : edge0;
         meet();
       }
       Pack8<T> u[NV];
@@ -339,7 +346,7 @@ __global__ void __launch_bounds__(kLnThreads, NV >= 8 ? 2 : NV >= 4 ? 3 : 4) ln_
   }
   // copies in flight land before the block ends
   if (!ok && t == 0)
-    for (int stage = 0; stage < kStages; ++stage) mbar_wait(smem_u32(&full[group * kStages + stage]), phase ^ 1);
+    for (int i = 0; i < kStages; ++i) mbar_wait(smem_u32(&full[group * kStages + i]), phase ^ 1);
 }
 
 // Rows longer than the registers hold: three passes over the row, the later
@@ -412,24 +419,33 @@ __device__ __forceinline__ int many_index(int lane) {
   return lane / (32 / N);
 }
 
-// Rows of up to 8 * NV * blockDim elements, R rows a round: a round's rows of x
-// and dy are staged two rounds ahead. One barrier a round joins the warps' sums
-// (which alternate between two buffers) and says that the stage has been read.
-// For 16-bit types xh is one FMA, x rstd - mean rstd: the second product's
-// rounding is below what the input's own rounding leaves of the difference.
-template <int T, bool Wide, int NV, int R>
-__global__ void __launch_bounds__(512) ln_backward_kernel(LnArgs a, float* part, uint32_t pitch) {
+// Rows of up to 8 * NV * L elements for the block's L computing threads, R rows
+// a round. The last warp stages the rounds' rows of x and dy, their mean and
+// rstd and the elements that the copies leave out, as stages become free; what
+// it takes to prepare a copy (hundreds of cycles) is off the others' path. One
+// barrier a round joins the computing warps' sums (which alternate between two
+// buffers) and says that the stage has been read. xh and dy stay in registers,
+// widened, from the sums to dx. For 16-bit types xh is one FMA, x rstd -
+// mean rstd: the second product's rounding is below what the input's own
+// rounding leaves of the difference. Rows past the block's last are staged as
+// zeros instead of being tested for.
+template <int T, bool Wide, int NV, int R, int MaxThreads, int MinBlocks>
+__global__ void __launch_bounds__(MaxThreads + 32, MinBlocks)
+ln_backward_kernel(LnArgs a, float* part, uint32_t pitch, int stages) {
   pdl_enter();
   using E = typename Elem<T>::type;
   constexpr int N = 2 * R;
   __shared__ float red[2][16][N];
-  __shared__ float stats[kStages][N];  // mean and rstd of a stage's rows
-  __shared__ unsigned long long full[kStages];
+  __shared__ float stats[kMaxStages][N];  // mean and rstd of a stage's rows
+  __shared__ unsigned long long full[kMaxStages], freed[kMaxStages];
   extern __shared__ __align__(128) uint8_t smem[];
-  const int t = threadIdx.x, L = blockDim.x, lane = t % 32, warp = t / 32, warps = L / 32;
-  const float inv_d = __fdiv_rn(1.0f, static_cast<float>(a.d));
+  const int t = threadIdx.x, L = blockDim.x - 32, lane = t % 32, warp = t / 32, warps = L / 32;
   const int64_t begin = a.rows * blockIdx.x / gridDim.x, end = a.rows * (blockIdx.x + 1) / gridDim.x;
-  if (t < kStages) mbar_init(smem_u32(&full[t]), 1);
+  const int rounds = static_cast<int>((end - begin + R - 1) / R);
+  if (t < stages) {
+    mbar_init(smem_u32(&full[t]), 1);
+    mbar_init(smem_u32(&freed[t]), 1);
+  }
   if (t == 0) mbar_init_fence();
   __syncthreads();
   // buffer of row i of x (which = 0) or dy (1) in a stage
@@ -437,134 +453,166 @@ __global__ void __launch_bounds__(512) ln_backward_kernel(LnArgs a, float* part,
   auto source = [&](int64_t r, int which) {
     return which ? static_cast<const E*>(a.dy) + r * a.dy_stride : static_cast<const E*>(a.x) + r * a.x_stride;
   };
-  // Every thread of the first R warps holds an element that the copies leave
-  // out: of row t / 32, x or dy by t / 16, the t % 16-th. The first 2 R threads
-  // hold a mean or rstd, and put it into `stats` a round before its use.
-  E edge[kStages] = {};
-  float stat[kStages] = {};
-  auto fetch = [&](int64_t r0, int stage) {
-    if (r0 >= end) return;
-    if (t == 0) {
+  if (warp == warps) {  // the staging warp
+    // Lane l < N holds row l / 2's mean or rstd of the next round; each lane
+    // the element (l % 16) of x (l < 16) or dy that the copies of each row leave out.
+    float stat = 0.0f;
+    E edge[R] = {};
+    auto ahead = [&](int round) {
+      const int64_t r0 = begin + static_cast<int64_t>(round) * R;
+      if (lane < N) stat = r0 + lane / 2 < end ? (lane % 2 ? a.rstd : a.mean)[r0 + lane / 2] : 0.0f;
+      if (!Wide)
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          if (r0 + i < end) {
+            const StagedRow<T, Wide> row(source(r0 + i, lane / 16), a.d);
+            if (lane % 16 < row.head + row.tail) edge[i] = row.row[row.edge(lane % 16, a.d)];
+          }
+    };
+    if (rounds) ahead(0);
+    int stage = 0;
+    uint32_t phase = 1;
+    bool ok = true;
+    int round = 0;
+    for (; round < rounds; ++round) {
+      const int64_t r0 = begin + static_cast<int64_t>(round) * R;
+      ok = round < stages || __all_sync(kAll, mbar_wait(smem_u32(&freed[stage]), phase));
+      if (!ok) break;
       const uint32_t bar = smem_u32(&full[stage]);
-      uint32_t bytes = 0;
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (r0 + i / 2 < end) bytes += StagedRow<T>(source(r0 + i / 2, i % 2), a.d).bytes;
-      mbar_expect_tx(bar, bytes);
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (r0 + i / 2 < end) StagedRow<T>(source(r0 + i / 2, i % 2), a.d).copy(smem_u32(buffer(stage, i / 2, i % 2)), bar);
+      for (int i = 0; i < R; ++i) {
+        if (r0 + i < end) {
+          const StagedRow<T, Wide> x(source(r0 + i, 0), a.d), dy(source(r0 + i, 1), a.d);
+          if (lane == 0) {
+            mbar_more_tx(bar, x.bytes + dy.bytes);
+            x.copy(smem_u32(buffer(stage, i, 0)), bar);
+            dy.copy(smem_u32(buffer(stage, i, 1)), bar);
+          }
+          if (!Wide) {
+            const StagedRow<T, Wide>& row = lane < 16 ? x : dy;
+            if (lane % 16 < row.head + row.tail)
+              reinterpret_cast<E*>(buffer(stage, i, lane / 16) + row.offset)[row.edge(lane % 16, a.d)] = edge[i];
+          }
+        } else {
+          for (uint32_t k = lane; k < 2 * pitch / 16; k += 32)
+            reinterpret_cast<uint4*>(buffer(stage, i, 0))[k] = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+      if (lane < N) stats[stage][lane] = stat;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+      if (round + 1 < rounds) ahead(round + 1);
+      if (++stage == stages) {
+        stage = 0;
+        phase ^= 1;
+      }
     }
-    if (!Wide && t < 32 * R && r0 + t / 32 < end) {
-      const StagedRow<T> row(source(r0 + t / 32, t / 16 % 2), a.d);
-      if (t % 16 < row.head + row.tail) edge[stage] = row.row[row.edge(t % 16, a.d)];
-    }
-    if (t < N) stat[stage] = r0 + t / 2 < end ? (t % 2 ? a.rstd : a.mean)[r0 + t / 2] : 0.0f;
-  };
-#pragma unroll
-  for (int stage = 0; stage < kStages; ++stage) {
-    fetch(begin + stage * R, stage);
-    if (t < N) stats[stage][t] = stat[stage];
+    // copies in flight land before the block ends
+    if (lane == 0)
+      for (int i = max(0, round - stages); i < round; ++i) mbar_wait(smem_u32(&full[i % stages]), (i / stages) & 1);
+    return;
   }
-  __syncthreads();
-  float w[NV][8], dw[NV][8], db[NV][8];
+  const float inv_d = __fdiv_rn(1.0f, static_cast<float>(a.d));
+  float w[NV][8], dw[NV][8], db[NV][8], xh[R][NV][8], g[R][NV][8];
+  bool mine[NV];
 #pragma unroll
-  for (int v = 0; v < NV; ++v)
+  for (int v = 0; v < NV; ++v) {
+    mine[v] = in_row<Wide>(v, 0, t, L, a.d);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int64_t j = column<Wide>(v, e, t, L);
       w[v][e] = j < a.d ? (a.weight ? load_as(a.weight, j, a.weight_type) : 1.0f) : 0.0f;
       dw[v][e] = db[v][e] = 0.0f;
-    }
-  auto hat = [](float x, float mean, float rstd, float shift) {
-    return T == MP_FP32 ? __fmul_rn(__fsub_rn(x, mean), rstd) : __fmaf_rn(x, rstd, shift);
-  };
-  bool ok = true;
-  uint32_t phase = 0;
-  for (int64_t r1 = begin; r1 < end; r1 += kStages * R, phase ^= 1) {
 #pragma unroll
-    for (int stage = 0; stage < kStages; ++stage) {
-      const int64_t r0 = r1 + stage * R;
-      if (r0 >= end) break;
-      // a wait that gives up (only a fault can cause that) makes the sums NaN
-      ok = ok && mbar_wait(smem_u32(&full[stage]), phase);
-      if (!Wide) {
-        if (t < 32 * R && r0 + t / 32 < end) {
-          const StagedRow<T> row(source(r0 + t / 32, t / 16 % 2), a.d);
-          if (t % 16 < row.head + row.tail)
-            reinterpret_cast<E*>(buffer(stage, t / 32, t / 16 % 2) + row.offset)[row.edge(t % 16, a.d)] = edge[stage];
-        }
-        __syncthreads();
-      }
-      Pack8<T> x[R][NV], g[R][NV];
-      float mean[R], rstd[R], shift[R], sums[N];
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        mean[i] = stats[stage][2 * i];
-        rstd[i] = stats[stage][2 * i + 1];
-        shift[i] = -__fmul_rn(mean[i], rstd[i]);
-        const bool live = r0 + i < end;
-        const int64_t n = live ? a.d : 0;
-        const uint32_t ox = Wide || !live ? 0 : StagedRow<T>(source(r0 + i, 0), a.d).offset;
-        const uint32_t og = Wide || !live ? 0 : StagedRow<T>(source(r0 + i, 1), a.d).offset;
-        float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          load_unit<T, Wide>(x[i][v], reinterpret_cast<const E*>(buffer(stage, i, 0) + ox), v, t, L, n);
-          load_unit<T, Wide>(g[i][v], reinterpret_cast<const E*>(buffer(stage, i, 1) + og), v, t, L, n);
-          float fx[8], fg[8];
-          x[i][v].get(fx);
-          g[i][v].get(fg);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float gw = __fmul_rn(fg[e], w[v][e]);  // 0 past the row
-            s1 = __fadd_rn(s1, gw);
-            s2 = __fmaf_rn(gw, hat(fx[e], mean[i], rstd[i], shift[i]), s2);
-          }
-        }
-        sums[2 * i] = ok ? s1 : __int_as_float(0x7FC00000);
-        sums[2 * i + 1] = s2;
-      }
-      const float mine = many_sum<N>(sums);
-      if (lane % (32 / N) == 0) red[stage][warp][many_index<N>(lane)] = mine;
-      if (t < N) stats[stage ^ 1][t] = stat[stage ^ 1];
-      __syncthreads();
-      if (ok) fetch(r0 + kStages * R, stage);
-      float total = 0.0f;
-      for (int q = lane % (32 / N); q < warps; q += 32 / N)
-        total = __fadd_rn(total, red[stage][q][many_index<N>(lane)]);
-#pragma unroll
-      for (int o = 16 / N; o > 0; o >>= 1) total = __fadd_rn(total, __shfl_xor_sync(kAll, total, o));
-      total = __fmul_rn(total, inv_d);
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        // dx = g rstd + (xh (-c2 rstd) - c1 rstd)
-        const float c1 = -__fmul_rn(__shfl_sync(kAll, total, (2 * i) * (32 / N)), rstd[i]);
-        const float c2 = -__fmul_rn(__shfl_sync(kAll, total, (2 * i + 1) * (32 / N)), rstd[i]);
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          float fx[8], fg[8], o[8];
-          x[i][v].get(fx);
-          g[i][v].get(fg);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float xh = hat(fx[e], mean[i], rstd[i], shift[i]);
-            o[e] = __fmaf_rn(__fmul_rn(fg[e], w[v][e]), rstd[i], __fmaf_rn(xh, c2, c1));
-            dw[v][e] = __fmaf_rn(fg[e], xh, dw[v][e]);
-            db[v][e] = __fadd_rn(db[v][e], fg[e]);
-          }
-          if (a.y && r0 + i < end) {
-            Pack8<T> u;
-            u.put(o);
-            store_unit<T, Wide>(u, static_cast<E*>(a.y) + (r0 + i) * a.y_stride, v, t, L, a.d);
-          }
-        }
-      }
+      for (int i = 0; i < R; ++i) xh[i][v][e] = g[i][v][e] = 0.0f;  // stays so past the row
     }
   }
-  // copies in flight land before the block ends
-  if (!ok && t == 0)
-    for (int stage = 0; stage < kStages; ++stage) mbar_wait(smem_u32(&full[stage]), phase ^ 1);
+  E* out = a.y ? static_cast<E*>(a.y) + begin * a.y_stride + (Wide ? 8 * t : 0) : nullptr;
+  bool ok = true;
+  int stage = 0;
+  uint32_t phase = 0;
+  // one copy of the body, as in the forward pass
+#pragma unroll 1
+  for (int round = 0; round < rounds; ++round) {
+    const int64_t r0 = begin + static_cast<int64_t>(round) * R;
+    // a wait that gives up (only a fault can cause that) makes the sums NaN
+    ok = ok && mbar_wait(smem_u32(&full[stage]), phase);
+    float rstd[R], sums[N];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const E* x = reinterpret_cast<const E*>(buffer(stage, i, 0));
+      const E* dy = reinterpret_cast<const E*>(buffer(stage, i, 1));
+      if (!Wide && r0 + i < end) {
+        x += StagedRow<T, Wide>(source(r0 + i, 0), a.d).offset / sizeof(E);
+        dy += StagedRow<T, Wide>(source(r0 + i, 1), a.d).offset / sizeof(E);
+      }
+      const float mean = stats[stage][2 * i];
+      rstd[i] = stats[stage][2 * i + 1];
+      const float shift = -__fmul_rn(mean, rstd[i]);
+      float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        if (mine[v]) {
+          Pack8<T> u;
+          float f[8];
+          load_unit<T, Wide>(u, dy, v, t, L, a.d);
+          u.get(g[i][v]);
+          load_unit<T, Wide>(u, x, v, t, L, a.d);
+          u.get(f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            xh[i][v][e] = T == MP_FP32 ? __fmul_rn(__fsub_rn(f[e], mean), rstd[i]) : __fmaf_rn(f[e], rstd[i], shift);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float gw = __fmul_rn(g[i][v][e], w[v][e]);  // 0 past the row
+          s1 = __fadd_rn(s1, gw);
+          s2 = __fmaf_rn(gw, xh[i][v][e], s2);
+        }
+      }
+      sums[2 * i] = ok ? s1 : __int_as_float(0x7FC00000);
+      sums[2 * i + 1] = s2;
+    }
+    const float part_sum = many_sum<N>(sums);
+    if (lane % (32 / N) == 0) red[round & 1][warp][many_index<N>(lane)] = part_sum;
+    asm volatile("bar.sync 1, %0;" ::"r"(L) : "memory");
+    if (t == 0) mbar_arrive(smem_u32(&freed[stage]));
+    float total = 0.0f;
+    for (int q = lane % (32 / N); q < warps; q += 32 / N)
+      total = __fadd_rn(total, red[round & 1][q][many_index<N>(lane)]);
+#pragma unroll
+    for (int o = 16 / N; o > 0; o >>= 1) total = __fadd_rn(total, __shfl_xor_sync(kAll, total, o));
+    total = __fmul_rn(total, inv_d);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      // dx = g rstd + (xh (-c2 rstd) - c1 rstd)
+      const float c1 = -__fmul_rn(__shfl_sync(kAll, total, (2 * i) * (32 / N)), rstd[i]);
+      const float c2 = -__fmul_rn(__shfl_sync(kAll, total, (2 * i + 1) * (32 / N)), rstd[i]);
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        float o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          o[e] = __fmaf_rn(__fmul_rn(g[i][v][e], w[v][e]), rstd[i], __fmaf_rn(xh[i][v][e], c2, c1));
+          dw[v][e] = __fmaf_rn(g[i][v][e], xh[i][v][e], dw[v][e]);
+          db[v][e] = __fadd_rn(db[v][e], g[i][v][e]);
+        }
+        if (mine[v] && out && r0 + i < end) {
+          Pack8<T> u;
+          u.put(o);
+          if (Wide)
+            u.store(out + v * 8 * L);
+          else
+            store_unit<T, Wide>(u, out, v, t, L, a.d);
+        }
+      }
+      if (out) out += a.y_stride;
+    }
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
   if (!part) return;
   float* pw = part + static_cast<int64_t>(blockIdx.x) * 2 * a.d;
 #pragma unroll
@@ -695,9 +743,9 @@ __global__ void __launch_bounds__(kLnThreads) ln_dw_long_kernel(LnArgs a, float*
   part[(c * 2 + 1) * a.d + j] = sb;
 }
 
-// dweight and dbias from `parts` blocks' sums: 32 columns a block, 16 threads
-// a column, each adding every 16th block's sum.
-constexpr int kFinishSlices = 16;
+// dweight and dbias from `parts` blocks' sums: 32 columns a block, 32 threads
+// a column, each adding every 32nd block's sum.
+constexpr int kFinishSlices = 32;
 
 __global__ void __launch_bounds__(32 * kFinishSlices) ln_finish_kernel(void* dweight, void* dbias, const float* part,
                                                                        int64_t d, int parts, int weight_type) {
@@ -736,30 +784,23 @@ constexpr int kLnShared = 227 * 1024;  // an SM's shared memory for blocks
 constexpr int64_t kStagedD = 8192;     // longer rows take the long kernels
 
 struct LnPlan {
-  int threads, parts;
+  int threads, parts, units, per_sm;  // threads that compute, units a thread
 };
 
 LnPlan backward_plan(int64_t rows, int64_t d) {
-  LnPlan p;
-  int64_t per_block;  // rows that make a further block worth its partial sum
-  int blocks_per_sm;
+  LnPlan p = {kLnThreads, 0, 1, 1};
+  int64_t per_block = 32, cap = 64;  // rows that make a further block worth its partial sum; blocks
   if (d <= 256) {
-    p.threads = kLnThreads;
-    const int lanes = d <= 64 ? 8 : d <= 128 ? 16 : 32;
-    per_block = kLnThreads / lanes;
-    blocks_per_sm = 4;
+    per_block = kLnThreads / (d <= 64 ? 8 : d <= 128 ? 16 : 32);
+    cap = 4 * kSms;
   } else if (d <= kStagedD) {
     const int64_t units = (d + 7) / 8;
-    const int64_t nv = units > 512 ? 2 : 1;
-    p.threads = static_cast<int>((units + 32 * nv - 1) / (32 * nv) * 32);
+    p.units = d > 4096 ? 2 : 1;
+    p.threads = static_cast<int>((units + 32 * p.units - 1) / (32 * p.units) * 32);
+    p.per_sm = std::max(1, std::min(5, 16 / (p.threads / 32 + 1)));
     per_block = 2;
-    blocks_per_sm = std::max(1, std::min(4, 512 / p.threads));
-  } else {
-    p.threads = kLnThreads;
-    per_block = 32;
-    blocks_per_sm = 1;
+    cap = p.per_sm * kSms;
   }
-  const int64_t cap = d <= kStagedD ? blocks_per_sm * kSms : 64;
   p.parts = static_cast<int>(std::max<int64_t>(1, std::min(cap, (rows + per_block - 1) / per_block)));
   return p;
 }
@@ -815,14 +856,17 @@ cudaError_t forward(const LnArgs& a, const DeviceInfo& dev, cudaStream_t s) {
   return wide ? forward_wide<T, true>(a, dev, s) : forward_wide<T, false>(a, dev, s);
 }
 
-template <int T, bool Wide, int NV, int R>
-cudaError_t backward_staged(const LnArgs& a, const LnPlan& p, float* part, uint32_t pitch, cudaStream_t s) {
+template <int T, bool Wide, int NV, int R, int MaxThreads, int MinBlocks>
+cudaError_t backward_staged(const LnArgs& a, const LnPlan& p, float* part, cudaStream_t s) {
   static std::atomic<bool> ready[64];
-  const cudaError_t e = allow_shared(ln_backward_kernel<T, Wide, NV, R>, kLnShared - 4096, ready);
+  const auto kernel = ln_backward_kernel<T, Wide, NV, R, MaxThreads, MinBlocks>;
+  const cudaError_t e = allow_shared(kernel, kLnShared - 4096, ready);
   if (e != cudaSuccess) return e;
-  return launch_pdl_smem(ln_backward_kernel<T, Wide, NV, R>, static_cast<unsigned>(p.parts),
-                         static_cast<unsigned>(p.threads), static_cast<size_t>(kStages) * 2 * R * pitch, s, a, part,
-                         pitch);
+  const uint32_t pitch = staged_pitch(a.d, T), stage = 2 * R * pitch;
+  const int stages = static_cast<int>(
+      std::max(2u, std::min<uint32_t>(kMaxStages, (kLnShared / static_cast<uint32_t>(p.per_sm) - 4096) / stage)));
+  return launch_pdl_smem(kernel, static_cast<unsigned>(p.parts), static_cast<unsigned>(p.threads) + 32,
+                         static_cast<size_t>(stages) * stage, s, a, part, pitch, stages);
 }
 
 template <int T, bool Wide>
@@ -831,13 +875,15 @@ cudaError_t backward_wide(const LnArgs& a, const LnPlan& p, float* part, cudaStr
   if (a.d <= 64) return launch_pdl(ln_backward_short_kernel<T, Wide, 8>, grid, threads, s, a, part);
   if (a.d <= 128) return launch_pdl(ln_backward_short_kernel<T, Wide, 16>, grid, threads, s, a, part);
   if (a.d <= 256) return launch_pdl(ln_backward_short_kernel<T, Wide, 32>, grid, threads, s, a, part);
-  // Rows a round: as many as the registers hold, one for each of the first
-  // warps (which hold the elements between the copies).
-  const uint32_t pitch = staged_pitch(a.d, T);
-  if (a.d > 4096) return backward_staged<T, Wide, 2, 1>(a, p, part, pitch, s);
-  if (T == MP_FP32 || p.threads < 128) return backward_staged<T, Wide, 1, 2>(a, p, part, pitch, s);
-  if constexpr (T != MP_FP32) return backward_staged<T, Wide, 1, 4>(a, p, part, pitch, s);
-  return cudaErrorInvalidValue;  // not reached
+  // Two rows a round (one where a thread has two units) are what 128 registers
+  // hold, and 16 such warps fill the register file. 32768 x 1600 bf16: 58 us;
+  // four rows a round 83 (spilled registers), 24 warps of 80 registers 86.
+  if (p.units == 2) return backward_staged<T, Wide, 2, 1, 512, 1>(a, p, part, s);
+  if (p.threads > 480) return backward_staged<T, Wide, 1, 2, 512, 1>(a, p, part, s);
+  if (p.threads > 224) return backward_staged<T, Wide, 1, 2, 480, 1>(a, p, part, s);
+  if (p.threads > 128) return backward_staged<T, Wide, 1, 2, 224, 2>(a, p, part, s);
+  if (p.threads > 96) return backward_staged<T, Wide, 1, 2, 128, 3>(a, p, part, s);
+  return backward_staged<T, Wide, 1, 2, 96, 4>(a, p, part, s);
 }
 
 template <int T>
