@@ -18,7 +18,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kDsThreads = 256;  // at most
+constexpr int kDsThreads = 128;  // at most
 constexpr int kDsWarps = kDsThreads / 32;
 constexpr int kMaxTeacher = 1024;
 constexpr int kDsCluster = 8;
@@ -70,7 +70,7 @@ __device__ __forceinline__ bool enter(const List& l, int32_t token) {  // the ta
 }
 
 template <int T>
-__global__ void __launch_bounds__(kDsThreads, 4) distill_kernel(DsArgs a, int slots) {
+__global__ void __launch_bounds__(kDsThreads, 6) distill_kernel(DsArgs a, int slots) {
   pdl_enter();
   using E = typename Elem<T>::type;
   const cg::cluster_group cluster = cg::this_cluster();
@@ -97,6 +97,9 @@ __global__ void __launch_bounds__(kDsThreads, 4) distill_kernel(DsArgs a, int sl
       if (part == 0 && threadIdx.x == 0) a.loss[r] = 0.0f;
       continue;
     }
+    const RowPart<T> in(x, a.vocab, part, parts);
+    Pack8<T> units[kUnits<T>];
+    first_chunk(units, in, threadIdx.x, threads);  // on its way while the list is read
     __syncthreads();  // the last row's list is read no more
     float tm = -kInf;
     bool bad = false;
@@ -111,15 +114,20 @@ __global__ void __launch_bounds__(kDsThreads, 4) distill_kernel(DsArgs a, int sl
       tm = max_nan(tm, l.q[i]);
     }
     RowStats st;
-    scan_row<T, false>(st, RowPart<T>(x, a.vocab, part, parts), c, slack, [](float) {});
-    st = join_block(st, red, c);
+    scan_row<T, false>(st, units, in, threadIdx.x, threads, c, slack, [](float) {}, [](auto&) {});
+    st = join_block(st, red);
     if (parts > 1) {
       if (threadIdx.x == 0) mine = st;
       cluster.sync();
-      st = join_all(parts, c, [&](int q) { return cluster.map_shared_rank(&mine, q); });
+      st = join_all(parts, [&](int q) { return cluster.map_shared_rank(&mine, q); });
       cluster.sync();  // before `mine`, or a logit another block still reads, is overwritten
     }
-    const RowLog log(st, c, a.scale);
+    const bool difference = out_of_range(st);
+    if (difference) {
+      st = difference_stats<T, false, BlockTeam>(x, a.vocab, st.m, c, red);
+      if (parts > 1) cluster.sync();  // every block has read the row
+    }
+    const RowLog log(st, difference, c, a.scale);
     // the teacher's distribution and the loss
     tm = block_reduce(tm, redf, true);
     const bool none = tm == -kInf;
@@ -158,7 +166,10 @@ __global__ void __launch_bounds__(kDsThreads, 4) distill_kernel(DsArgs a, int sl
       continue;
     }
     const float ws = __fmul_rn(w, a.scale), A = __fdiv_rn(ws, st.s);
-    map_row<T>(out, dx, x, [&](float v) { return __fmul_rn(exp2_fast(__fmul_rn(__fsub_rn(v, st.ref), c)), A); });
+    if (difference)
+      map_row<T>(out, dx, x, [&](float v) { return __fmul_rn(exp2_fast(__fmul_rn(__fsub_rn(v, st.m), c)), A); });
+    else
+      map_row<T>(out, dx, x, [&](float v) { return __fmul_rn(exp2_fast(__fmaf_rn(v, c, -st.R)), A); });
     __syncthreads();
     for (int i = threadIdx.x; i < a.k; i += threads) {
       const int32_t token = l.token[i];
@@ -171,7 +182,7 @@ __global__ void __launch_bounds__(kDsThreads, 4) distill_kernel(DsArgs a, int sl
         for (int j = i + 1; j < a.k; ++j)
           if (l.token[j] == token) q = __fadd_rn(q, l.q[j]);
       }
-      const float t = __fmul_rn(__fsub_rn(l.z[i], st.ref), c);
+      const float t = difference ? __fmul_rn(__fsub_rn(l.z[i], st.m), c) : __fmaf_rn(l.z[i], c, -st.R);
       dx[token] = Elem<T>::put(__fmul_rn(ws, __fsub_rn(__fdiv_rn(exp2_fast(t), st.s), q)));
     }
   }

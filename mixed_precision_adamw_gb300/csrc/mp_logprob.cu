@@ -301,16 +301,18 @@ __device__ __forceinline__ void read_part(const LpArgs& a, Pack8<T> (&x)[kUnits<
       ahead);
   const bool some = p.first + t < p.last || t < p.extra;
   if (Top) ps.lane_max[t / 32][t % 32] = some ? order_of(st.m) : 0;
-  st = join_warp(st, c);
+  st = join_warp(st);
   if (t % 32 == 0) ps.stats[t / 32] = st;
 }
 
 // A row's outputs from its statistics and its n candidates, by a team.
 template <int T, bool Entropy, bool Top, typename Team>
-__device__ __forceinline__ void write_row(const LpArgs& a, int64_t r, const RowStats& st, float c, const uint64_t* keys,
-                                          int n) {
+__device__ __forceinline__ void write_row(const LpArgs& a, int64_t r, RowStats st, float c, const uint64_t* keys,
+                                          int n, RowStats* red) {
   const typename Elem<T>::type* x = static_cast<const typename Elem<T>::type*>(a.logits) + r * a.stride;
-  const RowLog log(st, c, a.scale);
+  const bool difference = out_of_range(st);
+  if (difference) st = difference_stats<T, Entropy, Team>(x, a.vocab, st.m, c, red);
+  const RowLog log(st, difference, c, a.scale);
   if (Team::thread() == 0) {
     if (a.lse) a.lse[r] = log.lse;
     if (Entropy) a.entropy[r] = log.entropy;
@@ -357,7 +359,7 @@ __global__ void __launch_bounds__(kLpThreads, 8) lp_forward_kernel(LpArgs a, int
     first_chunk(units, p, threadIdx.x, threads);
     read_part<T, Entropy, Top>(a, units, p, threadIdx.x, threads, c, slack, slots, per_slot, ps, [](auto&) {});
     __syncthreads();
-    RowStats st = join_all(threads / 32, c, [&](int i) { return ps.stats + i; });
+    RowStats st = join_all(threads / 32, [&](int i) { return ps.stats + i; });
     int n = 0;
     if (Top) {
       if (threadIdx.x < 32) {
@@ -377,12 +379,12 @@ __global__ void __launch_bounds__(kLpThreads, 8) lp_forward_kernel(LpArgs a, int
       }
       cluster.sync();
       if (part == 0) {
-        st = join_all(parts, c, [&](int q) { return part_stats + q; });
+        st = join_all(parts, [&](int q) { return part_stats + q; });
         keys = part_keys;
         n = parts * kMaxTop;
       }
     }
-    if (part == 0) write_row<T, Entropy, Top, BlockTeam>(a, r, st, c, keys, n);
+    if (part == 0) write_row<T, Entropy, Top, BlockTeam>(a, r, st, c, keys, n, ps.stats);
     if (r + teams < a.rows) {  // before the next row's sums go where this row's were read
       if (parts > 1) cluster.sync();
       __syncthreads();
@@ -450,14 +452,14 @@ __global__ void __launch_bounds__(kLpRowThreads, 6) lp_rows_kernel(LpArgs a, int
     for (int64_t r = blockIdx.x; r < a.rows; r += teams, ++round) {
       const int set = round & 1;
       barrier_sync<kFull>(set);
-      const RowStats st = join_all(kLpWarps, c, [&](int i) { return ps[set].stats + i; });
+      const RowStats st = join_all(kLpWarps, [&](int i) { return ps[set].stats + i; });
       int n = 0;
       if (Top) {
         n = find_top<T>(static_cast<const E*>(a.logits) + r * a.stride, a.vocab, 0, 1, a.top_k, ps[set],
                                   Chunks{slots + set * kSlots * kLpThreads, per_slot, kLpThreads}, top);
         __syncwarp();
       }
-      write_row<T, Entropy, Top, WarpTeam>(a, r, st, c, top.keys, n);
+      write_row<T, Entropy, Top, WarpTeam>(a, r, st, c, top.keys, n, nullptr);
       barrier_arrive<kEmpty>(set);
     }
   }
