@@ -795,9 +795,9 @@ LnPlan backward_plan(int64_t rows, int64_t d) {
     cap = 4 * kSms;
   } else if (d <= kStagedD) {
     const int64_t units = (d + 7) / 8;
-    p.units = d > 4096 ? 2 : 1;
+    p.units = d > 7680 ? 3 : d > 4096 ? 2 : 1;
     p.threads = static_cast<int>((units + 32 * p.units - 1) / (32 * p.units) * 32);
-    p.per_sm = std::max(1, std::min(5, 16 / (p.threads / 32 + 1)));
+    p.per_sm = p.units > 1 ? 1 : std::max(1, std::min(5, 16 / (p.threads / 32 + 1)));
     per_block = 2;
     cap = p.per_sm * kSms;
   }
@@ -875,10 +875,22 @@ cudaError_t backward_wide(const LnArgs& a, const LnPlan& p, float* part, cudaStr
   if (a.d <= 64) return launch_pdl(ln_backward_short_kernel<T, Wide, 8>, grid, threads, s, a, part);
   if (a.d <= 128) return launch_pdl(ln_backward_short_kernel<T, Wide, 16>, grid, threads, s, a, part);
   if (a.d <= 256) return launch_pdl(ln_backward_short_kernel<T, Wide, 32>, grid, threads, s, a, part);
-  // Two rows a round (one where a thread has two units) are what 128 registers
-  // hold, and 16 such warps fill the register file. 32768 x 1600 bf16: 58 us;
-  // four rows a round 83 (spilled registers), 24 warps of 80 registers 86.
-  if (p.units == 2) return backward_staged<T, Wide, 2, 1, 512, 1>(a, p, part, s);
+  // Units a thread and rows a round are what the registers hold: a unit of a
+  // row takes 16, its weights and sums 24. Two rows of one unit fit 128, and 16
+  // such warps fill the register file. 32768 x 1600 bf16: 58 us; four rows a
+  // round 83 (spilled registers), 24 warps of 80 registers 86. Longer rows take
+  // more units in fewer warps; 8192 rows of bf16, us:
+  //   d     2 units, 2 rows   2 units, 1 row   3 units, 1 row   2 units, 1 row
+  //         168 registers     128              168              96 (spilled)
+  //   5632  56                62                                81
+  //   6144                    64               70               85
+  //   7680                    72               80               104
+  //   8192                                     82               108
+  // 4096 with one unit and two rows: 42, although 96 registers a thread spill 16
+  // bytes; two units of 168 registers 45.
+  if (p.units == 3) return backward_staged<T, Wide, 3, 1, 352, 1>(a, p, part, s);
+  if (p.units == 2 && p.threads > 352) return backward_staged<T, Wide, 2, 1, 480, 1>(a, p, part, s);
+  if (p.units == 2) return backward_staged<T, Wide, 2, 2, 352, 1>(a, p, part, s);
   if (p.threads > 480) return backward_staged<T, Wide, 1, 2, 512, 1>(a, p, part, s);
   if (p.threads > 224) return backward_staged<T, Wide, 1, 2, 480, 1>(a, p, part, s);
   if (p.threads > 128) return backward_staged<T, Wide, 1, 2, 224, 2>(a, p, part, s);

@@ -118,6 +118,13 @@ def test_layernorm_row_counts(mp, rows, d):
     ln_case(mp, rows, d, BF, FF)
 
 
+@pytest.mark.parametrize("dtype", [BF, FF])
+@pytest.mark.parametrize("d", [3840, 3841, 4096, 4097, 5632, 5633, 7680, 7681, 8191, 8192])
+def test_layernorm_register_classes(mp, d, dtype):
+    # either side of each change of units a thread; several rounds a block, the last one partly filled
+    ln_case(mp, 701, d, dtype, dtype)
+
+
 @pytest.mark.parametrize("d", [100, 768, 4096])
 def test_layernorm_large_offset(mp, d):
     # a common offset a thousand times the spread: two passes lose nothing to cancellation
