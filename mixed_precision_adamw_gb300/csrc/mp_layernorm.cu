@@ -33,42 +33,52 @@ struct LnArgs {
   int weight_type;
 };
 
-// A row divided over a group of L threads, NV units of eight elements each:
-// element e of unit v of thread t.
-template <bool Wide>
-__device__ __forceinline__ int64_t column(int v, int e, int t, int L) {
-  return Wide ? (static_cast<int64_t>(v) * L + t) * 8 + e : (static_cast<int64_t>(v) * 8 + e) * L + t;
-}
+// The columns of thread t of the L that share a row of d, NV units of eight
+// elements: element e of unit v. Wide rows: a unit is eight neighbours, so one
+// 16-B access (two for fp32). Other rows: S lanes (a warp, or all of a shorter
+// group) have a span of the row, in which neighbouring lanes take neighbouring
+// elements; whatever the lane and the warp add to a column is in `first`, the
+// rest is a constant of the access (bf16, forward and backward: 32768 x 1357
+// 60 and 91 us; 136 and 139 with neighbours over the whole group, whose
+// addresses and tests are computed for each element).
+template <bool Wide, int NV, int S = 32>
+struct Columns {
+  int first, left, step;  // left: columns from the first one on, to the row's or the span's end
 
-template <int T, bool Wide>
-__device__ __forceinline__ void load_unit(Pack8<T>& u, const typename Elem<T>::type* row, int v, int t, int L,
-                                          int64_t d) {
-  const int64_t j = column<Wide>(v, 0, t, L);
-  if (Wide) {
-    if (j < d)
-      u.load(row + j);
+  __device__ __forceinline__ Columns(int t, int L, int64_t d) {
+    if (Wide) {
+      first = 8 * t;
+      left = static_cast<int>(d) - first;
+      step = 8 * L;
+    } else {
+      const int n = static_cast<int>(d), spans = L / S, span = ((n + spans - 1) / spans + S - 1) / S * S;
+      first = t / S * span + t % S;
+      left = min(n, (t / S + 1) * span) - first;
+      step = 8 * S;
+    }
+  }
+  __device__ __forceinline__ int offset(int v, int e) const { return Wide ? v * step + e : (8 * v + e) * S; }
+  __device__ __forceinline__ int at(int v, int e) const { return first + offset(v, e); }
+  // whether the element lies in the row (Wide units are in or out whole)
+  __device__ __forceinline__ bool has(int v, int e) const { return offset(v, Wide ? 0 : e) < left; }
+
+  template <int T>
+  __device__ __forceinline__ void load(Pack8<T>& u, const typename Elem<T>::type* row, int v) const {
+    if (!Wide)
+      u.load_stepped(row + first, offset(v, 0), S, left);
+    else if (has(v, 0))
+      u.load(row + at(v, 0));
     else
       u.zero();
-  } else {
-    u.load_stepped(row, j, L, d);
   }
-}
-
-template <int T, bool Wide>
-__device__ __forceinline__ void store_unit(const Pack8<T>& u, typename Elem<T>::type* row, int v, int t, int L,
-                                           int64_t d) {
-  const int64_t j = column<Wide>(v, 0, t, L);
-  if (!Wide)
-    u.store_stepped(row, j, L, d);
-  else if (j < d)
-    u.store(row + j);
-}
-
-// Whether element e of a unit lies in the row (Wide units are in or out whole).
-template <bool Wide>
-__device__ __forceinline__ bool in_row(int v, int e, int t, int L, int64_t d) {
-  return column<Wide>(v, Wide ? 0 : e, t, L) < d;
-}
+  template <int T>
+  __device__ __forceinline__ void store(const Pack8<T>& u, typename Elem<T>::type* row, int v) const {
+    if (!Wide)
+      u.store_stepped(row + first, offset(v, 0), S, left);
+    else if (has(v, 0))
+      u.store(row + at(v, 0));
+  }
+};
 
 // Sum over groups of L <= 32 neighbouring lanes, to each of them.
 template <int L>
@@ -158,13 +168,13 @@ __device__ __forceinline__ void stage_weights(float* sw, const LnArgs& a, int64_
 }
 
 // y of a unit of a row from its x.
-template <int T, bool Wide>
+template <int T, bool Wide, int NV, int S>
 __device__ __forceinline__ void normalise_unit(Pack8<T>& u, const float* sw, const float* sb, float mean, float rstd,
-                                               int v, int t, int L, int64_t units, int64_t d) {
+                                               int v, const Columns<Wide, NV, S>& c, int64_t units) {
   float f[8], w[8], b[8];
   u.get(f);
   if (Wide) {
-    const int64_t unit = min(static_cast<int64_t>(v) * L + t, units - 1);
+    const int64_t unit = min(static_cast<int64_t>(c.at(v, 0) / 8), units - 1);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const float4 p = *reinterpret_cast<const float4*>(sw + (h * units + unit) * 4);
@@ -175,9 +185,9 @@ __device__ __forceinline__ void normalise_unit(Pack8<T>& u, const float* sw, con
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int64_t j = min(column<Wide>(v, e, t, L), d - 1);
-      w[e] = sw[j];
-      b[e] = sb[j];
+      const bool has = c.has(v, e);
+      w[e] = has ? sw[c.at(v, e)] : 0.0f;
+      b[e] = has ? sb[c.at(v, e)] : 0.0f;
     }
   }
 #pragma unroll
@@ -196,6 +206,7 @@ __global__ void __launch_bounds__(kLnThreads, 4) ln_forward_short_kernel(LnArgs 
   float* sw = reinterpret_cast<float*>(smem);
   const int t = threadIdx.x % L;
   const int64_t units = (a.d + 7) / 8;
+  const Columns<Wide, 1, L> cols(t, L, a.d);
   const float n = static_cast<float>(a.d);
   const int64_t groups = static_cast<int64_t>(gridDim.x) * (kLnThreads / L);
   const int64_t first = static_cast<int64_t>(blockIdx.x) * (kLnThreads / L) + threadIdx.x / L;
@@ -208,7 +219,10 @@ __global__ void __launch_bounds__(kLnThreads, 4) ln_forward_short_kernel(LnArgs 
     for (int i = 0; i < R; ++i) {
       const int64_t r = r0 + i * groups + first;
       const bool live = r < a.rows;
-      load_unit<T, Wide>(u[i], static_cast<const E*>(a.x) + (live ? r : 0) * a.x_stride, 0, t, L, live ? a.d : 0);
+      if (live)
+        cols.load(u[i], static_cast<const E*>(a.x) + r * a.x_stride, 0);
+      else
+        u[i].zero();
     }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -220,15 +234,15 @@ __global__ void __launch_bounds__(kLnThreads, 4) ln_forward_short_kernel(LnArgs 
       const float mean = __fdiv_rn(lanes_sum<L>(s), n);
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (in_row<Wide>(0, e, t, L, a.d)) {
+        if (cols.has(0, e)) {
           const float c = __fsub_rn(f[e], mean);
           q = __fmaf_rn(c, c, q);
         }
       const float var = __fdiv_rn(lanes_sum<L>(q), n);
       const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(var, a.eps)));
       if (r >= a.rows) continue;
-      normalise_unit<T, Wide>(u[i], sw, sw + 8 * units, mean, rstd, 0, t, L, units, a.d);
-      store_unit<T, Wide>(u[i], static_cast<E*>(a.y) + r * a.y_stride, 0, t, L, a.d);
+      normalise_unit(u[i], sw, sw + 8 * units, mean, rstd, 0, cols, units);
+      cols.store(u[i], static_cast<E*>(a.y) + r * a.y_stride, 0);
       if (t == 0) {
         if (a.mean_out) a.mean_out[r] = mean;
         if (a.rstd_out) a.rstd_out[r] = rstd;
@@ -250,6 +264,7 @@ __global__ void __launch_bounds__(kLnThreads, NV >= 8 ? 2 : NV >= 4 ? 3 : 4) ln_
   const int64_t units = (a.d + 7) / 8;
   float* sw = reinterpret_cast<float*>(smem);
   const int L = 32 * G, t = threadIdx.x % L, group = threadIdx.x / L, count = kLnThreads / L;
+  const Columns<Wide, NV> cols(t, L, a.d);
   uint8_t* buffers = smem + 64 * units + static_cast<size_t>(group) * kStages * pitch;
   const int64_t step = static_cast<int64_t>(gridDim.x) * count;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * count + group;
@@ -304,7 +319,7 @@ __global__ void __launch_bounds__(kLnThreads, NV >= 8 ? 2 : NV >= 4 ? 3 : 4) ln_
       }
       Pack8<T> u[NV];
 #pragma unroll
-      for (int v = 0; v < NV; ++v) load_unit<T, Wide>(u[v], data, v, t, L, a.d);
+      for (int v = 0; v < NV; ++v) cols.load(u[v], data, v);
       float s = 0.0f;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
@@ -324,7 +339,7 @@ __global__ void __launch_bounds__(kLnThreads, NV >= 8 ? 2 : NV >= 4 ? 3 : 4) ln_
         u[v].get(f);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (in_row<Wide>(v, e, t, L, a.d)) {
+          if (cols.has(v, e)) {
             const float c = __fsub_rn(f[e], mean);
             q = __fmaf_rn(c, c, q);
           }
@@ -334,9 +349,9 @@ __global__ void __launch_bounds__(kLnThreads, NV >= 8 ? 2 : NV >= 4 ? 3 : 4) ln_
       E* y = static_cast<E*>(a.y) + r * a.y_stride;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        if (!in_row<Wide>(v, 0, t, L, a.d)) continue;
-        normalise_unit<T, Wide>(u[v], sw, sw + 8 * units, mean, rstd, v, t, L, units, a.d);
-        store_unit<T, Wide>(u[v], y, v, t, L, a.d);
+        if (!cols.has(v, 0)) continue;
+        normalise_unit(u[v], sw, sw + 8 * units, mean, rstd, v, cols, units);
+        cols.store(u[v], y, v);
       }
       if (t == 0) {
         if (a.mean_out) a.mean_out[r] = mean;
@@ -513,15 +528,16 @@ ln_backward_kernel(LnArgs a, float* part, uint32_t pitch, int stages) {
     return;
   }
   const float inv_d = __fdiv_rn(1.0f, static_cast<float>(a.d));
+  const Columns<Wide, NV> cols(t, L, a.d);
   float w[NV][8], dw[NV][8], db[NV][8], xh[R][NV][8], g[R][NV][8];
   bool mine[NV];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    mine[v] = in_row<Wide>(v, 0, t, L, a.d);
+    mine[v] = cols.has(v, 0);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int64_t j = column<Wide>(v, e, t, L);
-      w[v][e] = j < a.d ? (a.weight ? load_as(a.weight, j, a.weight_type) : 1.0f) : 0.0f;
+      const int j = cols.at(v, e);
+      w[v][e] = cols.has(v, e) ? (a.weight ? load_as(a.weight, j, a.weight_type) : 1.0f) : 0.0f;
       dw[v][e] = db[v][e] = 0.0f;
 #pragma unroll
       for (int i = 0; i < R; ++i) xh[i][v][e] = g[i][v][e] = 0.0f;  // stays so past the row
@@ -555,9 +571,9 @@ ln_backward_kernel(LnArgs a, float* part, uint32_t pitch, int stages) {
         if (mine[v]) {
           Pack8<T> u;
           float f[8];
-          load_unit<T, Wide>(u, dy, v, t, L, a.d);
+          cols.load(u, dy, v);
           u.get(g[i][v]);
-          load_unit<T, Wide>(u, x, v, t, L, a.d);
+          cols.load(u, x, v);
           u.get(f);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
@@ -603,7 +619,7 @@ ln_backward_kernel(LnArgs a, float* part, uint32_t pitch, int stages) {
           if (Wide)
             u.store(out + v * 8 * L);
           else
-            store_unit<T, Wide>(u, out, v, t, L, a.d);
+            cols.store(u, out, v);
         }
       }
       if (out) out += a.y_stride;
@@ -619,8 +635,8 @@ ln_backward_kernel(LnArgs a, float* part, uint32_t pitch, int stages) {
   for (int v = 0; v < NV; ++v)
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (in_row<Wide>(v, e, t, L, a.d)) {
-        const int64_t j = column<Wide>(v, e, t, L);
+      if (cols.has(v, e)) {
+        const int j = cols.at(v, e);
         pw[j] = ok ? dw[v][e] : __int_as_float(0x7FC00000);
         pw[a.d + j] = db[v][e];
       }
@@ -636,21 +652,25 @@ __global__ void __launch_bounds__(kLnThreads) ln_backward_short_kernel(LnArgs a,
   __shared__ float joined[G][8 * L];
   const int t = threadIdx.x % L, group = threadIdx.x / L;
   const float inv_d = __fdiv_rn(1.0f, static_cast<float>(a.d));
+  const Columns<Wide, 1, L> cols(t, L, a.d);
   float w[8], dw[8], db[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const int64_t j = column<Wide>(0, e, t, L);
-    w[e] = j < a.d ? (a.weight ? load_as(a.weight, j, a.weight_type) : 1.0f) : 0.0f;
+    const int j = cols.at(0, e);
+    w[e] = cols.has(0, e) ? (a.weight ? load_as(a.weight, j, a.weight_type) : 1.0f) : 0.0f;
     dw[e] = db[e] = 0.0f;
   }
   const int64_t groups = static_cast<int64_t>(gridDim.x) * G;
   for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * G; r0 < a.rows; r0 += groups) {
     const int64_t r = r0 + group;
     const bool live = r < a.rows;
-    const int64_t at = live ? r : 0, n = live ? a.d : 0;
     Pack8<T> x, g;
-    load_unit<T, Wide>(x, static_cast<const E*>(a.x) + at * a.x_stride, 0, t, L, n);
-    load_unit<T, Wide>(g, static_cast<const E*>(a.dy) + at * a.dy_stride, 0, t, L, n);
+    x.zero();
+    g.zero();
+    if (live) {
+      cols.load(x, static_cast<const E*>(a.x) + r * a.x_stride, 0);
+      cols.load(g, static_cast<const E*>(a.dy) + r * a.dy_stride, 0);
+    }
     const float mean = live ? a.mean[r] : 0.0f, rstd = live ? a.rstd[r] : 0.0f;
     float fx[8], fg[8], s1 = 0.0f, s2 = 0.0f;
     x.get(fx);
@@ -670,7 +690,7 @@ __global__ void __launch_bounds__(kLnThreads) ln_backward_short_kernel(LnArgs a,
       for (int e = 0; e < 8; ++e)
         fx[e] = __fmul_rn(rstd, __fmaf_rn(-fx[e], c2, __fsub_rn(__fmul_rn(fg[e], w[e]), c1)));
       x.put(fx);
-      store_unit<T, Wide>(x, static_cast<E*>(a.y) + r * a.y_stride, 0, t, L, a.d);
+      cols.store(x, static_cast<E*>(a.y) + r * a.y_stride, 0);
     }
   }
   if (!part) return;
@@ -681,7 +701,7 @@ __global__ void __launch_bounds__(kLnThreads) ln_backward_short_kernel(LnArgs a,
     for (int e = 0; e < 8; ++e) joined[group][e * L + t] = k ? db[e] : dw[e];
     __syncthreads();
     for (int i = threadIdx.x; i < 8 * L; i += kLnThreads) {
-      const int64_t j = column<Wide>(0, i / L, i % L, L);
+      const int j = Columns<Wide, 1, L>(i % L, L, a.d).at(0, i / L);
       if (j >= a.d) continue;
       float s = 0.0f;
       for (int q = 0; q < G; ++q) s = __fadd_rn(s, joined[q][i]);

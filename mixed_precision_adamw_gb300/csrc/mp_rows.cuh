@@ -149,13 +149,13 @@ struct Pack8 {  // bf16, fp16
   }
   __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = v; }
-  __device__ __forceinline__ void load_stepped(const uint16_t* p, int64_t j, int64_t step, int64_t n) {
+  __device__ __forceinline__ void load_stepped(const uint16_t* p, int j, int step, int n) {
     uint32_t h[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) h[e] = j + e * step < n ? p[j + e * step] : 0u;
     v = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
   }
-  __device__ __forceinline__ void store_stepped(uint16_t* p, int64_t j, int64_t step, int64_t n) const {
+  __device__ __forceinline__ void store_stepped(uint16_t* p, int j, int step, int n) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -198,13 +198,13 @@ struct Pack8<MP_FP32> {
     reinterpret_cast<float4*>(p)[0] = a;
     reinterpret_cast<float4*>(p)[1] = b;
   }
-  __device__ __forceinline__ void load_stepped(const float* p, int64_t j, int64_t step, int64_t n) {
+  __device__ __forceinline__ void load_stepped(const float* p, int j, int step, int n) {
     float h[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) h[e] = j + e * step < n ? p[j + e * step] : 0.0f;
     put(h);
   }
-  __device__ __forceinline__ void store_stepped(float* p, int64_t j, int64_t step, int64_t n) const {
+  __device__ __forceinline__ void store_stepped(float* p, int j, int step, int n) const {
     float h[8];
     get(h);
 #pragma unroll
