@@ -135,7 +135,7 @@ __device__ __forceinline__ void load_any(Pack8<T>& x, const typename Elem<T>::ty
   if (aligned)
     x.load(row + j);
   else
-    x.load_stepped(row, j, 1, j + 8);
+    x.load_stepped(row + j, 0, 1, 8);
 }
 
 // Writes f(x[j]) for a part of a row: `out` divides dx (its alignment), x is
