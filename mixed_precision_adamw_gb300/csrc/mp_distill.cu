@@ -3,11 +3,12 @@
 //
 // A block takes a row: one pass over it for the sum of exponentials
 // (mp_softmax.cuh), a second that writes the gradient w scale (p - q). The
-// second reads the row out of L2, where the rows in flight fit (152 SMs x 4
-// blocks x 256 KB at the largest), so HBM sees each logit read once and each
-// gradient written once: 4 B an element for 16-bit types. The listed tokens
-// (few) are corrected afterwards by one thread each. Few rows are split over
-// the blocks of a cluster.
+// second reads the row out of L2 where the rows in flight fit (6 blocks an SM,
+// 91 MB at 50304 logits of 16 bits), so that HBM sees each logit read once and
+// each gradient written once: 4 B an element for 16-bit types. The listed
+// tokens (few) are corrected afterwards by one thread each. Few rows are split
+// over the blocks of a cluster. Many long rows take the ring below, which holds
+// most of a row in shared memory instead (8192 x 50304 bf16: 336 us).
 #include "mp_device.cuh"
 #include "mp_internal.h"
 #include "mp_softmax.cuh"
@@ -167,9 +168,9 @@ __global__ void __launch_bounds__(kDsThreads, 6) distill_kernel(DsArgs a, int sl
     }
     const float ws = __fmul_rn(w, a.scale), A = __fdiv_rn(ws, st.s);
     if (difference)
-      map_row<T>(out, dx, x, [&](float v) { return __fmul_rn(exp2_fast(__fmul_rn(__fsub_rn(v, st.m), c)), A); });
+      map_row<T, true>(out, dx, x, [&](float v) { return __fmul_rn(exp2_fast(__fmul_rn(__fsub_rn(v, st.m), c)), A); });
     else
-      map_row<T>(out, dx, x, [&](float v) { return __fmul_rn(exp2_fast(__fmaf_rn(v, c, -st.R)), A); });
+      map_row<T, true>(out, dx, x, [&](float v) { return __fmul_rn(exp2_fast(__fmaf_rn(v, c, -st.R)), A); });
     __syncthreads();
     for (int i = threadIdx.x; i < a.k; i += threads) {
       const int32_t token = l.token[i];

@@ -504,11 +504,11 @@ __global__ void __launch_bounds__(kLpThreads) lp_backward_kernel(LpArgs a, int p
       return __fmul_rn(p, __fmaf_rn(a1, max_nan(y, kLowest), a0));
     };
     if (h == 0.0f)
-      map_row<T>(out, dx, x, [&](float v) {
+      map_row<T, false>(out, dx, x, [&](float v) {
         return __fmul_rn(a0, exp2_fast(__fmul_rn(__fmaf_rn(v, scale, -lse), kLog2E)));
       });
     else
-      map_row<T>(out, dx, x, of);
+      map_row<T, false>(out, dx, x, of);
     __syncthreads();
     if (t >= 0 && threadIdx.x == 0 && out.holds(t)) dx[t] = Elem<T>::put(__fmaf_rn(g, scale, of(xt)));
   }

@@ -149,6 +149,19 @@ struct Pack8 {  // bf16, fp16
   }
   __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = v; }
+  // The elements at p, from the two 16-B pieces a and b that they lie in.
+  __device__ __forceinline__ void across(const uint16_t* p, uint4 a, uint4 b) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    const bool two = at & 8, one = at & 4;
+    const uint32_t shift = at & 2 ? 16 : 0;
+    const uint32_t t[6] = {two ? a.z : a.x, two ? a.w : a.y, two ? b.x : a.z,
+                           two ? b.y : a.w, two ? b.z : b.x, two ? b.w : b.y};
+    uint32_t w[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = one ? t[i + 1] : t[i];
+    v = make_uint4(__funnelshift_r(w[0], w[1], shift), __funnelshift_r(w[1], w[2], shift),
+                   __funnelshift_r(w[2], w[3], shift), __funnelshift_r(w[3], w[4], shift));
+  }
   __device__ __forceinline__ void load_stepped(const uint16_t* p, int j, int step, int n) {
     uint32_t h[8];
 #pragma unroll

@@ -128,19 +128,51 @@ __device__ __forceinline__ void load_units(Pack8<T> (&x)[U], const RowPart<T>& p
 template <int T>
 constexpr int kUnits = T == MP_FP32 ? 2 : 4;
 
-// Eight elements of a row from element j on, wherever they lie: one 16-B load
-// (two for fp32) if they start on a 16-B boundary, element by element if not.
-template <int T>
-__device__ __forceinline__ void load_any(Pack8<T>& x, const typename Elem<T>::type* row, int64_t j, bool aligned) {
-  if (aligned)
-    x.load(row + j);
-  else
-    x.load_stepped(row + j, 0, 1, 8);
+// U units of eight elements of a row of n, `step` elements apart, the first
+// from element j on, as far as they start before element `end`. Where they
+// start on a 16-B boundary: one 16-B load each (two for fp32). Where not, with
+// Across and 16-bit types the two 16-B pieces that a unit lies in, all loaded
+// before the first are shifted together; units at the row's ends, whose pieces
+// may reach beyond it, and the others are loaded element by element. 8192 x
+// 50304 bf16 in rows of 50307: the distillation 476 us across, 590 by elements;
+// the log probabilities' gradient 342 and 337, and its aligned rows 256 and 249,
+// for the registers that the pieces take.
+template <int T, bool Across, int U>
+__device__ __forceinline__ void load_any(Pack8<T> (&x)[U], const typename Elem<T>::type* row, int64_t j, int64_t step,
+                                         int64_t end, int64_t n, bool aligned) {
+  if (aligned) {
+#pragma unroll
+    for (int q = 0; q < U; ++q)
+      if (j + q * step < end) x[q].load(row + j + q * step);
+    return;
+  }
+  constexpr bool kAcross = Across && T != MP_FP32;
+  if constexpr (kAcross) {
+    uint4 a[U], b[U];
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      const int64_t k = j + q * step;
+      a[q] = b[q] = make_uint4(0u, 0u, 0u, 0u);
+      if (k < end && k >= 7 && k + 15 <= n) {
+        const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(row + k) & ~uintptr_t{15});
+        a[q] = p[0];
+        b[q] = p[1];
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < U; ++q) x[q].across(row + j, a[q], b[q]);  // one alignment: step is a multiple of 8
+  }
+#pragma unroll
+  for (int q = 0; q < U; ++q) {
+    const int64_t k = j + q * step;
+    if (k < end && (!kAcross || k < 7 || k + 15 > n)) x[q].load_stepped(row + k, 0, 1, 8);
+  }
 }
 
 // Writes f(x[j]) for a part of a row: `out` divides dx (its alignment), x is
-// read to match. Each thread reads what it writes, so dx may be x.
-template <int T, typename F>
+// read to match (Across: load_any). Each thread reads what it writes, so dx
+// may be x.
+template <int T, bool Across, typename F>
 __device__ __forceinline__ void map_row(const RowPart<T>& out, typename Elem<T>::type* dx,
                                         const typename Elem<T>::type* x, F&& f) {
   using E = typename Elem<T>::type;
@@ -149,9 +181,7 @@ __device__ __forceinline__ void map_row(const RowPart<T>& out, typename Elem<T>:
   const bool aligned = reinterpret_cast<uintptr_t>(x + out.head) % 16 == 0;
   for (int64_t i = out.first + threadIdx.x; i < out.last; i += static_cast<int64_t>(U) * threads) {
     Pack8<T> u[U];
-#pragma unroll
-    for (int q = 0; q < U; ++q)
-      if (i + q * threads < out.last) load_any<T>(u[q], x, out.head + 8 * (i + q * threads), aligned);
+    load_any<T, Across>(u, x, out.head + 8 * i, 8 * threads, out.head + 8 * out.last, out.n, aligned);
 #pragma unroll
     for (int q = 0; q < U; ++q)
       if (i + q * threads < out.last) {
