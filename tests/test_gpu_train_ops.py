@@ -701,6 +701,84 @@ def test_in_a_graph(mp):
     assert all(torch.equal(p, q) for p, q in zip(got, (y, dh, dw, loss, dx, logp, lse, tl, ti)))
 
 
+# --- inputs and outputs of unlike alignment ---------------------------------------
+
+def among_nan(t, off, pad=8):
+    """t at an offset of `off` elements, between NaNs: an element used from
+    beyond a row shows."""
+    rows, cols = t.shape
+    buf = torch.full((off + rows * (cols + pad) + 64,), math.nan, dtype=t.dtype, device="cuda")
+    view = buf[off:off + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
+    view.copy_(t)
+    return view
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FF])
+@pytest.mark.parametrize("vocab", [1, 8, 15, 16, 22, 23, 24, 31, 70, 1029, 8200])
+@pytest.mark.parametrize("pad", [8, 3])
+def test_softmax_gradients_of_unlike_alignment(mp, vocab, dtype, pad):
+    # with pad 3 the alignment changes from row to row as well
+    g = gen(vocab)
+    rows = 9
+    x = randn((rows, vocab), g, 2.0, dtype)
+    t = torch.randint(0, vocab, (rows,), generator=g, device="cuda")
+    lt, idx = teacher_for(x, min(vocab, 6), g)
+    dlogp, dent = randn((rows,), g), randn((rows,), g)
+    for off in range(8):
+        for out in (0, 1, 2, 5):
+            what = f"{vocab} {dtype} at {off} -> {out}"
+            xs = among_nan(x, off, pad)
+            logp, lse, ent = f32(rows), f32(rows), f32(rows)
+            mp.mp_token_logprob_forward(xs, t, logp=logp, lse=lse, entropy=ent)
+            dx = Guarded(rows, vocab, dtype, 8, out)
+            mp.mp_token_logprob_backward(dx.view, xs, t, lse=lse, dlogp=dlogp, entropy=ent, dentropy=dent)
+            rd, td = R.lp_backward(x, t, lse, ent, dlogp, dent, 1.0)
+            R.assert_within(dx.view, rd, R.rounded(rd, td, dtype), "log probabilities " + what)
+            dx.check("dlogits")
+            loss, dx = f32(rows), Guarded(rows, vocab, dtype, 8, out)
+            mp.mp_distill_topk(loss, dx.view, xs, lt, idx)
+            (rl, rd), (tl, td) = R.distill(x, lt, idx, None, 1.0)
+            R.assert_within(loss, rl, tl, "loss " + what)
+            R.assert_within(dx.view, rd, R.rounded(rd, td, dtype), "distillation " + what)
+            dx.check("dlogits")
+
+
+@pytest.mark.parametrize("rows", [77, 400])
+def test_distill_unlike_alignment_many_rows(mp, rows):
+    g = gen(rows)
+    x = randn((rows, 20001), g, 2.0, BF)
+    lt, idx = teacher_for(x, 33, g)
+    loss, dx = f32(rows), Guarded(rows, 20001, BF, 7, 0)
+    mp.mp_distill_topk(loss, dx.view, among_nan(x, 3, 2), lt, idx)
+    (rl, rd), (tl, td) = R.distill(x, lt, idx, None, 1.0)
+    R.assert_within(loss, rl, tl, "loss")
+    R.assert_within(dx.view, rd, R.rounded(rd, td, BF), "dlogits")
+    dx.check("dlogits")
+
+
+@pytest.mark.parametrize("dtype", [BF, FF])
+@pytest.mark.parametrize("d", [60, 257, 1365, 4100])
+@pytest.mark.parametrize("pad", [8, 5])
+def test_layernorm_unlike_alignment(mp, d, dtype, pad):
+    g = gen(d)
+    rows = 37
+    x, dy, w, b = (randn(s, g, 1.0, dtype) for s in ((rows, d), (rows, d), (d,), (d,)))
+    for off, off_dy, out in ((0, 1, 0), (1, 0, 0), (3, 6, 1), (0, 0, 5)):
+        y, dx = Guarded(rows, d, dtype, pad, out), Guarded(rows, d, dtype, 8, (out + 3) % 8)
+        mean, rstd, dw, db = f32(rows), f32(rows), torch.empty_like(w), torch.empty_like(b)
+        ws = torch.empty(mp.mp_layernorm_workspace_bytes(rows, d), dtype=torch.uint8, device="cuda")
+        xs, dys = among_nan(x, off, pad), among_nan(dy, off_dy, 8)
+        mp.mp_layernorm_forward(y.view, xs, w, b, mean=mean, rstd=rstd)
+        mp.mp_layernorm_backward(dx.view, dw, db, dys, xs, w, mean, rstd, workspace=ws)
+        (ry, rm, rr), (ty, tm, tr) = R.ln_forward(x, w, b, 1e-5)
+        (rdx, rdw, rdb), (tdx, tdw, tdb) = R.ln_backward(dy, x, w, mean, rstd)
+        for got, ref, tol, what in ((y.view, ry, ty, "y"), (dx.view, rdx, tdx, "dx"), (dw, rdw, tdw, "dweight"),
+                                    (db, rdb, tdb, "dbias")):
+            R.assert_within(got, ref, R.rounded(ref, tol, dtype), f"{what} {d} {dtype} {off} {off_dy} {out}")
+        y.check("y")
+        dx.check("dx")
+
+
 def test_binding_refusals(mp):
     x = torch.zeros(4, 8, dtype=BF, device="cuda")
     v, i = f32(4), torch.zeros(4, dtype=torch.int64, device="cuda")
