@@ -335,6 +335,10 @@ __device__ __forceinline__ void write_row(const LpArgs& a, int64_t r, RowStats s
     });
 }
 
+// The two halves of a cluster barrier, for every thread of the cluster.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
 // Short or few rows: a block, or the blocks of a cluster, read a row and
 // finish it.
 template <int T, bool Entropy, bool Top>
@@ -343,6 +347,10 @@ __global__ void __launch_bounds__(kLpThreads, 8) lp_forward_kernel(LpArgs a, int
   using E = typename Elem<T>::type;
   const cg::cluster_group cluster = cg::this_cluster();
   const int parts = cluster.num_blocks(), part = cluster.block_rank();
+  // The first block's shared memory may be written once that block runs and, in
+  // later rows, has finished the row before: the blocks arrive here and at each
+  // row's end, and wait only where they write to it.
+  if (parts > 1) cluster_arrive();
   __shared__ PartShared ps;
   __shared__ RowStats part_stats[kLpCluster];                     // of the first block: every block's
   __shared__ uint64_t part_keys[Top ? kLpCluster * kMaxTop : 1];  // likewise
@@ -371,6 +379,7 @@ __global__ void __launch_bounds__(kLpThreads, 8) lp_forward_kernel(LpArgs a, int
     }
     const uint64_t* keys = top.keys;
     if (parts > 1) {
+      cluster_wait();
       if (threadIdx.x == 0) *cluster.map_shared_rank(&part_stats[part], 0) = st;
       if (Top) {
         uint64_t* to = cluster.map_shared_rank(&part_keys[part * kMaxTop], 0);
@@ -386,7 +395,7 @@ __global__ void __launch_bounds__(kLpThreads, 8) lp_forward_kernel(LpArgs a, int
     }
     if (part == 0) write_row<T, Entropy, Top, BlockTeam>(a, r, st, c, keys, n, ps.stats);
     if (r + teams < a.rows) {  // before the next row's sums go where this row's were read
-      if (parts > 1) cluster.sync();
+      if (parts > 1) cluster_arrive();
       __syncthreads();
     }
   }
