@@ -105,7 +105,9 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 // resident warps to hold them. A copy moves the whole 16-B pieces of a row; the
 // fewer than 8 elements before and after them (rows that do not start or end on
 // a 16-B boundary) are loaded by threads and put beside them. A row lies in its
-// buffer at the offset that its address has from a 16-B boundary.
+// buffer at the offset that its address has from a 16-B boundary, so the next
+// row's copy may cover what was put there: the threads that did order it before
+// later copies (fence_to_bulk).
 template <int T, bool Wide>
 struct StagedRow {
   using E = typename Elem<T>::type;
@@ -268,8 +270,10 @@ __global__ void __launch_bounds__(kLnThreads, NV >= 8 ? 2 : NV >= 4 ? 3 : 4) ln_
   uint8_t* buffers = smem + 64 * units + static_cast<size_t>(group) * kStages * pitch;
   const int64_t step = static_cast<int64_t>(gridDim.x) * count;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * count + group;
-  if (threadIdx.x < kStages * count) mbar_init(smem_u32(&full[threadIdx.x]), 1);
-  if (threadIdx.x == 0) mbar_init_fence();
+  if (threadIdx.x < kStages * count) {
+    mbar_init(smem_u32(&full[threadIdx.x]), 1);
+    mbar_init_fence();
+  }
   __syncthreads();
   E edge0 = {}, edge1 = {};  // of the two stages
   auto fetch = [&](int64_t r, int stage) {  // by the group's first warp
@@ -315,6 +319,7 @@ __global__ void __launch_bounds__(kLnThreads, NV >= 8 ? 2 : NV >= 4 ? 3 : 4) ln_
       E* data = reinterpret_cast<E*>(buffers + stage * pitch + (Wide ? 0 : row.offset));
       if (!Wide) {
         if (t < row.head + row.tail) data[row.edge(t, a.d)] = stage ? edge1 : edge0;
+        if (t < 32) fence_to_bulk();
         meet();
       }
       Pack8<T> u[NV];
@@ -460,8 +465,8 @@ ln_backward_kernel(LnArgs a, float* part, uint32_t pitch, int stages) {
   if (t < stages) {
     mbar_init(smem_u32(&full[t]), 1);
     mbar_init(smem_u32(&freed[t]), 1);
+    mbar_init_fence();
   }
-  if (t == 0) mbar_init_fence();
   __syncthreads();
   // buffer of row i of x (which = 0) or dy (1) in a stage
   auto buffer = [&](int stage, int i, int which) { return smem + ((stage * R + i) * 2 + which) * pitch; };
@@ -514,6 +519,7 @@ ln_backward_kernel(LnArgs a, float* part, uint32_t pitch, int stages) {
         }
       }
       if (lane < N) stats[stage][lane] = stat;
+      if (!Wide) fence_to_bulk();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
       if (round + 1 < rounds) ahead(round + 1);

@@ -123,7 +123,7 @@ __device__ __forceinline__ void bulk_wait_read() {
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Orders this thread's earlier shared-memory writes before later bulk copies
-// that read them.
+// that read or overwrite them.
 __device__ __forceinline__ void fence_to_bulk() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 }  // namespace mpk
