@@ -313,8 +313,15 @@ __global__ void __launch_bounds__(kLnThreads, NV >= 8 ? 2 : NV >= 4 ? 3 : 4) ln_
 #pragma unroll 1
   for (int64_t r = first; r < a.rows; r += step, phase ^= stage, stage ^= 1) {
     {
-      // a wait that gives up (only a fault can cause that) makes what follows NaN
-      ok = ok && mbar_wait(smem_u32(&full[group * kStages + stage]), phase);
+      // A wait that gives up (only a fault can cause that) makes what follows
+      // NaN. Nothing more is fetched then, and the two copies in flight land first.
+      if (ok && !mbar_wait(smem_u32(&full[group * kStages + stage]), phase)) {
+        ok = false;
+        if (t == 0) {
+          mbar_drain(smem_u32(&full[group * kStages + stage]), phase);
+          if (r + step < a.rows) mbar_drain(smem_u32(&full[group * kStages + (stage ^ 1)]), phase ^ stage);
+        }
+      }
       const StagedRow<T, Wide> row(static_cast<const E*>(a.x) + r * a.x_stride, a.d);
       E* data = reinterpret_cast<E*>(buffers + stage * pitch + (Wide ? 0 : row.offset));
       if (!Wide) {
@@ -333,10 +340,10 @@ __global__ void __launch_bounds__(kLnThreads, NV >= 8 ? 2 : NV >= 4 ? 3 : 4) ln_
 #pragma unroll
         for (int e = 0; e < 8; ++e) s = __fadd_rn(s, f[e]);  // elements past the row are 0
       }
-      float mean = __fdiv_rn(group_sum(s, 0), n);
+      if (!ok) s = __int_as_float(0x7FC00000);
+      const float mean = __fdiv_rn(group_sum(s, 0), n);
       if (G == 1) __syncwarp();
       if (ok) fetch(r + kStages * step, stage);  // every thread of the group has read the buffer
-      if (!ok) mean = __int_as_float(0x7FC00000);
       float q = 0.0f;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
@@ -364,9 +371,6 @@ __global__ void __launch_bounds__(kLnThreads, NV >= 8 ? 2 : NV >= 4 ? 3 : 4) ln_
       }
     }
   }
-  // copies in flight land before the block ends
-  if (!ok && t == 0)
-    for (int i = 0; i < kStages; ++i) mbar_wait(smem_u32(&full[group * kStages + i]), phase ^ 1);
 }
 
 // Rows longer than the registers hold: three passes over the row, the later
@@ -530,7 +534,7 @@ ln_backward_kernel(LnArgs a, float* part, uint32_t pitch, int stages) {
     }
     // copies in flight land before the block ends
     if (lane == 0)
-      for (int i = max(0, round - stages); i < round; ++i) mbar_wait(smem_u32(&full[i % stages]), (i / stages) & 1);
+      for (int i = max(0, round - stages); i < round; ++i) mbar_drain(smem_u32(&full[i % stages]), (i / stages) & 1);
     return;
   }
   const float inv_d = __fdiv_rn(1.0f, static_cast<float>(a.d));
@@ -557,7 +561,8 @@ ln_backward_kernel(LnArgs a, float* part, uint32_t pitch, int stages) {
 #pragma unroll 1
   for (int round = 0; round < rounds; ++round) {
     const int64_t r0 = begin + static_cast<int64_t>(round) * R;
-    // a wait that gives up (only a fault can cause that) makes the sums NaN
+    // A wait that gives up (only a fault can cause that) makes the sums NaN, and
+    // the stage, whose copies may still be in flight, is not given back.
     ok = ok && mbar_wait(smem_u32(&full[stage]), phase);
     float rstd[R], sums[N];
 #pragma unroll
@@ -598,7 +603,7 @@ ln_backward_kernel(LnArgs a, float* part, uint32_t pitch, int stages) {
     const float part_sum = many_sum<N>(sums);
     if (lane % (32 / N) == 0) red[round & 1][warp][many_index<N>(lane)] = part_sum;
     asm volatile("bar.sync 1, %0;" ::"r"(L) : "memory");
-    if (t == 0) mbar_arrive(smem_u32(&freed[stage]));
+    if (t == 0 && ok) mbar_arrive(smem_u32(&freed[stage]));
     float total = 0.0f;
     for (int q = lane % (32 / N); q < warps; q += 32 / N)
       total = __fadd_rn(total, red[round & 1][q][many_index<N>(lane)]);
@@ -644,7 +649,7 @@ ln_backward_kernel(LnArgs a, float* part, uint32_t pitch, int stages) {
       if (cols.has(v, e)) {
         const int j = cols.at(v, e);
         pw[j] = ok ? dw[v][e] : __int_as_float(0x7FC00000);
-        pw[a.d + j] = db[v][e];
+        pw[a.d + j] = ok ? db[v][e] : __int_as_float(0x7FC00000);
       }
 }
 

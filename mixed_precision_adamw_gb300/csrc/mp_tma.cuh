@@ -5,7 +5,7 @@
 // A bulk load (cp.async.bulk global -> shared) completes on an mbarrier that
 // was told how many bytes to expect; a bulk store (shared -> global) is
 // tracked by bulk groups. Both need 16-B aligned addresses and sizes that are
-// multiples of 16 B. Every wait here gives up after kTmaWaitLimitNs of the
+// multiples of 16 B. Every wait here gives up after a second of the
 // global timer and reports it, so that a kernel can record an error and end
 // instead of spinning forever.
 #pragma once
@@ -14,7 +14,14 @@
 
 namespace mpk {
 
-constexpr uint64_t kTmaWaitLimitNs = 1000000000ull;  // one second
+// Limits of the waits: one second. A build with a shorter limit of the waits
+// that a kernel may give up shows what it does then; those in which the copies
+// in flight land before a block ends keep theirs.
+#ifndef MP_WAIT_LIMIT_NS
+#define MP_WAIT_LIMIT_NS 1000000000ull
+#endif
+constexpr uint64_t kTmaWaitLimitNs = MP_WAIT_LIMIT_NS;
+constexpr uint64_t kTmaDrainLimitNs = 1000000000ull;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -66,14 +73,34 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return done != 0;
 }
 
+// The same without suspending the thread for a while.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
 // Waits until the barrier's phase of the given parity has completed; false
-// if that took longer than kTmaWaitLimitNs.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+// if that took longer than `limit_ns` (0: if it has not yet).
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns = kTmaWaitLimitNs) {
+  if (limit_ns == 0) return mbar_test(bar, parity);
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_ns();
   while (!mbar_try_wait(bar, parity))
-    if (global_ns() - t0 > kTmaWaitLimitNs) return false;
+    if (global_ns() - t0 > limit_ns) return false;
   return true;
+}
+
+// The wait for copies that must land before a block ends, also after another
+// wait has given up.
+__device__ __forceinline__ bool mbar_drain(uint32_t bar, uint32_t parity) {
+  return mbar_wait(bar, parity, kTmaDrainLimitNs);
 }
 
 // An L2 policy that evicts the lines a copy touches first.
