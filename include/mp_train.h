@@ -178,6 +178,9 @@ int mp_token_logprob_backward(void* dlogits, const void* logits, const void* tar
  * -inf throughout has a zero gradient. NaN or +inf among a row's logits
  * makes its loss and gradient NaN, among its listed teacher logits the loss
  * and the gradient of the listed tokens.
+ * Should a wait inside the kernel run out (after a second; a fault of the GPU),
+ * every row that is not whole has loss NaN and dlogits[r][0] NaN, and
+ * MP_ERR_CUDA is stored into *d_status (if it held 0).
  * Errors: MP_ERR_NULL, MP_ERR_ALIGN, MP_ERR_RANGE, MP_ERR_CUDA.
  * ------------------------------------------------------------------------- */
 int mp_distill_topk(float* loss, void* dlogits, const void* logits, const void* teacher, const void* index,

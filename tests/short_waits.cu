@@ -1,5 +1,5 @@
-// The layer norm kernels in a library of their own whose waits for the copies
-// run out at once (MP_WAIT_LIMIT_NS = 0; compiled by
+// The layer norm and distillation kernels in a library of their own whose
+// waits run out at once (MP_WAIT_LIMIT_NS = 0; compiled by
 // test_gpu_train_give_up.py), with what they need of the rest.
 #include "mp_internal.h"
 

@@ -26,7 +26,7 @@ def short(tmp_path_factory):
     from mixed_precision_adamw_gb300 import build as B
     out = tmp_path_factory.mktemp("short_waits")
     sources = [os.path.join(os.path.dirname(os.path.abspath(__file__)), "short_waits.cu"),
-               os.path.join(B.CSRC, "mp_layernorm.cu")]
+               os.path.join(B.CSRC, "mp_layernorm.cu"), os.path.join(B.CSRC, "mp_distill.cu")]
 
     def compile(src):
         obj = str(out / (os.path.basename(src) + ".o"))
@@ -107,3 +107,31 @@ def layernorm_case(short, rows, d, pad, dtype):
     return (gave_y, gave_mean, right_or_nan(dx, rdx, R.rounded(rdx, tdx, dtype), "dx"),
             right_or_nan(dw, rdw, R.rounded(rdw, tdw, FF), "dweight"),
             right_or_nan(db, rdb, R.rounded(rdb, tdb, FF), "dbias"))
+
+
+@pytest.mark.parametrize("dtype,vocab,in_place", [(BF, 50304, False), (BF, 128256, True), (FF, 60000, True)])
+def test_distill_gives_up(short, dtype, vocab, in_place):
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    rows, k = 470, 40
+    x = (torch.randn(rows, vocab, generator=g, device="cuda") * 2).to(dtype)
+    idx = torch.rand(rows, vocab, generator=g, device="cuda").topk(k, dim=1).indices
+    t = torch.randn(rows, k, generator=g, device="cuda").to(dtype)
+    w = torch.rand(rows, generator=g, device="cuda") + 0.5
+    w[::7] = 0.0
+    (rl, rd), (tl, td) = R.distill(x, t, idx, w, 1.0)
+    logits = x.clone()
+    dx = logits if in_place else torch.full_like(x, 7.0)
+    loss, status = torch.full((rows,), 7.0, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    torch.full((1 << 29,), 1, dtype=torch.uint8, device="cuda")  # x is not in L2: loads take their time
+    torch.cuda.synchronize()
+    args = (ptr(x if not in_place else logits), ptr(t), ptr(idx), ptr(w), *i64(rows, vocab), ctypes.c_int32(k),
+            *i64(vocab, vocab, k, k), ctypes.c_float(1.0), ctypes.c_int32(0 if dtype == BF else 2), ctypes.c_int32(1))
+    assert short.mp_distill_topk(ptr(loss), ptr(dx), *args, ptr(status), None) == 0
+    torch.cuda.synchronize()
+    gave = torch.isnan(loss)
+    assert gave.any() and int(status) == 6, "no wait gave up"
+    assert torch.isnan(dx[gave, 0]).all(), "a row that gave up has a gradient that looks whole"
+    right_or_nan(loss, rl, tl, "loss")
+    ok = (dx.double() - rd).abs() <= R.rounded(rd, td, dtype)
+    ok[:, 0] |= torch.isnan(dx[:, 0])  # a row may be marked although it was whole
+    assert ok[~gave].all(), "a row that did not give up is wrong"
