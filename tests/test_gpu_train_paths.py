@@ -114,3 +114,98 @@ def test_layernorm_stages_used_again_at_other_offsets(mp, rows, d, dtype, pad):
     g = gen(rows)
     x, dy = among_nan(randn((rows, d), g, 1.5, dtype), 1, pad), among_nan(randn((rows, d), g, 1.0, dtype), 3, pad + 2)
     ln_check(mp, x, dy, 1 + randn((d,), g, 0.2), randn((d,), g, 0.3), what=f"pad {pad}")
+
+
+# --- finite logits of large magnitude ------------------------------------------------
+
+MASKS = [-1e9, -1e10, -1e12, -1e30, "lowest / 4"]
+
+
+def masked_rows(rows, vocab, dtype, value, seed):
+    """Logits whose rows are masked in turn by the value: not at all, over the first half, all but one token, all
+    of them, the last half, and a row that lies at its negative."""
+    low = torch.finfo(dtype).min
+    value = low / 4 if isinstance(value, str) else value
+    x = randn((rows, vocab), gen(seed), 2.0, dtype)
+    x[1::6, : vocab // 2] = value
+    keep = x[2::6, vocab // 3].clone()
+    x[2::6] = value
+    x[2::6, vocab // 3] = keep
+    x[3::6] = value
+    x[4::6, vocab // 2:] = value
+    x[5::6] = -value
+    return x
+
+
+def chains_of_a_warp(monkeypatch):
+    # rows far from 0 are summed by one warp or one block: n / 32 additions after one another
+    monkeypatch.setattr(R, "depth", lambda n: 96 + n / 32)
+
+
+def lp_large(mp, x, scale, k, entropy=True, slices=1):
+    rows, vocab = x.shape
+    t = torch.randint(0, vocab, (rows,), generator=gen(7), device="cuda")
+    t[2::6] = vocab // 3
+    logp, lse, ent = f32(rows), f32(rows), f32(rows) if entropy else None
+    tl = f32(rows, k) if k else None
+    ti = torch.full((rows, k), -9, dtype=torch.int32, device="cuda") if k else None
+    mp.mp_token_logprob_forward(x, t, logp=logp, lse=lse, entropy=ent, top_logp=tl, top_index=ti, scale=scale)
+    torch.cuda.synchronize()
+    step = (rows + slices - 1) // slices
+    for a in range(0, rows, step):
+        s = slice(a, min(rows, a + step))
+        ref, tol = R.lp_forward(x[s], t[s], scale, k)
+        # log p comes from differences of logits, whatever the size of lse: R's bound of log(sum), and the difference's
+        z, m, e, sums, _ = R._stats(x[s], scale)
+        p = e / sums
+        dist = torch.where(p > 0, p * (m - z), 0.0).sum(1)
+        log_s = torch.log(sums)[:, 0]
+        t_log_s = (R.depth(vocab) + 6) * R.U + 3 * R.U * dist + 2 * R.U * log_s.abs()
+        tol["logp"] = t_log_s + 4 * R.U * ref["logp"].abs()
+        if k:
+            tol["top_logp"] = t_log_s[:, None] + 4 * R.U * ref["top_logp"].abs()
+            assert torch.equal(ti[s], ref["top_index"]), "top_index"
+        for name, got in (("lse", lse), ("logp", logp), ("entropy", ent), ("top_logp", tl)):
+            if got is not None:
+                R.assert_within(got[s], ref[name], tol[name], f"{rows}x{vocab} {x.dtype} {name}")
+
+
+@pytest.mark.parametrize("scale", [0.5, 1.0, 1 / 0.6])
+@pytest.mark.parametrize("value", MASKS)
+@pytest.mark.parametrize("dtype", [BF, FF])
+def test_logprob_large_masks(mp, monkeypatch, dtype, value, scale):
+    chains_of_a_warp(monkeypatch)
+    for rows, vocab in ((6, 8192), (6, 131), (6, 50304), (300, 5000)):
+        lp_large(mp, masked_rows(rows, vocab, dtype, value, rows), scale, 5)
+    lp_large(mp, masked_rows(6, 8192, dtype, value, 3)[1:2], scale, 0)
+
+
+@pytest.mark.parametrize("value", MASKS)
+@pytest.mark.parametrize("dtype", [BF, FF])
+def test_logprob_large_masks_many_long_rows(mp, monkeypatch, dtype, value):
+    chains_of_a_warp(monkeypatch)
+    lp_large(mp, masked_rows(2100, 16391, dtype, value, 4), 1.0, 5, slices=4)
+
+
+@pytest.mark.parametrize("scale", [0.5, 1.0, 1 / 0.6])
+@pytest.mark.parametrize("value", MASKS)
+@pytest.mark.parametrize("dtype", [BF, FF])
+def test_distill_large_masks(mp, monkeypatch, dtype, value, scale):
+    chains_of_a_warp(monkeypatch)
+    for rows, vocab in ((6, 8192), (6, 131), (300, 5000), (6, 128256), (400, 40000)):
+        x = masked_rows(rows, vocab, dtype, value, rows)
+        g = gen(8)
+        idx = torch.rand(rows, vocab, generator=g, device="cuda").topk(12, dim=1).indices
+        idx[1::6] = vocab // 2 + idx[1::6] % (vocab // 2)
+        idx[2::6] = vocab // 3
+        idx[4::6] %= vocab // 2
+        t = randn((rows, 12), g, 2.0, dtype)
+        (rl, rd), (tl, td) = R.distill(x, t, idx, None, scale)
+        loss, dx, alone = f32(rows), torch.full_like(x, -7.0), f32(rows)
+        mp.mp_distill_topk(loss, dx, x, t, idx, scale=scale)
+        mp.mp_distill_topk(alone, None, x, t, idx, scale=scale)
+        torch.cuda.synchronize()
+        what = f"{rows}x{vocab} {dtype} {value} {scale}"
+        R.assert_within(loss, rl, tl, what + " loss")
+        R.assert_within(alone, rl, tl, what + " loss alone")
+        R.assert_within(dx, rd, R.rounded(rd, td, dtype), what + " dlogits")
