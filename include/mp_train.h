@@ -105,13 +105,14 @@ int mp_layernorm_backward(void* dx, void* dweight, void* dbias, const void* dy, 
  *   targets     [rows] of `index_type`; negative: no given token (logp 0).
  *               A target >= vocab gives logp NaN and stores MP_ERR_RANGE into
  *               *d_status (if it held 0); nothing is read out of range.
- *   rows >= 0 (0 is a no-op), vocab in [1, 2^31 - 1], scale finite and > 0,
+ *   rows >= 0 (0 is a no-op), vocab in [1, 2^31 - 1], 0 < scale <= 2^126,
  *   0 <= top_k <= min(32, vocab).
  *   d_status    int32[1], may be NULL.
  * Masked tokens have logit -inf: probability 0, and no part in the entropy.
  * A row that is -inf throughout has lse -inf, logp -inf and entropy 0. A row
  * that holds NaN or +inf has lse, logp, entropy and top_logp NaN; in the order
- * of the alternatives NaN ranks above +inf.
+ * of the alternatives NaN ranks above +inf. Differences of a row's logits are
+ * fp32: more than 3.4e38 below the largest counts as -inf.
  * Errors: MP_ERR_NULL, MP_ERR_ALIGN, MP_ERR_RANGE, MP_ERR_CUDA.
  * ------------------------------------------------------------------------- */
 int mp_token_logprob_forward(float* logp, float* lse, float* entropy, float* top_logp, int32_t* top_index,
@@ -170,8 +171,8 @@ int mp_token_logprob_backward(void* dlogits, const void* logits, const void* tar
  *               MP_ERR_RANGE into *d_status (if it held 0).
  *   row_weight  float[rows], or NULL: ones. A row of weight 0 has loss 0 and a
  *               zero gradient, whatever its logits hold.
- *   rows >= 0 (0 is a no-op), vocab in [1, 2^31 - 1], k in [1, 1024], scale
- *   finite and > 0.
+ *   rows >= 0 (0 is a no-op), vocab in [1, 2^31 - 1], k in [1, 1024],
+ *   0 < scale <= 2^126.
  * A teacher logit of -inf has q = 0 and adds nothing. A row without a listed
  * token of q > 0 has loss 0 and a zero gradient. A listed token of q > 0
  * whose student logit is -inf makes the loss +inf. A student row that is

@@ -21,7 +21,7 @@ inline bool index_type_ok(int32_t t) { return t == MP_INT32 || t == MP_INT64; }
 inline bool rows_ok(int64_t rows) { return rows >= 0 && rows < kMaxRows; }
 inline bool vocab_ok(int64_t vocab) { return vocab >= 1 && vocab <= INT32_MAX; }
 inline bool stride_ok(int64_t stride, int64_t length) { return stride >= length && stride < kMaxRows; }
-inline bool scale_ok(float scale) { return scale > 0.0f && std::isfinite(scale); }
+inline bool scale_ok(float scale) { return scale > 0.0f && scale <= 0x1p126f; }  // scale * log2(e) is finite
 inline bool aligned_to(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 inline bool aligned4(const void* p) { return aligned_to(p, 4); }
 inline bool type_aligned(const void* p, int32_t t) { return aligned_to(p, t == MP_FP32 ? 4 : 2); }

@@ -209,3 +209,25 @@ def test_distill_large_masks(mp, monkeypatch, dtype, value, scale):
         R.assert_within(loss, rl, tl, what + " loss")
         R.assert_within(alone, rl, tl, what + " loss alone")
         R.assert_within(dx, rd, R.rounded(rd, td, dtype), what + " dlogits")
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 126, 2.0 ** -126])
+def test_extreme_scales(mp, scale):
+    # the largest scale accepted; equal logits, and logits whose scaled differences are far apart or nearly 0
+    x = torch.zeros(3, 900, device="cuda")
+    x[1] = torch.arange(900, device="cuda") * 2.0 ** -120
+    x[2] = torch.arange(900, device="cuda").float()
+    t = torch.tensor([5, 899, 899], device="cuda")
+    logp, lse, ent = f32(3), f32(3), f32(3)
+    mp.mp_token_logprob_forward(x, t, logp=logp, lse=lse, entropy=ent, scale=scale)
+    z = x.double() * scale
+    p = torch.log_softmax(z, 1)
+    ref = p.gather(1, t[:, None])[:, 0]
+    tol = 200 * R.U * (1 + math.log(900))
+    assert ((logp.double() - ref).abs() <= tol).all()
+    assert ((ent.double() - torch.special.entr(p.exp()).sum(1)).abs() <= tol).all()
+    loss, dx = f32(3), torch.empty_like(x)
+    mp.mp_distill_topk(loss, dx, x, torch.zeros(3, 1, device="cuda"), t[:, None], scale=scale)
+    assert ((loss.double() + ref).abs() <= tol).all()
+    one = torch.nn.functional.one_hot(t, 900)
+    assert (((dx.double() / scale) - (p.exp() - one)).abs() <= tol).all()

@@ -1,0 +1,14 @@
+"""Limits of the training-head operators' arguments (no GPU needed: every call
+here is refused, or has nothing to do, before any device work)."""
+import pytest
+
+from test_train_args import DST, LPB, LPF, call, mp  # noqa: F401
+
+
+@pytest.mark.parametrize("name,base", [("mp_token_logprob_forward", LPF), ("mp_token_logprob_backward", LPB),
+                                       ("mp_distill_topk", DST)])
+def test_scale_limit(mp, name, base):  # noqa: F811
+    # scale * log2(e) has to be finite in fp32
+    for scale, status in ((2.0 ** 126, mp.MP_OK), (2.0 ** 126 * (1 + 2.0 ** -23), mp.MP_ERR_RANGE),
+                          (3e38, mp.MP_ERR_RANGE), (2.0 ** -149, mp.MP_OK)):
+        assert call(mp, name, list(base), base, rows=0, scale=scale) == status, scale
