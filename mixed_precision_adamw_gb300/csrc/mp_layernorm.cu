@@ -1010,6 +1010,7 @@ extern "C" int mp_layernorm_backward(void* dx, void* dweight, void* dbias, const
   if (!type_ok(type) || !type_ok(weight_type) || !shape_ok(rows, d) || (dx && !stride_ok(dx_stride, d)) ||
       !stride_ok(dy_stride, d) || !stride_ok(x_stride, d))
     return MP_ERR_RANGE;
+  if (rows == 0 && !dweight && !dbias) return MP_OK;
   if (!dx && !dweight && !dbias) return MP_ERR_NULL;
   if (rows > 0 && (!dy || !x || !mean || !rstd)) return MP_ERR_NULL;
   if (dx && ((dx == dy && dx_stride != dy_stride) || (dx == x && dx_stride != x_stride))) return MP_ERR_RANGE;

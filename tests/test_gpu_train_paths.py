@@ -231,3 +231,13 @@ def test_extreme_scales(mp, scale):
     assert ((loss.double() + ref).abs() <= tol).all()
     one = torch.nn.functional.one_hot(t, 900)
     assert (((dx.double() / scale) - (p.exp() - one)).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("d", [64, 1000, 9000])
+def test_layernorm_backward_of_no_rows(mp, d):
+    x, none = torch.empty(0, d, dtype=BF, device="cuda"), torch.empty(0, device="cuda")
+    mp.mp_layernorm_backward(x.clone(), None, None, x, x, None, none, none)
+    dw = f32(d)
+    ws = torch.empty(mp.mp_layernorm_workspace_bytes(0, d), dtype=torch.uint8, device="cuda")
+    mp.mp_layernorm_backward(x.clone(), dw, None, x, x, None, none, none, workspace=ws)
+    assert (dw == 0).all()
