@@ -449,10 +449,11 @@ __device__ __forceinline__ int many_index(int lane) {
 // it takes to prepare a copy (hundreds of cycles) is off the others' path. One
 // barrier a round joins the computing warps' sums (which alternate between two
 // buffers) and says that the stage has been read. xh and dy stay in registers,
-// widened, from the sums to dx. For 16-bit types xh is one FMA, x rstd -
-// mean rstd: the second product's rounding is below what the input's own
-// rounding leaves of the difference. Rows past the block's last are staged as
-// zeros instead of being tested for.
+// widened, from the sums to dx. xh is taken from the difference x - mean: one
+// FMA, x rstd - mean rstd, saves an operation (57.8 us against 58.3 at 32768 x
+// 1600 bf16, 42.6 against 43.1 at 8192 x 4096), but leaves the rounding of mean
+// rstd in every xh of a row whose offset is large beside its spread. Rows past
+// the block's last are staged as zeros instead of being tested for.
 template <int T, bool Wide, int NV, int R, int MaxThreads, int MinBlocks>
 __global__ void __launch_bounds__(MaxThreads + 32, MinBlocks)
 ln_backward_kernel(LnArgs a, float* part, uint32_t pitch, int stages) {
@@ -575,7 +576,6 @@ ln_backward_kernel(LnArgs a, float* part, uint32_t pitch, int stages) {
       }
       const float mean = stats[stage][2 * i];
       rstd[i] = stats[stage][2 * i + 1];
-      const float shift = -__fmul_rn(mean, rstd[i]);
       float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
@@ -587,8 +587,7 @@ ln_backward_kernel(LnArgs a, float* part, uint32_t pitch, int stages) {
           cols.load(u, x, v);
           u.get(f);
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            xh[i][v][e] = T == MP_FP32 ? __fmul_rn(__fsub_rn(f[e], mean), rstd[i]) : __fmaf_rn(f[e], rstd[i], shift);
+          for (int e = 0; e < 8; ++e) xh[i][v][e] = __fmul_rn(__fsub_rn(f[e], mean), rstd[i]);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {

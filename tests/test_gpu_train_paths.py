@@ -241,3 +241,19 @@ def test_layernorm_backward_of_no_rows(mp, d):
     ws = torch.empty(mp.mp_layernorm_workspace_bytes(0, d), dtype=torch.uint8, device="cuda")
     mp.mp_layernorm_backward(x.clone(), dw, None, x, x, None, none, none, workspace=ws)
     assert (dw == 0).all()
+
+
+# --- layer norm of rows with a common offset -------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF, HF, FF])
+@pytest.mark.parametrize("d", [96, 200, 768, 1357, 1600, 4096, 4100, 5632, 8192, 9001])
+def test_layernorm_common_offset(mp, d, dtype):
+    # a row's values lie around one offset a thousand times their spread (fp32), or as far out as the type tells them
+    # apart; constant rows, whose normalised values are 0 and whose 1/std is the largest; fp32 weight gradients
+    g = gen(d)
+    rows = 300
+    at = {BF: 100.0, HF: 1000.0, FF: 1500.0}[dtype]
+    x = (randn((rows, d), g, 1.5) + at * torch.where(torch.rand(rows, 1, generator=g, device="cuda") < 0.5, -1.0, 1.0)).to(dtype)
+    x[::3] = (torch.arange(100, device="cuda") * 41.0 - 2000.0)[:, None].to(dtype)
+    dy = randn((rows, d), g, 1.0, dtype)
+    ln_check(mp, x, dy, 1 + randn((d,), g, 0.2), randn((d,), g, 0.3), what="offset")
