@@ -257,3 +257,88 @@ def test_layernorm_common_offset(mp, d, dtype):
     x[::3] = (torch.arange(100, device="cuda") * 41.0 - 2000.0)[:, None].to(dtype)
     dy = randn((rows, d), g, 1.0, dtype)
     ln_check(mp, x, dy, 1 + randn((d,), g, 0.2), randn((d,), g, 0.3), what="offset")
+
+
+# --- the kernels of many rows ------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF, HF, FF])
+@pytest.mark.parametrize("d", [264, 520, 1024, 1600, 2048, 2056, 4096, 4104, 8192, 261, 1013, 1029, 2047, 4099, 8191])
+def test_layernorm_warps_of_a_row(mp, d, dtype):
+    # row counts on either side of those at which fewer warps take a row: from one to eight, one to eight units a thread
+    g = gen(d)
+    for rows in (37, 151, 153, 303, 305, 607, 609, 1215, 1217, 2500):
+        x, dy = randn((rows, d), g, 1.5, dtype), randn((rows, d), g, 1.0, dtype)
+        ln_check(mp, x, dy, 1 + randn((d,), g, 0.2), randn((d,), g, 0.3), slices=1)
+
+
+def hard_rows(x, every):
+    """Rows that go wrong first, where one block takes every `every`-th row: three of them one after the other."""
+    dtype, vocab = x.dtype, x.shape[1]
+    kinds = [
+        lambda r: r.fill_(-INF),
+        lambda r: r.fill_(torch.finfo(dtype).min),
+        lambda r: r[vocab // 2].fill_(math.nan),
+        lambda r: r[vocab // 3].fill_(INF),
+        lambda r: r.fill_(0.5),                                            # all equal
+        lambda r: r.copy_(torch.sort(r.float()).values.to(dtype)),         # rising
+        lambda r: r.copy_(torch.sort(r.float(), descending=True).values.to(dtype)),
+        lambda r: r.copy_(r.float().round().clamp(-2, 2).to(dtype)),       # thousands of equal ones at the top
+        lambda r: r[: vocab - 1].fill_(-INF),                              # one token
+        lambda r: r[: vocab // 2].fill_(-1e4),
+        lambda r: r.fill_(math.nan),
+        lambda r: r[7:].copy_(r[7:] * 0),
+        lambda r: r.fill_(-3e4),
+    ]
+    n = 0
+    for block in range(len(kinds)):
+        for turn in range(block, x.shape[0], every):
+            kinds[n % len(kinds)](x[turn])
+            n += 1
+        n += 1  # the next block begins with another
+
+
+@pytest.mark.parametrize("entropy", [True, False])
+@pytest.mark.parametrize("k", [0, 1, 32])
+@pytest.mark.parametrize("dtype", [BF, HF, FF])
+def test_logprob_many_long_rows(mp, monkeypatch, dtype, k, entropy):
+    chains_of_a_warp(monkeypatch)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    # either side of the row count and of the vocabulary from which blocks read one row after the other
+    for rows, vocab, pad, off in ((12 * sms - 1, 16384, 0, 0), (12 * sms, 16384, 8, 0), (12 * sms + 276, 16383, 1, 0),
+                                  (12 * sms + 276, 16391, 3, 5), (12 * sms + 276, 50304, 0, 0), (3000, 20001, 0, 1)):
+        x = randn((rows, vocab), gen(rows + vocab), 2.0, dtype)
+        hard_rows(x, 6 * sms)
+        x = among_nan(x, off, pad)
+        lp_any(mp, x, k, entropy)
+
+
+def lp_any(mp, x, k, entropy, slices=6):
+    rows, vocab = x.shape
+    t = torch.randint(0, vocab, (rows,), generator=gen(9), device="cuda", dtype=torch.int32)
+    t[5::11] = -1
+    outs = []
+    for _ in range(3):
+        o = {"lse": f32(rows), "logp": f32(rows)}
+        if entropy:
+            o["entropy"] = f32(rows)
+        if k:
+            o["top_logp"] = f32(rows, k)
+            o["top_index"] = torch.full((rows, k), -9, dtype=torch.int32, device="cuda")
+        mp.mp_token_logprob_forward(x, t, **o)
+        outs.append(o)
+    torch.cuda.synchronize()
+    for o in outs[1:]:  # the same bits on every run (NaN included)
+        assert all(torch.equal(v.view(torch.int32), outs[0][n].view(torch.int32)) for n, v in o.items())
+    step = (rows + slices - 1) // slices
+    for a in range(0, rows, step):
+        s = slice(a, min(rows, a + step))
+        ref, tol = R.lp_forward(x[s], t[s], 1.0, k)
+        given = t[s] >= 0
+        assert (outs[0]["logp"][s][~given] == 0).all()  # exactly, whatever the row holds
+        for name, got in outs[0].items():
+            if name == "logp":
+                R.assert_within(got[s][given], ref[name][given], tol[name][given], f"{rows}x{vocab} {x.dtype} logp")
+            elif name == "top_index":
+                assert torch.equal(got[s], ref[name]), f"{rows}x{vocab} {x.dtype} top_index"
+            else:
+                R.assert_within(got[s], ref[name], tol[name], f"{rows}x{vocab} {x.dtype} {name}")
