@@ -342,3 +342,24 @@ def lp_any(mp, x, k, entropy, slices=6):
                 assert torch.equal(got[s], ref[name]), f"{rows}x{vocab} {x.dtype} top_index"
             else:
                 R.assert_within(got[s], ref[name], tol[name], f"{rows}x{vocab} {x.dtype} {name}")
+
+
+@pytest.mark.parametrize("dtype", [BF, FF])
+@pytest.mark.parametrize("rows,vocab", [(1, 4099), (1, 128256), (3, 50261), (40, 20001), (300, 5000)])
+def test_logprob_gradient_over_split_rows(mp, rows, vocab, dtype):
+    # a row over its own logits by several blocks; the given token in each of their parts, and at the row's ends
+    g = gen(vocab)
+    x = randn((rows, vocab), g, 2.0, dtype)
+    dlogp, dent = randn((rows,), g), randn((rows,), g)
+    for at in (0, 1, vocab // 3, vocab // 2, vocab - 9, vocab - 1):
+        t = torch.full((rows,), at, device="cuda")
+        t[rows // 2:] = vocab - 1 - at
+        logp, lse, ent = f32(rows), f32(rows), f32(rows)
+        mp.mp_token_logprob_forward(x, t, logp=logp, lse=lse, entropy=ent)
+        apart, over = torch.empty_like(x), x.clone()
+        kw = dict(lse=lse, dlogp=dlogp, entropy=ent, dentropy=dent)
+        mp.mp_token_logprob_backward(apart, x, t, **kw)
+        mp.mp_token_logprob_backward(over, over, t, **kw)
+        rd, td = R.lp_backward(x, t, lse, ent, dlogp, dent, 1.0)
+        R.assert_within(apart, rd, R.rounded(rd, td, dtype), f"{at}")
+        assert torch.equal(over, apart)
