@@ -263,6 +263,7 @@ __global__ void __launch_bounds__(kLnThreads, NV >= 8 ? 2 : NV >= 4 ? 3 : 4) ln_
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float red[2][kLnThreads / 32];
   __shared__ unsigned long long full[kStages * kLnThreads / 32];
+  __shared__ uint32_t gave_up[kLnThreads / 32];  // stage + 2 phase of the wait that a group's first thread gave up
   const int64_t units = (a.d + 7) / 8;
   float* sw = reinterpret_cast<float*>(smem);
   const int L = 32 * G, t = threadIdx.x % L, group = threadIdx.x / L, count = kLnThreads / L;
@@ -313,14 +314,11 @@ __global__ void __launch_bounds__(kLnThreads, NV >= 8 ? 2 : NV >= 4 ? 3 : 4) ln_
 #pragma unroll 1
   for (int64_t r = first; r < a.rows; r += step, phase ^= stage, stage ^= 1) {
     {
-      // A wait that gives up (only a fault can cause that) makes what follows
-      // NaN. Nothing more is fetched then, and the two copies in flight land first.
+      // a wait that gives up (only a fault can cause that) makes what follows NaN,
+      // and nothing more is fetched
       if (ok && !mbar_wait(smem_u32(&full[group * kStages + stage]), phase)) {
         ok = false;
-        if (t == 0) {
-          mbar_drain(smem_u32(&full[group * kStages + stage]), phase);
-          if (r + step < a.rows) mbar_drain(smem_u32(&full[group * kStages + (stage ^ 1)]), phase ^ stage);
-        }
+        if (t == 0) gave_up[group] = stage + 2 * phase;
       }
       const StagedRow<T, Wide> row(static_cast<const E*>(a.x) + r * a.x_stride, a.d);
       E* data = reinterpret_cast<E*>(buffers + stage * pitch + (Wide ? 0 : row.offset));
@@ -370,6 +368,14 @@ __global__ void __launch_bounds__(kLnThreads, NV >= 8 ? 2 : NV >= 4 ? 3 : 4) ln_
         if (a.rstd_out) a.rstd_out[r] = rstd;
       }
     }
+  }
+  // The copy that was waited for and the one after it (if there was one) land
+  // before the block ends.
+  if (!ok && t == 0) {
+    stage = gave_up[group] % 2;
+    phase = gave_up[group] / 2;
+    mbar_drain(smem_u32(&full[group * kStages + stage]), phase);
+    mbar_drain(smem_u32(&full[group * kStages + (stage ^ 1)]), phase ^ stage);
   }
 }
 
