@@ -508,8 +508,7 @@ __global__ void __launch_bounds__(kLpThreads) lp_backward_kernel(LpArgs a, int p
     const float a1 = __fmul_rn(-scale, h);
     // the target's element is written by one thread of the block whose part it is
     // in, from the value read before that part is overwritten
-    const bool mine = t >= 0 && out.holds(t);
-    const float xt = mine ? Elem<T>::get(x[t]) : 0.0f;
+    const float xt = t >= 0 && (parts == 1 || out.holds(t)) ? Elem<T>::get(x[t]) : 0.0f;
     __syncthreads();
     auto of = [&](float v) {
       const float y = __fmaf_rn(v, scale, -lse);
@@ -524,7 +523,7 @@ __global__ void __launch_bounds__(kLpThreads) lp_backward_kernel(LpArgs a, int p
     else
       map_row<T, false>(out, dx, x, of);
     __syncthreads();
-    if (mine && threadIdx.x == 0) dx[t] = Elem<T>::put(__fmaf_rn(g, scale, of(xt)));
+    if (t >= 0 && threadIdx.x == 0 && out.holds(t)) dx[t] = Elem<T>::put(__fmaf_rn(g, scale, of(xt)));
   }
 }
 
