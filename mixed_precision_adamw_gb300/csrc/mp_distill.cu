@@ -6,9 +6,10 @@
 // second reads the row out of L2 where the rows in flight fit (6 blocks an SM,
 // 91 MB at 50304 logits of 16 bits), so that HBM sees each logit read once and
 // each gradient written once: 4 B an element for 16-bit types. The listed
-// tokens (few) are corrected afterwards by one thread each. Few rows are split
+// tokens (few) are corrected afterwards by one thread each. Six blocks an SM
+// leave a thread 80 registers, and 36 to 64 bytes of it spill. Few rows are split
 // over the blocks of a cluster. Many long rows take the ring below, which holds
-// most of a row in shared memory instead (8192 x 50304 bf16: 336 us).
+// most of a row in shared memory instead (8192 x 50304 bf16: 339 us).
 #include "mp_device.cuh"
 #include "mp_internal.h"
 #include "mp_softmax.cuh"
@@ -704,9 +705,11 @@ __global__ void __launch_bounds__(kRingBlock, 1) distill_ring_kernel(DsArgs a) {
       st = st.join(c);
       const float A = __fdiv_rn(__fmul_rn(sh.list[set].w, a.scale), st.s), ref = st.ref;
       const bool zero = sh.list[set].none || ref == -kInf;
-      // A 2^((x - ref) c) as 2^(c x + B): two operations fewer an element. The
-      // rounding of B, where |B| < 64, is a relative error below 2^-19 of the
-      // gradient; 16-bit types round it by 2^-12 or more. Other rows, and fp32,
+      // A 2^((x - ref) c) as 2^(c x + B): two operations fewer an element. B, where
+      // |B| and |ref c| are below 64, is off by half a step of 2^-18 for its own
+      // rounding and for that of ref c, and by a step of log2(A), 2^-17 below 128:
+      // below 2^-16, a relative error below 2^-16.5 of the gradient, which is then
+      // rounded by up to 2^-11 (fp16) or 2^-8 (bf16) of it. Other rows, and fp32,
       // take the difference first.
       const float B = __fsub_rn(log2f(A), __fmul_rn(ref, c));
       const bool folded = T != MP_FP32 && fabsf(B) < 64.0f && fabsf(__fmul_rn(ref, c)) < 64.0f;

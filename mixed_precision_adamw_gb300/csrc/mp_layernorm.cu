@@ -39,7 +39,7 @@ struct LnArgs {
 // group) have a span of the row, in which neighbouring lanes take neighbouring
 // elements; whatever the lane and the warp add to a column is in `first`, the
 // rest is a constant of the access (bf16, forward and backward: 32768 x 1357
-// 60 and 91 us; 136 and 139 with neighbours over the whole group, whose
+// 62 and 92 us; 136 and 139 with neighbours over the whole group, whose
 // addresses and tests are computed for each element).
 template <bool Wide, int NV, int S = 32>
 struct Columns {
@@ -916,14 +916,15 @@ cudaError_t backward_wide(const LnArgs& a, const LnPlan& p, float* part, cudaStr
   // such warps fill the register file. 32768 x 1600 bf16: 58 us; four rows a
   // round 83 (spilled registers), 24 warps of 80 registers 86. Longer rows take
   // more units in fewer warps; 8192 rows of bf16, us:
-  //   d     2 units, 2 rows   2 units, 1 row   3 units, 1 row   2 units, 1 row
-  //         168 registers     128              168              96 (spilled)
-  //   5632  56                62                                81
-  //   6144                    64               70               85
-  //   7680                    72               80               104
-  //   8192                                     82               108
-  // 4096 with one unit and two rows: 42, although 96 registers a thread spill 16
-  // bytes; two units of 168 registers 45.
+  //   d     2 units, 2 rows   2 units, 1 row   3 units, 1 row    2 units, 1 row
+  //         168 registers     128              168 (12-28 B      96 (spilled)
+  //                                            of it spill)
+  //   5632  55                62                                 81
+  //   6144                    62               70                85
+  //   7680                    71               80                104
+  //   8192                                     82                108
+  // 4096 with one unit and two rows: 43, although 12 to 32 bytes of the 96
+  // registers a thread spill; two units of 168 registers 45.
   if (p.units == 3) return backward_staged<T, Wide, 3, 1, 352, 1>(a, p, part, s);
   if (p.units == 2 && p.threads > 352) return backward_staged<T, Wide, 2, 1, 480, 1>(a, p, part, s);
   if (p.units == 2) return backward_staged<T, Wide, 2, 2, 352, 1>(a, p, part, s);
