@@ -138,7 +138,7 @@ int mp_token_logprob_forward(float* logp, float* lse, float* entropy, float* top
  * A row whose dlogp and dentropy are both 0, or whose lse is -inf, gets a
  * zero gradient. p is taken from lse, whose fp32 rounding (2^-24 |lse|) is a
  * relative error of the row's every p: a row that is masked throughout should
- * hold -inf, not the type's lowest value.
+ * hold -inf, not a finite value of large magnitude.
  * Errors: MP_ERR_NULL (also when there is neither dlogp nor dentropy),
  *         MP_ERR_ALIGN, MP_ERR_RANGE, MP_ERR_CUDA.
  * ------------------------------------------------------------------------- */
