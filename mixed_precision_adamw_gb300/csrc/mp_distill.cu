@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(kRingBlock, 1) distill_ring_kernel(DsArgs a) {
       auto note = [&](float top) {
         if (top <= lim) return;
         st.s = st.ref == -kInf ? 0.0f : __fmul_rn(st.s, exp2_fast(__fmul_rn(__fsub_rn(st.ref, top), c)));
-        st.ref = top;
+        st.ref = max_nan(st.ref, top);  // NaN stays, whatever follows it
         lim = __fadd_rn(top, slack);
       };
       for (int i = 0; i < row.tiles; ++i, at.next()) {

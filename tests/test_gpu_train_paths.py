@@ -363,3 +363,29 @@ def test_logprob_gradient_over_split_rows(mp, rows, vocab, dtype):
         rd, td = R.lp_backward(x, t, lse, ent, dlogp, dent, 1.0)
         R.assert_within(apart, rd, R.rounded(rd, td, dtype), f"{at}")
         assert torch.equal(over, apart)
+
+
+# --- NaN and infinities anywhere in a row ---------------------------------------------------
+
+@pytest.mark.parametrize("value", [math.nan, INF])
+@pytest.mark.parametrize("masked", [0, 1, 3])
+@pytest.mark.parametrize("dtype,vocab", [(HF, 37041), (BF, 46090), (BF, 50304), (FF, 19016), (BF, 128256), (FF, 33000),
+                                         (BF, 5000), (FF, 777), (BF, 20001)])
+def test_nan_anywhere_shows(mp, dtype, vocab, masked, value):
+    # one NaN or +inf a row, at each of many places; with `masked`, thirds of the row after it hold -inf alone
+    g = gen(vocab)
+    for rows in (5, 608, 1900 if vocab < 60000 else 700):
+        x = randn((rows, vocab), g, 2.5, dtype)
+        keep = vocab - masked * (vocab // 4)
+        x[:, keep:] = -INF
+        at = torch.randint(0, keep, (rows,), generator=g, device="cuda")
+        at[:4] = torch.tensor([0, keep - 1, keep // 2, keep - 2], device="cuda")
+        x.scatter_(1, at[:, None], value)
+        idx = (at[:, None] + 1 + torch.randint(0, max(1, keep - 1), (rows, 4), generator=g, device="cuda")) % keep
+        t = randn((rows, 4), g, 1.0, dtype)
+        loss, alone, dx, lse, ent = f32(rows), f32(rows), torch.full_like(x, -7.0), f32(rows), f32(rows)
+        mp.mp_distill_topk(loss, dx, x, t, idx)
+        mp.mp_distill_topk(alone, None, x, t, idx)
+        mp.mp_token_logprob_forward(x, lse=lse, entropy=ent)
+        for name, v in (("loss", loss), ("loss alone", alone), ("lse", lse), ("entropy", ent), ("dlogits", dx)):
+            assert torch.isnan(v).all(), f"{name}: {int((~torch.isnan(v)).sum())} of {v.numel()} are not NaN, {rows} rows"
