@@ -149,7 +149,8 @@ __global__ void __launch_bounds__(kDsThreads, 6) distill_kernel(DsArgs a, int sl
         q = __fmul_rn(exp2_fast(__fmul_rn(d, c)), inv_ts);
         if (q != 0.0f) {
           const float log_q = __fmaf_rn(d, a.scale, -log_ts);
-          kl = __fmaf_rn(q, __fsub_rn(log_q, log.log_p(l.z[i])), kl);
+          // times w first: at the lowest fp32 logit the sum alone would be beyond fp32
+          kl = __fmaf_rn(__fmul_rn(w, q), __fsub_rn(log_q, log.log_p(l.z[i])), kl);
         }
       }
       l.q[i] = q;
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(kDsThreads, 6) distill_kernel(DsArgs a, int sl
     bad = __syncthreads_or(bad);
     twice = __syncthreads_or(twice);
     if (part == 0 && threadIdx.x == 0) {
-      a.loss[r] = bad ? __int_as_float(0x7FC00000) : none ? 0.0f : __fmul_rn(w, kl);
+      a.loss[r] = bad ? __int_as_float(0x7FC00000) : none ? 0.0f : kl;
       if (bad && a.d_status) atomicCAS(a.d_status, 0, MP_ERR_RANGE);
     }
     if (!dx) continue;
@@ -569,11 +570,11 @@ __device__ __noinline__ bool ring_store(const DsArgs& a, uint8_t* tiles, RingSha
       for (int j = lane; j < a.k; j += 32)
         if (l.q[j] != 0.0f) {
           const float log_p = st.ref == -kInf ? -kInf : __fmaf_rn(__fsub_rn(l.z[j], st.ref), a.scale, -log_s);
-          kl = __fmaf_rn(-l.q[j], log_p, kl);
+          kl = __fmaf_rn(-__fmul_rn(w, l.q[j]), log_p, kl);  // times w first, as above
         }
-      kl = __fadd_rn(warp_sum(kl), l.kl0);
+      kl = __fmaf_rn(w, l.kl0, warp_sum(kl));
       if (lane == 0) {
-        a.loss[r] = l.bad ? __int_as_float(0x7FC00000) : l.none ? 0.0f : __fmul_rn(w, kl);
+        a.loss[r] = l.bad ? __int_as_float(0x7FC00000) : l.none ? 0.0f : kl;
         if (l.bad && a.d_status) atomicCAS(a.d_status, 0, MP_ERR_RANGE);
       }
     }

@@ -389,3 +389,22 @@ def test_nan_anywhere_shows(mp, dtype, vocab, masked, value):
         mp.mp_token_logprob_forward(x, lse=lse, entropy=ent)
         for name, v in (("loss", loss), ("loss alone", alone), ("lse", lse), ("entropy", ent), ("dlogits", dx)):
             assert torch.isnan(v).all(), f"{name}: {int((~torch.isnan(v)).sum())} of {v.numel()} are not NaN, {rows} rows"
+
+
+@pytest.mark.parametrize("dtype", [BF, FF])
+@pytest.mark.parametrize("rows,vocab", [(6, 500), (3, 40000), (400, 40000), (2000, 3000)])
+def test_distill_of_tokens_at_the_lowest_value(mp, dtype, rows, vocab):
+    # every listed token has the type's lowest logit: the loss is near the end of fp32, and finite
+    g = gen(rows)
+    x = randn((rows, vocab), g, 2.0, dtype)
+    x[:, vocab // 2:] = torch.finfo(dtype).min
+    idx = torch.randint(vocab // 2, vocab, (rows, 24), generator=g, device="cuda")
+    t = randn((rows, 24), g, 2.0, dtype)
+    w = torch.rand(rows, generator=g, device="cuda") * 1.8 - 0.9
+    loss, alone, dx = f32(rows), f32(rows), torch.full_like(x, -7.0)
+    mp.mp_distill_topk(loss, dx, x, t, idx, row_weight=w)
+    mp.mp_distill_topk(alone, None, x, t, idx, row_weight=w)
+    (rl, rd), (tl, td) = R.distill(x, t, idx, w, 1.0)
+    R.assert_within(loss, rl, tl, "loss")
+    R.assert_within(alone, rl, tl, "loss alone")
+    R.assert_within(dx, rd, R.rounded(rd, td, dtype), "dlogits")
