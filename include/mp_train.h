@@ -15,6 +15,9 @@
  *    a result is rounded to nearest even once, when it is written.
  *  - Results are bit-identical on every run with the same arguments, sizes
  *    and alignments on the same GPU model (no float atomics).
+ *  - Waits inside a kernel end after a second at most. Should one run out (a
+ *    fault of the GPU), layer norm's outputs are NaN from there on; what
+ *    distillation leaves is said there.
  *  - Any row count, length, stride and element-aligned address is accepted.
  *    Rows that start on 16-B boundaries and hold a multiple of 16 bytes run
  *    wide loads and stores; others run narrower ones, slower.
