@@ -693,3 +693,9 @@ from . import train  # noqa: E402
 from .train import *  # noqa: E402,F401,F403
 
 __all__ += train.__all__
+
+# and of include/mp_block.h
+from . import block  # noqa: E402
+from .block import *  # noqa: E402,F401,F403
+
+__all__ += block.__all__

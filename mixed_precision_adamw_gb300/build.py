@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libmpadamw.so")
 PROBE_LIB = os.path.join(PKG, "libmpprobe.so")
 
 SOURCES = ["mp_api.cu", "mp_step.cu", "mp_norm.cu", "mp_sr.cu", "mp_outlier.cu", "mp_small.cu", "mp_copy.cu",
-           "mp_layernorm.cu", "mp_logprob.cu", "mp_distill.cu"]
+           "mp_layernorm.cu", "mp_logprob.cu", "mp_distill.cu", "mp_rmsnorm.cu", "mp_rope.cu", "mp_gated.cu"]
 PROBE_SOURCES = ["mp_probe.cu"]
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = [
