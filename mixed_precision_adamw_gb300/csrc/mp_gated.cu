@@ -36,45 +36,57 @@ struct GatedArgs {
 // How a block lies over the matrix: `across` threads along a row, the rest down
 // the rows; `chunks` blocks cover a row.
 struct Tiling {
-  int across;
-  int64_t chunks;
+  int across, chunks;
 };
 
 struct Place {
-  int64_t r, c;  // of the thread's first unit; its rows are `down` apart
-  int down;
+  int64_t r;  // of the thread's first unit; its rows are `down` apart
+  int c, down;
+  int run;  // neighbouring lanes of a row
 };
 
 __device__ __forceinline__ Place place(const Tiling& g, int rows_a_thread) {
-  const int64_t strip = blockIdx.x / g.chunks, chunk = blockIdx.x - strip * g.chunks;
+  const int strip = static_cast<int>(blockIdx.x) / g.chunks, chunk = static_cast<int>(blockIdx.x) - strip * g.chunks;
   const int down = kThreadsG / g.across;
-  return {strip * down * rows_a_thread + threadIdx.x / g.across, 8 * (chunk * g.across + threadIdx.x % g.across),
-          down};
-}
-
-// 1 / (1 + exp(-v)); what would be below 2^-126 (v under -87.3) is 0.
-__device__ __forceinline__ float sigmoid(float v) {
-  float s;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(__fadd_rn(1.0f, exp2_fast(__fmul_rn(v, -kLog2E)))));
-  return s;
+  return {static_cast<int64_t>(strip) * (down * rows_a_thread) + threadIdx.x / g.across,
+          8 * (chunk * g.across + static_cast<int>(threadIdx.x) % g.across), down, min(g.across, 32)};
 }
 
 constexpr float kGelu = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 
-// sigma(v(a)).
+// sigma(v(a)) = 1 / (1 + exp(-v)); what would be below 2^-126 (v under -87.3) is 0.
 template <int Act>
-__device__ __forceinline__ float act_sigma(float a) {
-  if (Act == MP_ACT_SILU) return sigmoid(a);
-  return sigmoid(__fmul_rn(__fmul_rn(kGelu, a), __fmaf_rn(0.044715f, __fmul_rn(a, a), 1.0f)));
+__device__ __forceinline__ F8 sigma8(const F8& a) {
+  F8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float2 v = a.p[i];
+    if (Act == MP_ACT_GELU)
+      v = mul2(mul2(v, both(kGelu)), fma2(both(0.044715f), mul2(v, v), both(1.0f)));
+    v = mul2(v, both(-kLog2E));
+    v = add2(make_float2(exp2_fast(v.x), exp2_fast(v.y)), both(1.0f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.p[i].x) : "f"(v.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.p[i].y) : "f"(v.y));
+  }
+  return r;
 }
 
-// act'(a), with s = sigma(v(a)).
+// act'(a) = sigma + a v' sigma (1 - sigma), with s = sigma(v(a)). Far out a v' may
+// overflow where sigma (1 - sigma) is 0: the product is then left out.
 template <int Act>
-__device__ __forceinline__ float act_slope(float a, float s) {
-  const float t = __fmul_rn(s, __fsub_rn(1.0f, s));
-  float v = a;
-  if (Act == MP_ACT_GELU) v = __fmul_rn(__fmul_rn(kGelu, a), __fmaf_rn(3.0f * 0.044715f, __fmul_rn(a, a), 1.0f));
-  return t > 0.0f ? __fmaf_rn(t, v, s) : s;  // far out a v' may overflow where sigma (1 - sigma) is 0
+__device__ __forceinline__ F8 slope8(const F8& a, const F8& s) {
+  F8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 t = mul2(s.p[i], fma2(s.p[i], both(-1.0f), both(1.0f)));
+    float2 v = a.p[i];
+    if (Act == MP_ACT_GELU)
+      v = mul2(mul2(v, both(kGelu)), fma2(both(3.0f * 0.044715f), mul2(v, v), both(1.0f)));
+    r.p[i] = fma2(t, v, s.p[i]);
+    r.p[i].x = t.x > 0.0f ? r.p[i].x : s.p[i].x;
+    r.p[i].y = t.y > 0.0f ? r.p[i].y : s.p[i].y;
+  }
+  return r;
 }
 
 // ---- forward ----------------------------------------------------------------------
@@ -83,32 +95,35 @@ __global__ void __launch_bounds__(kThreadsG) gated_forward_kernel(GatedArgs a, T
   pdl_enter();
   using E = typename Elem<T>::type;
   const Place at = place(g, R);
-  const int64_t blocks = (a.d + 31) / 32;
-  Pack8<T> ga[R], up[R];
+  const int d = static_cast<int>(a.d), c = at.c;
+  const int64_t blocks = (d + 31) / 32;
+  const E* gate = static_cast<const E*>(a.gate) + at.r * a.gate_stride;
+  const E* up = a.up ? static_cast<const E*>(a.up) + at.r * a.up_stride : nullptr;
+  Pack8<T> ga[R], ua[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const int64_t r = at.r + i * at.down, c = r < a.rows ? at.c : a.d;
-    load_unit<T, Wide>(ga[i], static_cast<const E*>(a.gate) + r * a.gate_stride, c, a.d);
-    if (a.up) load_unit<T, Wide>(up[i], static_cast<const E*>(a.up) + r * a.up_stride, c, a.d);
+    const int ci = at.r + i * at.down < a.rows ? c : d;
+    load_unit<T, Wide>(ga[i], gate + i * at.down * a.gate_stride, ci, d);
+    if (up) load_unit<T, Wide>(ua[i], up + i * at.down * a.up_stride, ci, d);
   }
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int64_t r = at.r + i * at.down;
     const bool live = r < a.rows;
-    float f[8], u[8];
-    ga[i].get(f);
-    if (a.gate8) put_block8<T, Wide>(f, a.gate8 + r * a.gate8_stride, a.gate8_scale + r * blocks, at.c, a.d, live);
-    if (a.up) {
-      up[i].get(u);
-      if (a.up8) put_block8<T, Wide>(u, a.up8 + r * a.up8_stride, a.up8_scale + r * blocks, at.c, a.d, live);
+    F8 f = get8(ga[i]), u;
+    if (a.gate8)
+      put_block8<T, Wide>(f, quad_amax(ga[i]), a.gate8 + r * a.gate8_stride, a.gate8_scale + r * blocks, c, d, live,
+                          at.run);
+    if (up) {
+      u = get8(ua[i]);
+      if (a.up8)
+        put_block8<T, Wide>(u, quad_amax(ua[i]), a.up8 + r * a.up8_stride, a.up8_scale + r * blocks, c, d, live,
+                            at.run);
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      f[e] = __fmul_rn(f[e], act_sigma<Act>(f[e]));
-      if (a.up) f[e] = __fmul_rn(f[e], u[e]);
-    }
-    ga[i].put(f);
-    if (live) store_unit<T, Wide>(ga[i], static_cast<E*>(a.y) + r * a.y_stride, at.c, a.d);
+    f = mul8(f, sigma8<Act>(f));
+    if (up) f = mul8(f, u);
+    put8(ga[i], f);
+    store_unit<T, Wide>(ga[i], static_cast<E*>(a.y) + r * a.y_stride, c, d, live, at.run);
   }
 }
 
@@ -118,67 +133,52 @@ __global__ void __launch_bounds__(kThreadsG) gated_backward_kernel(GatedArgs a, 
   pdl_enter();
   using E = typename Elem<T>::type;
   const Place at = place(g, R);
-  const int64_t blocks = (a.d + 31) / 32;
-  Pack8<T> dy[R], ga[Kept ? 1 : R], up[Kept ? 1 : R];
+  const int d = static_cast<int>(a.d), c = at.c;
+  const int64_t blocks = (d + 31) / 32;
+  Pack8<T> dy[R], ga[Kept ? 1 : R], ua[Kept ? 1 : R];
   uint2 g8[Kept ? R : 1], u8[Kept ? R : 1];
   uint32_t gs[Kept ? R : 1], us[Kept ? R : 1];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const int64_t r = at.r + i * at.down, c = r < a.rows ? at.c : a.d;
-    load_unit<T, Wide>(dy[i], static_cast<const E*>(a.dy) + r * a.dy_stride, c, a.d);
+    const int64_t r = at.r + i * at.down;
+    const int ci = r < a.rows ? c : d;
+    load_unit<T, Wide>(dy[i], static_cast<const E*>(a.dy) + r * a.dy_stride, ci, d);
     if constexpr (Kept) {
-      const bool in = c < a.d;
-      g8[i] = load_unit8<Wide>(static_cast<const uint8_t*>(a.gate) + r * a.gate_stride, c, a.d);
+      const bool in = ci < d;
+      g8[i] = load_unit8<Wide>(static_cast<const uint8_t*>(a.gate) + r * a.gate_stride, ci, d);
       gs[i] = in ? a.gate_scale[r * blocks + c / 32] : 127u;
       if (a.up) {
-        u8[i] = load_unit8<Wide>(static_cast<const uint8_t*>(a.up) + r * a.up_stride, c, a.d);
+        u8[i] = load_unit8<Wide>(static_cast<const uint8_t*>(a.up) + r * a.up_stride, ci, d);
         us[i] = in ? a.up_scale[r * blocks + c / 32] : 127u;
       }
     } else {
-      load_unit<T, Wide>(ga[i], static_cast<const E*>(a.gate) + r * a.gate_stride, c, a.d);
-      if (a.up) load_unit<T, Wide>(up[i], static_cast<const E*>(a.up) + r * a.up_stride, c, a.d);
+      load_unit<T, Wide>(ga[i], static_cast<const E*>(a.gate) + r * a.gate_stride, ci, d);
+      if (a.up) load_unit<T, Wide>(ua[i], static_cast<const E*>(a.up) + r * a.up_stride, ci, d);
     }
   }
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int64_t r = at.r + i * at.down;
-    if (r >= a.rows) break;
-    float f[8], u[8], d[8], o[8], p[8];
-    dy[i].get(d);
+    const bool live = r < a.rows;
+    F8 f, u;
     if constexpr (Kept) {
-      e4m3_unpack(g8[i], f);
-      const float s = block_scale_value(gs[i]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(f[e], s);
-      if (a.up) {
-        e4m3_unpack(u8[i], u);
-        const float q = block_scale_value(us[i]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) u[e] = __fmul_rn(u[e], q);
-      }
+      f = mul8(e4m3_unpack(g8[i]), block_scale_value(gs[i]));
+      if (a.up) u = mul8(e4m3_unpack(u8[i]), block_scale_value(us[i]));
     } else {
-      ga[i].get(f);
-      if (a.up) up[i].get(u);
+      f = get8(ga[i]);
+      if (a.up) u = get8(ua[i]);
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float s = act_sigma<Act>(f[e]), act = __fmul_rn(f[e], s);
-      o[e] = __fmul_rn(a.up ? __fmul_rn(d[e], u[e]) : d[e], act_slope<Act>(f[e], s));
-      p[e] = __fmul_rn(d[e], act);
-      d[e] = a.up ? __fmul_rn(act, u[e]) : act;
-    }
+    const F8 d0 = get8(dy[i]), s = sigma8<Act>(f), act = mul8(f, s);
     Pack8<T> w;
-    if (a.dgate) {
-      w.put(o);
-      store_unit<T, Wide>(w, static_cast<E*>(a.dgate) + r * a.dgate_stride, at.c, a.d);
-    }
+    put8(w, mul8(a.up ? mul8(d0, u) : d0, slope8<Act>(f, s)));
+    store_unit<T, Wide>(w, static_cast<E*>(a.dgate) + r * a.dgate_stride, c, d, live, at.run);
     if (a.dup) {
-      w.put(p);
-      store_unit<T, Wide>(w, static_cast<E*>(a.dup) + r * a.dup_stride, at.c, a.d);
+      put8(w, mul8(d0, act));
+      store_unit<T, Wide>(w, static_cast<E*>(a.dup) + r * a.dup_stride, c, d, live, at.run);
     }
     if (a.y) {
-      w.put(d);
-      store_unit<T, Wide>(w, static_cast<E*>(a.y) + r * a.y_stride, at.c, a.d);
+      put8(w, a.up ? mul8(act, u) : act);
+      store_unit<T, Wide>(w, static_cast<E*>(a.y) + r * a.y_stride, c, d, live, at.run);
     }
   }
 }
@@ -199,20 +199,19 @@ __global__ void __launch_bounds__(kThreadsG) pack_blocks_kernel(Rows8Args a, Til
   pdl_enter();
   using E = typename Elem<T>::type;
   const Place at = place(g, R);
-  const int64_t blocks = (a.d + 31) / 32;
+  const int d = static_cast<int>(a.d), c = at.c;
+  const int64_t blocks = (d + 31) / 32;
+  const E* from = static_cast<const E*>(a.x_in) + at.r * a.x_stride;
+  uint8_t* to = a.q + at.r * a.q_stride;
+  uint8_t* scales = static_cast<uint8_t*>(a.scale) + at.r * blocks;
   Pack8<T> x[R];
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int64_t r = at.r + i * at.down;
-    load_unit<T, Wide>(x[i], static_cast<const E*>(a.x_in) + r * a.x_stride, r < a.rows ? at.c : a.d, a.d);
-  }
+  for (int i = 0; i < R; ++i)
+    load_unit<T, Wide>(x[i], from + i * at.down * a.x_stride, at.r + i * at.down < a.rows ? c : d, d);
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int64_t r = at.r + i * at.down;
-    float f[8];
-    x[i].get(f);
-    put_block8<T, Wide>(f, a.q + r * a.q_stride, static_cast<uint8_t*>(a.scale) + r * blocks, at.c, a.d, r < a.rows);
-  }
+  for (int i = 0; i < R; ++i)
+    put_block8<T, Wide>(get8(x[i]), quad_amax(x[i]), to + i * at.down * a.q_stride, scales + i * at.down * blocks, c,
+                        d, at.r + i * at.down < a.rows, at.run);
 }
 
 template <int T, bool Wide, int R>
@@ -220,29 +219,26 @@ __global__ void __launch_bounds__(kThreadsG) unpack_kernel(Rows8Args a, Tiling g
   pdl_enter();
   using E = typename Elem<T>::type;
   const Place at = place(g, R);
-  const int64_t blocks = (a.d + 31) / 32;
+  const int d = static_cast<int>(a.d), c = at.c;
+  const int64_t blocks = (d + 31) / 32;
   const bool row = a.kind == MP_SCALE_ROW;
   uint2 q[R];
   float s[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const int64_t r = at.r + i * at.down, c = r < a.rows ? at.c : a.d;
-    q[i] = load_unit8<Wide>(a.q_in + r * a.q_stride, c, a.d);
-    s[i] = c >= a.d ? 0.0f
-           : row    ? static_cast<const float*>(a.scale)[r]
-                    : block_scale_value(static_cast<const uint8_t*>(a.scale)[r * blocks + c / 32]);
+    const int64_t r = at.r + i * at.down;
+    const int ci = r < a.rows ? c : d;
+    q[i] = load_unit8<Wide>(a.q_in + r * a.q_stride, ci, d);
+    s[i] = ci >= d ? 0.0f
+           : row   ? static_cast<const float*>(a.scale)[r]
+                   : block_scale_value(static_cast<const uint8_t*>(a.scale)[r * blocks + c / 32]);
   }
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int64_t r = at.r + i * at.down;
-    if (r >= a.rows) break;
-    float f[8];
-    e4m3_unpack(q[i], f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(f[e], s[i]);
     Pack8<T> x;
-    x.put(f);
-    store_unit<T, Wide>(x, static_cast<E*>(a.x) + r * a.x_stride, at.c, a.d);
+    put8(x, mul8(e4m3_unpack(q[i]), s[i]));
+    store_unit<T, Wide>(x, static_cast<E*>(a.x) + r * a.x_stride, c, d, r < a.rows, at.run);
   }
 }
 
@@ -251,10 +247,10 @@ __global__ void __launch_bounds__(kThreadsG) unpack_kernel(Rows8Args a, Tiling g
 // Threads of a block along a row of d elements: the fewest lanes left over, more
 // of them along the row where that is equal. Whole quads of lanes (32 columns).
 Tiling tiling(int64_t d) {
-  const int64_t units = (d + 31) / 32 * 4;
+  const int units = static_cast<int>((d + 31) / 32 * 4);
   Tiling best = {kThreadsG, (units + kThreadsG - 1) / kThreadsG};
   for (int across = kThreadsG / 2; across >= 8; across /= 2) {
-    const int64_t chunks = (units + across - 1) / across;
+    const int chunks = (units + across - 1) / across;
     if (chunks * across < best.chunks * best.across) best = {across, chunks};
   }
   return best;

@@ -8,15 +8,19 @@
 // (7 with h kept in 8 bits).
 #include "mp_device.cuh"
 #include "mp_internal.h"
+#include "mp_tma.cuh"
 #include "mp_units.cuh"
 
 namespace mpk {
 namespace {
 
-constexpr int64_t kRowD = 8192;  // longest row that registers hold
+constexpr int64_t kShortD = 256;   // a warp or less a row
+constexpr int64_t kStagedD = 8192; // longest row that a block's registers hold
 constexpr int kMaxThreads = 512;
 constexpr int kLongThreads = 512;
 constexpr int64_t kSms = 152;
+constexpr int kMaxStages = 4;
+constexpr uint32_t kSmShared = 227 * 1024;  // an SM's shared memory for blocks
 
 struct RmsArgs {
   void* y;  // dx in the backward pass
@@ -39,122 +43,244 @@ struct RmsArgs {
   int plain;  // y8 alone, of x itself (no norm)
 };
 
-// Sum and largest over the threads of a row: L lanes of a warp, or G warps that
-// meet at a barrier of their own. `red` holds two floats a warp, of alternate rows.
-template <int L>
-__device__ __forceinline__ void row_join(float& s, float& m, bool want_m, float2 (*red)[kMaxThreads / 32], int G,
-                                         int group, int parity) {
+// The thread's weights of the unit at column c.
+__device__ __forceinline__ F8 load_weights(const RmsArgs& a, int c) {
+  float w[8];
 #pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) s = __fadd_rn(s, __shfl_xor_sync(kAll, s, o));
-  if (want_m)
+  for (int e = 0; e < 8; ++e)
+    w[e] = c + e < a.d ? (a.weight ? load_as(a.weight, c + e, a.weight_type) : 1.0f) : 0.0f;
+  F8 r;
 #pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(kAll, m, o));
-  if (L < 32 || G == 1) return;
-  if (threadIdx.x % 32 == 0) red[parity][threadIdx.x / 32] = make_float2(s, m);
-  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * G) : "memory");
-  s = 0.0f;
-  for (int w = 0; w < G; ++w) {
-    const float2 v = red[parity][group * G + w];
-    s = __fadd_rn(s, v.x);
-    m = w ? max_nan(m, v.y) : v.y;
+  for (int i = 0; i < 4; ++i) r.p[i] = make_float2(w[2 * i], w[2 * i + 1]);
+  return r;
+}
+
+// Weights widened into shared memory once a block: neither their type nor their
+// place (they may sit anywhere in a flat buffer) matters afterwards. A unit's
+// eight lie in two planes of four, so that a warp's lanes read neighbouring
+// 16 bytes.
+__device__ __forceinline__ void stage_weights(float4* sw, const RmsArgs& a, int units, int threads) {
+  for (int u = threadIdx.x; u < units; u += threads) {
+    const F8 w = load_weights(a, 8 * u);
+    sw[u] = make_float4(w.p[0].x, w.p[0].y, w.p[1].x, w.p[1].y);
+    sw[units + u] = make_float4(w.p[2].x, w.p[2].y, w.p[3].x, w.p[3].y);
   }
 }
 
-// Rows of up to 8 * NV * (threads of a row) elements. The next row is on its way
-// while a row is summed and written.
-template <int T, bool Wide, int NV, int L>
-__global__ void __launch_bounds__(kMaxThreads) rms_forward_kernel(RmsArgs a, int G) {
+__device__ __forceinline__ F8 staged_weights(const float4* sw, int unit, int units) {
+  unit = min(unit, units - 1);
+  const float4 a = sw[unit], b = sw[units + unit];
+  F8 r;
+  r.p[0] = make_float2(a.x, a.y);
+  r.p[1] = make_float2(a.z, a.w);
+  r.p[2] = make_float2(b.x, b.y);
+  r.p[3] = make_float2(b.z, b.w);
+  return r;
+}
+
+template <int T>
+__device__ __forceinline__ void fill_nan(Pack8<T>& u) {
+  if constexpr (T == MP_FP32)
+    u.fill(__uint_as_float(0x7FC00000u));
+  else
+    u.fill(T == MP_BF16 ? 0x7FC0 : 0x7E00);
+}
+
+// A unit's outputs. All lanes of a warp call (live, run: as store_unit). `inverse`:
+// of the row's 8-bit scale.
+template <int T, bool Wide>
+__device__ __forceinline__ void put_unit(const RmsArgs& a, const Pack8<T>& u, const F8& w, float rstd, bool row8,
+                                         float inverse, int64_t r, int c, int d, bool live, int run) {
+  using E = typename Elem<T>::type;
+  const int64_t blocks = (d + 31) / 32;
+  const F8 f = get8(u);
+  if (a.h) store_unit<T, Wide>(u, static_cast<E*>(a.h) + r * a.h_stride, c, d, live, run);
+  if (a.h8)
+    put_block8<T, Wide>(f, quad_amax(u), a.h8 + r * a.h8_stride, a.h8_scale + r * blocks, c, d, live, run);
+  if (!a.y && !a.y8) return;
+  const F8 y = mul8(mul8(f, rstd), w);
+  if (a.y) {
+    Pack8<T> o;
+    put8(o, y);
+    store_unit<T, Wide>(o, static_cast<E*>(a.y) + r * a.y_stride, c, d, live, run);
+  }
+  if (row8)
+    store_unit8<Wide>(e4m3_pack(mul8(y, inverse)), a.y8 + r * a.y8_stride, c, d, live, run);
+  else if (a.y8)
+    put_block8<MP_FP32, Wide>(y, quad_amax(y), a.y8 + r * a.y8_stride, static_cast<uint8_t*>(a.y8_scale) + r * blocks,
+                              c, d, live, run);
+}
+
+// From a row's sums (to each of its threads): rstd and the inverse of its 8-bit
+// scale; the first thread writes what there is one of.
+__device__ __forceinline__ float row_results(const RmsArgs& a, float s, float m, float inv_d, bool row8, int64_t r,
+                                             bool writes, float& inverse) {
+  const float rstd = a.plain ? 1.0f : rsqrtf(__fmaf_rn(s, inv_d, a.eps));
+  inverse = 0.0f;
+  if (row8) {
+    const float scale = row_scale(__fmul_rn(m, rstd));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(inverse) : "f"(scale));
+    if (writes) static_cast<float*>(a.y8_scale)[r] = scale;
+  }
+  if (writes && a.rstd) a.rstd[r] = rstd;
+  return rstd;
+}
+
+// Short rows, up to 8 * L elements: L lanes of a warp take a row, and the next row
+// is on its way while one is summed and written.
+template <int T, bool Wide, int L>
+__global__ void __launch_bounds__(256) rms_forward_short_kernel(RmsArgs a) {
   pdl_enter();
   using E = typename Elem<T>::type;
+  const int t = threadIdx.x % L, c = 8 * t, d = static_cast<int>(a.d);
+  const int64_t groups = 256 / L, step = gridDim.x * groups;
+  const float inv_d = __fdiv_rn(1.0f, static_cast<float>(d));
+  const bool row8 = a.y8 && a.y8_kind == MP_SCALE_ROW;
+  const F8 w = load_weights(a, c);
+  Pack8<T> xn, rn;
+  auto fetch = [&](int64_t r) {
+    const int at = r < a.rows ? c : d;
+    load_unit<T, Wide>(xn, static_cast<const E*>(a.x) + r * a.x_stride, at, d);
+    if (a.residual) load_unit<T, Wide>(rn, static_cast<const E*>(a.residual) + r * a.residual_stride, at, d);
+  };
+  int64_t r = blockIdx.x * groups + threadIdx.x / L;
+  const int64_t ahead = threadIdx.x % 32 / L;
+  fetch(r);
+  // every lane of a warp runs the same number of rounds (the shuffles are whole-warp)
+#pragma unroll 1
+  for (; r - ahead < a.rows; r += step) {
+    const bool live = r < a.rows;
+    Pack8<T> u = xn;
+    if (a.residual) put8(u, add8(get8(u), get8(rn)));
+    fetch(r + step);
+    const F8 f = get8(u);
+    float2 s2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s2 = fma2(f.p[i], f.p[i], s2);
+    float s = __fadd_rn(s2.x, s2.y), m = row8 ? amax8(0.0f, mul8(f, w)) : 0.0f;
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) s = __fadd_rn(s, __shfl_xor_sync(kAll, s, o));
+    if (row8)
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(kAll, m, o));
+    float inverse;
+    const float rstd = row_results(a, s, m, inv_d, row8, r, t == 0 && live, inverse);
+    put_unit<T, Wide>(a, u, w, rstd, row8, inverse, r, c, d, live, L);
+  }
+}
+
+// Longer rows: groups of G warps take a row each, NV units a thread, from a ring
+// of staged rows of their own. A group's warps meet at a named barrier of their
+// own once a row, for its sum; by then they have read the stage, which is filled
+// again.
+template <int T, bool Wide, int NV>
+__global__ void __launch_bounds__(kMaxThreads, 1)
+rms_forward_kernel(RmsArgs a, int G, uint32_t pitch, int stages) {
+  pdl_enter();
+  using E = typename Elem<T>::type;
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 red[2][kMaxThreads / 32];
-  const int per_row = L < 32 ? L : 32 * G, t = threadIdx.x % per_row, group = threadIdx.x / per_row;
-  const int groups = blockDim.x / per_row;
+  __shared__ unsigned long long full[kMaxThreads / 32 * kMaxStages];
+  const int L = 32 * G, t = threadIdx.x % L, group = threadIdx.x / L, groups = blockDim.x / L;
+  const int d = static_cast<int>(a.d), units = (d + 7) / 8;
+  const bool has_res = a.residual;
+  const uint32_t stage_bytes = has_res ? 2 * pitch : pitch;
+  float4* sw = reinterpret_cast<float4*>(smem);
+  uint8_t* ring = smem + 32 * units + static_cast<size_t>(group) * stages * stage_bytes;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-  const float inv_d = __fdiv_rn(1.0f, static_cast<float>(a.d));
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + group;
+  if (threadIdx.x < groups * stages) {
+    mbar_init(smem_u32(&full[threadIdx.x]), 1);
+    mbar_init_fence();
+  }
+  __syncthreads();
   const E* x = static_cast<const E*>(a.x);
   const E* res = static_cast<const E*>(a.residual);
-  float w[NV][8];
-#pragma unroll
-  for (int v = 0; v < NV; ++v)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int64_t j = 8 * (t + static_cast<int64_t>(v) * per_row) + e;
-      w[v][e] = j < a.d ? (a.weight ? load_as(a.weight, j, a.weight_type) : 1.0f) : 0.0f;
+  const uint32_t length = static_cast<uint32_t>(d) * sizeof(E);
+  auto fetch = [&](int64_t r, int stage) {  // by the group's first thread
+    if (r >= a.rows) return;
+    const uint32_t bar = smem_u32(&full[group * stages + stage]), to = smem_u32(ring + stage * stage_bytes);
+    const Pieces p(x + r * a.x_stride, length);
+    if (has_res) {
+      const Pieces q(res + r * a.residual_stride, length);
+      mbar_expect_tx(bar, p.bytes + q.bytes);
+      bulk_load(to + pitch, q.src, q.bytes, bar);
+    } else {
+      mbar_expect_tx(bar, p.bytes);
     }
-  const bool row8 = a.y8 && a.y8_kind == MP_SCALE_ROW;
-  Pack8<T> xn[NV], rn[NV];
-  auto fetch = [&](int64_t r) {
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int64_t c = 8 * (t + static_cast<int64_t>(v) * per_row);
-      load_unit<T, Wide>(xn[v], x + r * a.x_stride, r < a.rows ? c : a.d, a.d);
-      if (res) load_unit<T, Wide>(rn[v], res + r * a.residual_stride, r < a.rows ? c : a.d, a.d);
-    }
+    bulk_load(to, p.src, p.bytes, bar);
   };
-  // every lane of a warp runs the same number of rounds (the shuffles are whole-warp)
-  int64_t r = static_cast<int64_t>(blockIdx.x) * groups + group;
-  const int64_t ahead = L < 32 ? threadIdx.x % 32 / L : 0;
-  fetch(r);
-  int parity = 0;
+  if (t == 0)
+    for (int i = 0; i < stages; ++i) fetch(first + i * step, i);
+  stage_weights(sw, a, units, blockDim.x);
+  __syncthreads();
+  const float inv_d = __fdiv_rn(1.0f, static_cast<float>(d));
+  const bool row8 = a.y8 && a.y8_kind == MP_SCALE_ROW;
+  bool ok = true;
+  int stage = 0, parity = 0;
+  uint32_t phase = 0;
+  int64_t gave_up = 0;
 #pragma unroll 1
-  for (; r - ahead < a.rows; r += step, parity ^= 1) {
-    const bool live = r < a.rows;
+  for (int64_t r = first; r < a.rows; r += step, parity ^= 1) {
+    // a wait that gives up (only a fault can cause that) makes what follows NaN,
+    // and nothing more is fetched
+    if (ok && !mbar_wait(smem_u32(&full[group * stages + stage]), phase)) {
+      ok = false;
+      gave_up = r;
+    }
+    const uint8_t* at = ring + stage * stage_bytes;
+    const E* xs = reinterpret_cast<const E*>(at + (Wide ? 0 : Pieces(x + r * a.x_stride, length).offset));
+    const E* rs = reinterpret_cast<const E*>(
+        at + pitch + (Wide || !has_res ? 0 : Pieces(res + r * a.residual_stride, length).offset));
     Pack8<T> u[NV];
-    float s = 0.0f, m = 0.0f;
+    float2 s2 = make_float2(0.0f, 0.0f);
+    float m = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      u[v] = xn[v];
-      float f[8];
-      u[v].get(f);
-      if (res) {
-        float g[8];
-        rn[v].get(g);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = __fadd_rn(f[e], g[e]);
-        u[v].put(f);
-        u[v].get(f);
+      const int c = 8 * (t + v * L);
+      load_unit<T, Wide>(u[v], xs, c, d);
+      if (has_res) {
+        Pack8<T> q;
+        load_unit<T, Wide>(q, rs, c, d);
+        put8(u[v], add8(get8(u[v]), get8(q)));
       }
+      if (!ok) fill_nan(u[v]);
+      const F8 f = get8(u[v]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s = __fmaf_rn(f[e], f[e], s);
-      if (row8) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(__fmul_rn(f[e], w[v][e])));
-      }
+      for (int i = 0; i < 4; ++i) s2 = fma2(f.p[i], f.p[i], s2);
+      if (row8) m = amax8(m, mul8(f, staged_weights(sw, t + v * L, units)));
     }
-    fetch(r + step);
-    row_join<L>(s, m, row8, red, G, group, parity);
-    const float rstd = a.plain ? 1.0f : rsqrtf(__fmaf_rn(s, inv_d, a.eps));
-    float inverse = 0.0f;
-    if (row8) {
-      const float scale = row_scale(__fmul_rn(m, rstd));
-      inverse = __frcp_rn(scale);
-      if (t == 0 && live) static_cast<float*>(a.y8_scale)[r] = scale;
-    }
-    if (t == 0 && live && a.rstd) a.rstd[r] = rstd;
-    const int64_t blocks = (a.d + 31) / 32;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int64_t c = 8 * (t + static_cast<int64_t>(v) * per_row);
-      float f[8];
-      u[v].get(f);
-      if (a.h && live) store_unit<T, Wide>(u[v], static_cast<E*>(a.h) + r * a.h_stride, c, a.d);
-      if (a.h8) put_block8<T, Wide>(f, a.h8 + r * a.h8_stride, a.h8_scale + r * blocks, c, a.d, live);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(__fmul_rn(f[e], rstd), w[v][e]);
-      if (a.y && live) {
-        Pack8<T> o;
-        o.put(f);
-        store_unit<T, Wide>(o, static_cast<E*>(a.y) + r * a.y_stride, c, a.d);
+    float s = warp_sum(__fadd_rn(s2.x, s2.y));
+    if (row8) m = warp_max(m);
+    if (G > 1) {
+      if (t % 32 == 0) red[parity][threadIdx.x / 32] = make_float2(s, m);
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(L) : "memory");
+      s = 0.0f;
+      for (int i = 0; i < G; ++i) {
+        const float2 f = red[parity][group * G + i];
+        s = __fadd_rn(s, f.x);
+        m = max_nan(m, f.y);
       }
-      if (row8) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(f[e], inverse);
-        if (live) store_unit8<Wide>(e4m3_pack(f), a.y8 + r * a.y8_stride, c, a.d);
-      } else if (a.y8) {
-        put_block8<MP_FP32, Wide>(f, a.y8 + r * a.y8_stride, static_cast<uint8_t*>(a.y8_scale) + r * blocks, c, a.d,
-                                  live);
-      }
+    } else {
+      __syncwarp();
     }
+    if (t == 0 && ok) fetch(r + stages * step, stage);
+    float inverse;
+    const float rstd = row_results(a, s, m, inv_d, row8, r, t == 0, inverse);
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      put_unit<T, Wide>(a, u[v], staged_weights(sw, t + v * L, units), rstd, row8, inverse, r, 8 * (t + v * L), d, true,
+                        32);
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+  // the copies that were not waited for land before the block ends
+  if (!ok && t == 0) {
+    const int64_t round = (gave_up - first) / step;
+    for (int64_t i = round; i < round + stages && first + i * step < a.rows; ++i)
+      mbar_drain(smem_u32(&full[group * stages + i % stages]), (i / stages) & 1);
   }
 }
 
@@ -186,7 +312,8 @@ template <int T>
 __device__ __forceinline__ void long_block8(float f, uint8_t* row, uint8_t* scales, int64_t j, int64_t d) {
   const uint32_t byte = block_scale(warp_max(fabsf(f)));
   if (j >= d) return;
-  const float g[8] = {f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  F8 g = zero8();
+  g.p[0].x = f;
   row[j] = static_cast<uint8_t>(block_pack<T>(g, byte).x);
   if (j % 32 == 0) scales[j / 32] = static_cast<uint8_t>(byte);
 }
@@ -244,131 +371,296 @@ __global__ void __launch_bounds__(kLongThreads) rms_forward_long_kernel(RmsArgs 
 // A thread owns the same columns in every row it sees and adds their dy xh in
 // registers; a block writes its sums once, part[block][d], and a second, small
 // launch adds the blocks' sums in block order.
-template <int T, bool Wide, bool H8, int NV, int L>
-__global__ void __launch_bounds__(kMaxThreads) rms_backward_kernel(RmsArgs a, float* part, int G) {
+
+// xh of a unit of h, as stored or in 8 bits.
+template <int T>
+__device__ __forceinline__ F8 normalised(const Pack8<T>& u, float rstd) {
+  return mul8(get8(u), rstd);
+}
+__device__ __forceinline__ F8 normalised(uint2 q, uint32_t scale, float rstd) {
+  return mul8(e4m3_unpack(q), __fmul_rn(block_scale_value(scale), rstd));
+}
+
+// Short rows, L lanes each.
+template <int T, bool Wide, bool H8, int L>
+__global__ void __launch_bounds__(256) rms_backward_short_kernel(RmsArgs a, float* part) {
   pdl_enter();
   using E = typename Elem<T>::type;
-  __shared__ float2 red[2][kMaxThreads / 32];
-  extern __shared__ __align__(16) float joined[];  // a block's groups' sums
-  const int per_row = L < 32 ? L : 32 * G, t = threadIdx.x % per_row, group = threadIdx.x / per_row;
-  const int groups = blockDim.x / per_row;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-  const float inv_d = __fdiv_rn(1.0f, static_cast<float>(a.d));
-  const int64_t blocks = (a.d + 31) / 32;
+  constexpr int kGroups = 256 / L;
+  __shared__ float joined[256 * 8];  // the groups' sums
+  const int t = threadIdx.x % L, group = threadIdx.x / L, c = 8 * t, d = static_cast<int>(a.d);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups, blocks = (d + 31) / 32;
+  const float inv_d = __fdiv_rn(1.0f, static_cast<float>(d));
+  const F8 w = load_weights(a, c);
+  F8 dw = zero8();
+  Pack8<T> yn, gn, hn;
+  uint2 qn = make_uint2(0u, 0u);
+  uint32_t bn = 127u;
+  float rstd_n = 0.0f;
+  auto fetch = [&](int64_t r) {
+    const bool live = r < a.rows;
+    const int at = live ? c : d;
+    rstd_n = live ? a.rstd_in[r] : 0.0f;
+    load_unit<T, Wide>(yn, static_cast<const E*>(a.dy) + r * a.dy_stride, at, d);
+    if constexpr (H8) {
+      qn = load_unit8<Wide>(static_cast<const uint8_t*>(a.x) + r * a.x_stride, at, d);
+      bn = at < d ? a.x_scale[r * blocks + at / 32] : 127u;
+    } else {
+      load_unit<T, Wide>(hn, static_cast<const E*>(a.x) + r * a.x_stride, at, d);
+    }
+    if (a.residual) load_unit<T, Wide>(gn, static_cast<const E*>(a.residual) + r * a.residual_stride, at, d);
+  };
+  int64_t r = static_cast<int64_t>(blockIdx.x) * kGroups + group;
+  const int64_t ahead = threadIdx.x % 32 / L;
+  fetch(r);
+#pragma unroll 1
+  for (; r - ahead < a.rows; r += step) {
+    const bool live = r < a.rows;
+    const float rstd = rstd_n;
+    F8 xh;
+    if constexpr (H8)
+      xh = normalised(qn, bn, rstd);
+    else
+      xh = normalised(hn, rstd);
+    const F8 f = get8(yn), g = mul8(f, w);
+    F8 o = zero8();
+    if (a.residual) o = get8(gn);
+    fetch(r + step);
+    float2 s2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s2 = fma2(g.p[i], xh.p[i], s2);
+      dw.p[i] = fma2(f.p[i], xh.p[i], dw.p[i]);
+    }
+    float s = __fadd_rn(s2.x, s2.y);
+#pragma unroll
+    for (int q = L / 2; q > 0; q >>= 1) s = __fadd_rn(s, __shfl_xor_sync(kAll, s, q));
+    if (!a.y) continue;
+    const float k = -__fmul_rn(__fmul_rn(s, inv_d), rstd);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o.p[i] = fma2(g.p[i], both(rstd), fma2(xh.p[i], both(k), o.p[i]));
+    Pack8<T> u;
+    put8(u, o);
+    store_unit<T, Wide>(u, static_cast<E*>(a.y) + r * a.y_stride, c, d, live, L);
+  }
+  if (!part) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    joined[group * 8 * L + c + 2 * i] = dw.p[i].x;
+    joined[group * 8 * L + c + 2 * i + 1] = dw.p[i].y;
+  }
+  __syncthreads();
+  for (int j = threadIdx.x; j < d; j += 256) {
+    float s = 0.0f;
+    for (int q = 0; q < kGroups; ++q) s = __fadd_rn(s, joined[q * 8 * L + j]);
+    part[static_cast<int64_t>(blockIdx.x) * d + j] = s;
+  }
+}
+
+// Longer rows: all but the last warp of a block compute, NV units a thread, R rows
+// a round; the last warp stages the rounds' rows of dy, h (and its scales) and dh,
+// and their rstd, as stages become free. One barrier a round joins the rows' sums
+// (which alternate between two buffers).
+constexpr int kBackwardThreads = 576;  // the most that share an SM's registers: 96 each
+
+struct StageMap {  // of one stage in bytes
+  uint32_t pitch, h_pitch, scale_pitch;  // a row of dy and dh; of h; of h's scales
+  uint32_t row, size;                    // all of one row; of R rows
+};
+
+template <int T, bool Wide, bool H8, int NV, int R>
+__global__ void __launch_bounds__(kBackwardThreads, 1)
+rms_backward_kernel(RmsArgs a, float* part, StageMap map, int stages) {
+  pdl_enter();
+  using E = typename Elem<T>::type;
+  __shared__ float red[2][kMaxThreads / 32][R];
+  __shared__ float stats[kMaxStages][R];  // rstd of a stage's rows
+  __shared__ unsigned long long full[kMaxStages], freed[kMaxStages];
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int t = threadIdx.x, L = blockDim.x - 32, lane = t % 32, warp = t / 32, warps = L / 32;
+  const int64_t begin = a.rows * blockIdx.x / gridDim.x, end = a.rows * (blockIdx.x + 1) / gridDim.x;
+  const int64_t rounds = (end - begin + R - 1) / R, blocks = (a.d + 31) / 32;
+  const int d = static_cast<int>(a.d);
+  if (t < stages) {
+    mbar_init(smem_u32(&full[t]), 1);
+    mbar_init(smem_u32(&freed[t]), warps);
+    mbar_init_fence();
+  }
+  __syncthreads();
   const E* dy = static_cast<const E*>(a.dy);
   const E* dh = static_cast<const E*>(a.residual);
-  float w[NV][8], dw[NV][8];
+  const uint32_t length = static_cast<uint32_t>(d) * sizeof(E);
+  auto dy_row = [&](int64_t r) { return Pieces(dy + r * a.dy_stride, length); };
+  auto dh_row = [&](int64_t r) { return Pieces(dh + r * a.residual_stride, length); };
+  auto h_row = [&](int64_t r) {
+    return H8 ? Pieces(static_cast<const uint8_t*>(a.x) + r * a.x_stride, static_cast<uint32_t>(a.d))
+              : Pieces(static_cast<const E*>(a.x) + r * a.x_stride, length);
+  };
+  auto scale_row = [&](int64_t r) { return Pieces(a.x_scale + r * blocks, static_cast<uint32_t>(blocks)); };
+  if (warp == warps) {  // the staging warp
+    float stat = lane < R && begin + lane < end ? a.rstd_in[begin + lane] : 0.0f;
+    int stage = 0;
+    uint32_t phase = 1;
+    int64_t round = 0;
+    for (; round < rounds; ++round) {
+      const int64_t r0 = begin + round * R;
+      if (round >= stages && !__all_sync(kAll, mbar_wait(smem_u32(&freed[stage]), phase))) break;
+      const uint32_t bar = smem_u32(&full[stage]), to = smem_u32(smem + stage * map.size);
+      if (lane < R) stats[stage][lane] = stat;
+      __syncwarp();
+      if (lane == 0) {
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          if (r0 + i < end) {
+            bytes += dy_row(r0 + i).bytes + h_row(r0 + i).bytes;
+            if (H8) bytes += scale_row(r0 + i).bytes;
+            if (dh) bytes += dh_row(r0 + i).bytes;
+          }
+        mbar_expect_tx(bar, bytes);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          if (r0 + i < end) {
+            uint32_t at = to + i * map.row;
+            const Pieces p = dy_row(r0 + i), q = h_row(r0 + i);
+            bulk_load(at, p.src, p.bytes, bar);
+            at += map.pitch;
+            bulk_load(at, q.src, q.bytes, bar);
+            at += map.h_pitch;
+            if (H8) {
+              const Pieces s = scale_row(r0 + i);
+              bulk_load(at, s.src, s.bytes, bar);
+              at += map.scale_pitch;
+            }
+            if (dh) {
+              const Pieces g = dh_row(r0 + i);
+              bulk_load(at, g.src, g.bytes, bar);
+            }
+          }
+      }
+      const int64_t next = r0 + R + lane;
+      stat = lane < R && next < end ? a.rstd_in[next] : 0.0f;
+      if (++stage == stages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    // copies in flight land before the block ends
+    if (lane == 0)
+      for (int64_t i = max(int64_t{0}, round - stages); i < round; ++i)
+        mbar_drain(smem_u32(&full[i % stages]), (i / stages) & 1);
+    return;
+  }
+  const float inv_d = __fdiv_rn(1.0f, static_cast<float>(d));
+  F8 w[NV], dw[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    w[v] = load_weights(a, 8 * (t + v * L));
+    dw[v] = zero8();
+  }
+  bool ok = true;
+  int stage = 0;
+  uint32_t phase = 0;
+#pragma unroll 1
+  for (int64_t round = 0; round < rounds; ++round) {
+    const int64_t r0 = begin + round * R;
+    const int live = static_cast<int>(min(static_cast<int64_t>(R), end - r0));
+    // A wait that gives up (only a fault can cause that) makes the sums NaN.
+    ok = ok && mbar_wait(smem_u32(&full[stage]), phase);
+    const uint8_t* base = smem + stage * map.size;
+    float sums[R];
+    F8 xh[R][NV], f[R][NV];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      float2 s2 = make_float2(0.0f, 0.0f);
+      if (i < live) {
+        const uint8_t* at = base + i * map.row;
+        const uint8_t* ys = at + (Wide ? 0 : dy_row(r0 + i).offset);
+        // 8-bit rows are on an 8-byte grid at least
+        const uint8_t* hs = at + map.pitch + (Wide && !H8 ? 0 : h_row(r0 + i).offset);
+        const uint8_t* ss = H8 ? at + map.pitch + map.h_pitch + scale_row(r0 + i).offset : nullptr;
+        const float rstd = stats[stage][i];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const int c = 8 * (t + v * L);
+          Pack8<T> u;
+          if constexpr (H8) {
+            xh[i][v] = normalised(load_unit8<Wide>(hs, c, d), c < d ? ss[c / 32] : 127u, rstd);
+          } else {
+            load_unit<T, Wide>(u, reinterpret_cast<const E*>(hs), c, d);
+            xh[i][v] = normalised(u, rstd);
+          }
+          load_unit<T, Wide>(u, reinterpret_cast<const E*>(ys), c, d);
+          f[i][v] = get8(u);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            s2 = fma2(mul2(f[i][v].p[q], w[v].p[q]), xh[i][v].p[q], s2);
+            dw[v].p[q] = fma2(f[i][v].p[q], xh[i][v].p[q], dw[v].p[q]);
+          }
+        }
+      }
+      sums[i] = ok ? __fadd_rn(s2.x, s2.y) : __uint_as_float(0x7FC00000u);
+    }
+    float total = many_sum<R>(sums);
+    if (lane % (32 / R) == 0) red[round & 1][warp][many_index<R>(lane)] = total;
+    asm volatile("bar.sync 1, %0;" ::"r"(L) : "memory");
+    total = 0.0f;
+    for (int q = lane % (32 / R); q < warps; q += 32 / R)
+      total = __fadd_rn(total, red[round & 1][q][many_index<R>(lane)]);
+#pragma unroll
+    for (int o = 16 / R; o > 0; o >>= 1) total = __fadd_rn(total, __shfl_xor_sync(kAll, total, o));
+    total = -__fmul_rn(total, inv_d);
+    if (a.y) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const float mean = __shfl_sync(kAll, total, i * (32 / R));
+        if (i >= live) continue;
+        const uint8_t* gs = base + (i + 1) * map.row - map.pitch + (Wide || !dh ? 0 : dh_row(r0 + i).offset);
+        const float rstd = stats[stage][i], k = __fmul_rn(mean, rstd);
+        E* out = static_cast<E*>(a.y) + (r0 + i) * a.y_stride;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const int c = 8 * (t + v * L);
+          Pack8<T> u;
+          F8 o = zero8();
+          if (dh) {
+            load_unit<T, Wide>(u, reinterpret_cast<const E*>(gs), c, d);
+            o = get8(u);
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            o.p[q] = fma2(mul2(f[i][v].p[q], w[v].p[q]), both(rstd), fma2(xh[i][v].p[q], both(k), o.p[q]));
+          put8(u, o);
+          store_unit<T, Wide>(u, out, c, d, true, 32);
+        }
+      }
+    }
+    __syncwarp();
+    // the stage has been read; after a wait that gave up its copies may still be in flight
+    if (lane == 0 && ok) mbar_arrive(smem_u32(&freed[stage]));
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+  if (!part) return;
+  float* to = part + static_cast<int64_t>(blockIdx.x) * d;
 #pragma unroll
   for (int v = 0; v < NV; ++v)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int64_t j = 8 * (t + static_cast<int64_t>(v) * per_row) + e;
-      w[v][e] = j < a.d ? (a.weight ? load_as(a.weight, j, a.weight_type) : 1.0f) : 0.0f;
-      dw[v][e] = 0.0f;
+      const int j = 8 * (t + v * L) + e;
+      const float s = e % 2 ? dw[v].p[e / 2].y : dw[v].p[e / 2].x;
+      if (j < d) to[j] = ok ? s : __uint_as_float(0x7FC00000u);
     }
-  Pack8<T> yn[NV], gn[NV], hn[H8 ? 1 : NV];
-  uint2 qn[H8 ? NV : 1];
-  uint32_t bn[H8 ? NV : 1];
-  float rstd_n = 0.0f;
-  auto fetch = [&](int64_t r) {
-    const bool live = r < a.rows;
-    rstd_n = live ? a.rstd_in[r] : 0.0f;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int64_t c = live ? 8 * (t + static_cast<int64_t>(v) * per_row) : a.d;
-      load_unit<T, Wide>(yn[v], dy + r * a.dy_stride, c, a.d);
-      if constexpr (H8) {
-        qn[v] = load_unit8<Wide>(static_cast<const uint8_t*>(a.x) + r * a.x_stride, c, a.d);
-        bn[v] = c < a.d ? a.x_scale[r * blocks + c / 32] : 127u;
-      } else {
-        load_unit<T, Wide>(hn[v], static_cast<const E*>(a.x) + r * a.x_stride, c, a.d);
-      }
-      if (dh) load_unit<T, Wide>(gn[v], dh + r * a.residual_stride, c, a.d);
-    }
-  };
-  int64_t r = static_cast<int64_t>(blockIdx.x) * groups + group;
-  const int64_t ahead = L < 32 ? threadIdx.x % 32 / L : 0;
-  fetch(r);
-  int parity = 0;
-#pragma unroll 1
-  for (; r - ahead < a.rows; r += step, parity ^= 1) {
-    const bool live = r < a.rows;
-    const float rstd = rstd_n;
-    Pack8<T> g[NV], dhp[NV];
-    float xh[NV][8], s = 0.0f;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      g[v] = yn[v];
-      if (dh) dhp[v] = gn[v];
-      if constexpr (H8) {
-        e4m3_unpack(qn[v], xh[v]);
-        const float k = __fmul_rn(block_scale_value(bn[v]), rstd);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) xh[v][e] = __fmul_rn(xh[v][e], k);
-      } else {
-        hn[v].get(xh[v]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) xh[v][e] = __fmul_rn(xh[v][e], rstd);
-      }
-      float f[8];
-      g[v].get(f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        s = __fmaf_rn(__fmul_rn(f[e], w[v][e]), xh[v][e], s);
-        dw[v][e] = __fmaf_rn(f[e], xh[v][e], dw[v][e]);
-      }
-    }
-    fetch(r + step);
-    float none = 0.0f;
-    row_join<L>(s, none, false, red, G, group, parity);
-    if (!a.y || !live) continue;
-    const float c = -__fmul_rn(__fmul_rn(s, inv_d), rstd);
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      float f[8], o[8];
-      g[v].get(f);
-      if (dh)
-        dhp[v].get(o);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        o[e] = __fmaf_rn(__fmul_rn(f[e], w[v][e]), rstd, __fmaf_rn(xh[v][e], c, dh ? o[e] : 0.0f));
-      Pack8<T> u;
-      u.put(o);
-      store_unit<T, Wide>(u, static_cast<E*>(a.y) + r * a.y_stride, 8 * (t + static_cast<int64_t>(v) * per_row), a.d);
-    }
-  }
-  if (!part) return;
-  float* to = part + static_cast<int64_t>(blockIdx.x) * a.d;
-  if (groups == 1) {
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int64_t j = 8 * (t + static_cast<int64_t>(v) * per_row) + e;
-        if (j < a.d) to[j] = dw[v][e];
-      }
-    return;
-  }
-  const int width = 8 * NV * per_row;
-#pragma unroll
-  for (int v = 0; v < NV; ++v)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) joined[group * width + 8 * (t + v * per_row) + e] = dw[v][e];
-  __syncthreads();
-  for (int j = threadIdx.x; j < a.d; j += blockDim.x) {
-    float s = 0.0f;
-    for (int q = 0; q < groups; ++q) s = __fadd_rn(s, joined[q * width + j]);
-    to[j] = s;
-  }
 }
 
 // Rows longer than the registers hold: dx row by row, in two passes.
 template <int T, bool H8>
 __device__ __forceinline__ float long_h(const RmsArgs& a, int64_t r, int64_t j) {
   if constexpr (H8) {
-    float f[8];
-    e4m3_unpack(make_uint2(static_cast<const uint8_t*>(a.x)[r * a.x_stride + j], 0u), f);
-    return __fmul_rn(f[0], block_scale_value(a.x_scale[r * ((a.d + 31) / 32) + j / 32]));
+    const F8 f = e4m3_unpack(make_uint2(static_cast<const uint8_t*>(a.x)[r * a.x_stride + j], 0u));
+    return __fmul_rn(f.p[0].x, block_scale_value(a.x_scale[r * ((a.d + 31) / 32) + j / 32]));
   } else {
     return Elem<T>::get(static_cast<const typename Elem<T>::type*>(a.x)[r * a.x_stride + j]);
   }
@@ -445,45 +737,45 @@ __global__ void __launch_bounds__(32 * kFinishSlices) rms_finish_kernel(void* dw
 
 // ---- launches -------------------------------------------------------------------
 
-// How the threads of a block share rows of d elements.
-struct RowPlan {
-  int lanes, units, warps, threads;  // lanes of a row if under a warp; units a thread; warps of a row; of a block
-};
-
-RowPlan row_plan(int64_t d, int64_t most_units) {
-  const int64_t units = (d + 7) / 8;
-  RowPlan p = {32, 1, 1, 256};
-  if (units <= 16) {
-    p.lanes = units <= 8 ? 8 : 16;
-    return p;
-  }
-  p.units = units > most_units ? 2 : 1;
-  p.warps = static_cast<int>((units + 32 * p.units - 1) / (32 * p.units));
-  p.threads = 32 * p.warps * std::max(1, 8 / p.warps);
-  return p;
+template <int T, bool Wide, int L>
+cudaError_t forward_short(const RmsArgs& a, const DeviceInfo& dev, cudaStream_t s) {
+  const int64_t groups = 256 / L, blocks = std::min<int64_t>((a.rows + groups - 1) / groups, 4 * dev.sms);
+  return launch_pdl(rms_forward_short_kernel<T, Wide, L>, static_cast<unsigned>(blocks), 256, s, a);
 }
 
-template <int T, bool Wide, int NV, int L>
-cudaError_t forward_rows(const RmsArgs& a, const RowPlan& p, const DeviceInfo& dev, cudaStream_t s) {
-  const int64_t groups = p.threads / (L < 32 ? L : 32 * p.warps);
-  const int64_t per_sm = std::max<int64_t>(1, 1024 / p.threads);
-  const int64_t blocks = std::min((a.rows + groups - 1) / groups, per_sm * dev.sms);
-  return launch_pdl(rms_forward_kernel<T, Wide, NV, L>, static_cast<unsigned>(blocks),
-                    static_cast<unsigned>(p.threads), s, a, p.warps);
+template <int T, bool Wide, int NV>
+cudaError_t forward_staged(const RmsArgs& a, int G, const DeviceInfo& dev, cudaStream_t s) {
+  static std::atomic<bool> ready[64];
+  const cudaError_t e = allow_shared(rms_forward_kernel<T, Wide, NV>, kSmShared - 4096, ready);
+  if (e != cudaSuccess) return e;
+  const uint32_t pitch = pieces_pitch(a.d * (T == MP_FP32 ? 4 : 2)), row = (a.residual ? 2 : 1) * pitch;
+  const uint32_t weights = static_cast<uint32_t>((a.d + 7) / 8 * 32), room = kSmShared - 4096 - weights;
+  // one block an SM: as many groups as have two stages each
+  const int groups = static_cast<int>(std::max<uint32_t>(1, std::min<uint32_t>(kMaxThreads / (32 * G), room / (2 * row))));
+  const int stages = static_cast<int>(std::max<uint32_t>(2, std::min<uint32_t>(kMaxStages, room / (groups * row))));
+  const int64_t blocks = std::min<int64_t>((a.rows + groups - 1) / groups, dev.sms);
+  return launch_pdl_smem(rms_forward_kernel<T, Wide, NV>, static_cast<unsigned>(blocks),
+                         static_cast<unsigned>(32 * G * groups), weights + static_cast<size_t>(stages) * groups * row,
+                         s, a, G, pitch, stages);
 }
 
 template <int T, bool Wide>
 cudaError_t forward_wide(const RmsArgs& a, const DeviceInfo& dev, cudaStream_t s) {
-  const RowPlan p = row_plan(a.d, 64);
-  if (p.lanes == 8) return forward_rows<T, Wide, 1, 8>(a, p, dev, s);
-  if (p.lanes == 16) return forward_rows<T, Wide, 1, 16>(a, p, dev, s);
-  if (p.units == 1) return forward_rows<T, Wide, 1, 32>(a, p, dev, s);
-  return forward_rows<T, Wide, 2, 32>(a, p, dev, s);
+  if (a.d <= 64) return forward_short<T, Wide, 8>(a, dev, s);
+  if (a.d <= 128) return forward_short<T, Wide, 16>(a, dev, s);
+  if (a.d <= kShortD) return forward_short<T, Wide, 32>(a, dev, s);
+  // Four units a thread, so that what a row costs each of its threads is shared by
+  // many elements; fewer where there are too few rows to fill the GPU with as many warps.
+  const int units = static_cast<int>((a.d + 7) / 8);
+  const auto warps = [&](int nv) { return (units + 32 * nv - 1) / (32 * nv); };
+  if (warps(1) <= kMaxThreads / 32 && a.rows * warps(2) < 8 * dev.sms) return forward_staged<T, Wide, 1>(a, warps(1), dev, s);
+  if (a.rows * warps(4) < 8 * dev.sms || units <= 64) return forward_staged<T, Wide, 2>(a, warps(2), dev, s);
+  return forward_staged<T, Wide, 4>(a, warps(4), dev, s);
 }
 
 template <int T>
 cudaError_t forward(const RmsArgs& a, const DeviceInfo& dev, cudaStream_t s) {
-  if (a.d > kRowD)
+  if (a.d > kStagedD)
     return launch_pdl(rms_forward_long_kernel<T>, static_cast<unsigned>(std::min<int64_t>(a.rows, 4 * dev.sms)),
                       kLongThreads, s, a);
   const bool wide = wide_rows(a.x, a.d, a.x_stride, a.rows, T) &&
@@ -500,61 +792,88 @@ cudaError_t forward_of(int32_t type, const RmsArgs& a, const DeviceInfo& dev, cu
                          : type == MP_FP16 ? forward<MP_FP16>(a, dev, s) : forward<MP_FP32>(a, dev, s);
 }
 
-// Blocks of the backward pass, from rows and d alone: they fix the order of the
-// sums over rows and the workspace.
-int backward_parts(int64_t rows, int64_t d) {
-  int64_t cap, per_block;  // blocks; rows that make a further block worth its partial sum
-  if (d > kRowD) {
-    cap = 64;
-    per_block = 32;
-  } else {
-    const RowPlan p = row_plan(d, 512);
-    const int64_t groups = p.threads / (p.lanes < 32 ? p.lanes : 32 * p.warps);
-    cap = std::max<int64_t>(1, 1024 / p.threads) * kSms;
-    per_block = 2 * groups;
+// Threads and blocks of the backward pass, from rows and d alone: they fix the
+// order of the sums over rows and the workspace.
+struct BackwardPlan {
+  int parts, units, threads, per_sm;  // blocks; units a thread; threads that compute
+};
+
+BackwardPlan backward_plan(int64_t rows, int64_t d) {
+  BackwardPlan p = {0, 1, 256, 4};
+  int64_t cap = 64, per_block = 32;  // blocks; rows that make a further block worth its partial sum
+  if (d <= kShortD) {
+    cap = 4 * kSms;
+    per_block = 2 * 256 / (d <= 64 ? 8 : d <= 128 ? 16 : 32);
+  } else if (d <= kStagedD) {
+    const int64_t units = (d + 7) / 8;
+    p.units = units > kMaxThreads ? 2 : 1;
+    p.threads = static_cast<int>((units + 32 * p.units - 1) / (32 * p.units) * 32);
+    p.per_sm = std::max(1, std::min(5, 18 / (p.threads / 32 + 1)));
+    cap = p.per_sm * kSms;
+    per_block = 2;
   }
-  return static_cast<int>(std::max<int64_t>(1, std::min(cap, (rows + per_block - 1) / per_block)));
+  p.parts = static_cast<int>(std::max<int64_t>(1, std::min(cap, (rows + per_block - 1) / per_block)));
+  return p;
 }
 
-template <int T, bool Wide, bool H8, int NV, int L>
-cudaError_t backward_rows(const RmsArgs& a, const RowPlan& p, int parts, float* part, cudaStream_t s) {
-  const int per_row = L < 32 ? L : 32 * p.warps;
-  const size_t smem = p.threads > per_row ? static_cast<size_t>(p.threads) * NV * 8 * sizeof(float) : 0;
-  return launch_pdl_smem(rms_backward_kernel<T, Wide, H8, NV, L>, static_cast<unsigned>(parts),
-                         static_cast<unsigned>(p.threads), smem, s, a, part, p.warps);
+template <int T, bool Wide, bool H8, int NV, int R>
+cudaError_t backward_staged(const RmsArgs& a, const BackwardPlan& p, float* part, StageMap map, uint32_t room,
+                            cudaStream_t s) {
+  static std::atomic<bool> ready[64];
+  const auto kernel = rms_backward_kernel<T, Wide, H8, NV, R>;
+  const cudaError_t e = allow_shared(kernel, kSmShared - 4096, ready);
+  if (e != cudaSuccess) return e;
+  map.size = R * map.row;
+  const int stages = static_cast<int>(std::max(2u, std::min<uint32_t>(kMaxStages, room / map.size)));
+  return launch_pdl_smem(kernel, static_cast<unsigned>(p.parts), static_cast<unsigned>(p.threads) + 32,
+                         static_cast<size_t>(stages) * map.size, s, a, part, map, stages);
+}
+
+template <int T, bool Wide, bool H8, int L>
+cudaError_t backward_short(const RmsArgs& a, const BackwardPlan& p, float* part, cudaStream_t s) {
+  return launch_pdl(rms_backward_short_kernel<T, Wide, H8, L>, static_cast<unsigned>(p.parts), 256, s, a, part);
 }
 
 template <int T, bool Wide, bool H8>
-cudaError_t backward_wide(const RmsArgs& a, int parts, float* part, cudaStream_t s) {
-  const RowPlan p = row_plan(a.d, 512);
-  if (p.lanes == 8) return backward_rows<T, Wide, H8, 1, 8>(a, p, parts, part, s);
-  if (p.lanes == 16) return backward_rows<T, Wide, H8, 1, 16>(a, p, parts, part, s);
-  if (p.units == 1) return backward_rows<T, Wide, H8, 1, 32>(a, p, parts, part, s);
-  return backward_rows<T, Wide, H8, 2, 32>(a, p, parts, part, s);
+cudaError_t backward_wide(const RmsArgs& a, const BackwardPlan& p, float* part, cudaStream_t s) {
+  if (a.d <= 64) return backward_short<T, Wide, H8, 8>(a, p, part, s);
+  if (a.d <= 128) return backward_short<T, Wide, H8, 16>(a, p, part, s);
+  if (a.d <= kShortD) return backward_short<T, Wide, H8, 32>(a, p, part, s);
+  StageMap map = {};
+  map.pitch = pieces_pitch(a.d * (T == MP_FP32 ? 4 : 2));
+  map.h_pitch = H8 ? pieces_pitch(a.d) : map.pitch;
+  map.scale_pitch = H8 ? pieces_pitch((a.d + 31) / 32) : 0;
+  map.row = map.pitch + map.h_pitch + map.scale_pitch + (a.residual ? map.pitch : 0);
+  // Rows a round: what registers hold next to the weights and their sums, two of one
+  // unit a thread or one of two; and what lets two rounds be staged.
+  const uint32_t room = kSmShared / static_cast<uint32_t>(p.per_sm) - 2048;
+  if (p.units == 2) return backward_staged<T, Wide, H8, 2, 1>(a, p, part, map, room, s);
+  if (4 * map.row <= room) return backward_staged<T, Wide, H8, 1, 2>(a, p, part, map, room, s);
+  return backward_staged<T, Wide, H8, 1, 1>(a, p, part, map, room, s);
 }
 
 template <int T, bool H8>
 cudaError_t backward(const RmsArgs& a, void* dweight, float* part, const DeviceInfo& dev, cudaStream_t s) {
-  const int parts = backward_parts(a.rows, a.d);
+  const BackwardPlan p = backward_plan(a.rows, a.d);
   cudaError_t e = cudaSuccess;
-  if (a.d <= kRowD) {
+  if (a.d <= kStagedD) {
     const bool wide = wide_rows(a.dy, a.d, a.dy_stride, a.rows, T) &&
                       (!a.residual || wide_rows(a.residual, a.d, a.residual_stride, a.rows, T)) &&
                       (!a.y || wide_rows(a.y, a.d, a.y_stride, a.rows, T)) &&
                       (H8 ? wide_rows8(a.x, a.d, a.x_stride, a.rows) : wide_rows(a.x, a.d, a.x_stride, a.rows, T));
     float* to = dweight ? part : nullptr;
-    e = wide ? backward_wide<T, true, H8>(a, parts, to, s) : backward_wide<T, false, H8>(a, parts, to, s);
+    e = wide ? backward_wide<T, true, H8>(a, p, to, s) : backward_wide<T, false, H8>(a, p, to, s);
   } else {
     const int64_t strips = (a.d + kLongThreads - 1) / kLongThreads;
     if (dweight)  // before dx, which may be written over dy or h
-      e = launch_pdl(rms_dw_long_kernel<T, H8>, static_cast<unsigned>(strips * parts), kLongThreads, s, a, part);
+      e = launch_pdl(rms_dw_long_kernel<T, H8>, static_cast<unsigned>(strips * p.parts), kLongThreads, s, a, part);
     if (e == cudaSuccess && a.y && a.rows)
       e = launch_pdl(rms_dx_long_kernel<T, H8>, static_cast<unsigned>(std::min<int64_t>(a.rows, 4 * dev.sms)),
                      kLongThreads, s, a);
   }
   if (e == cudaSuccess && dweight)
     e = launch_pdl(rms_finish_kernel, static_cast<unsigned>((a.d + 31) / 32), 32 * kFinishSlices, s, dweight,
-                   static_cast<const float*>(part), a.d, parts, a.weight_type);
+                   static_cast<const float*>(part), a.d, p.parts, a.weight_type);
   return e;
 }
 
@@ -636,7 +955,7 @@ extern "C" int mp_rmsnorm_forward(void* y, void* h, float* rstd, void* y8, void*
 extern "C" size_t mp_rmsnorm_workspace_bytes(int64_t rows, int64_t d) {
   using namespace mpk;
   if (!unit_shape_ok(rows, d)) return 0;
-  return static_cast<size_t>(backward_parts(rows, d)) * d * sizeof(float);
+  return static_cast<size_t>(backward_plan(rows, d).parts) * d * sizeof(float);
 }
 
 extern "C" int mp_rmsnorm_backward(void* dx, void* dweight, const void* dy, const void* dh, const void* h,
