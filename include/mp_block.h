@@ -183,7 +183,7 @@ int mp_rope_frequencies(uint64_t* turns, float* factor, int32_t rotary_dim, doub
  *               output); up NULL: none.
  *   gate8, up8  [rows, d], gate and up in 8 bits with gate8_scale and up8_scale
  *               of kind MP_SCALE_BLOCK, for the backward pass; NULL: not wanted.
- *   rows >= 0 (0 is a no-op), d in [1, 2^24], rows * ceil(d / 2048) < 2^31.
+ *   rows in [0, 2^31 - 1] (0 is a no-op), d in [1, 2^24].
  * A gate of -inf gives NaN.
  * Errors: MP_ERR_NULL, MP_ERR_ALIGN, MP_ERR_RANGE, MP_ERR_CUDA.
  * ------------------------------------------------------------------------- */
@@ -224,7 +224,7 @@ int mp_gated_backward(void* dgate, void* dup, void* y, const void* dy, const voi
  *
  *   x           [rows, d] of `type`.
  *   q           [rows, d] e4m3.
- *   rows >= 0 (0 is a no-op), d in [1, 2^24], rows * ceil(d / 2048) < 2^31.
+ *   rows in [0, 2^31 - 1] (0 is a no-op), d in [1, 2^24].
  * Errors: MP_ERR_NULL, MP_ERR_ALIGN, MP_ERR_RANGE, MP_ERR_CUDA.
  * ------------------------------------------------------------------------- */
 int mp_pack8(void* q, void* scale, const void* x, int64_t rows, int64_t d, int64_t q_stride, int64_t x_stride,

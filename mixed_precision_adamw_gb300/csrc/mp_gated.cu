@@ -33,10 +33,11 @@ struct GatedArgs {
   int64_t y_stride, dgate_stride, dup_stride, dy_stride, gate_stride, up_stride, gate8_stride, up8_stride;
 };
 
-// How a block lies over the matrix: `across` threads along a row, the rest down
-// the rows; `chunks` blocks cover a row.
+// How a block lies over the matrix: 2^across threads along a row, the rest down the
+// rows. The grid's x covers a row, y and z (y has no more than 65535) the rows.
 struct Tiling {
-  int across, chunks;
+  int across;
+  int chunks;
 };
 
 struct Place {
@@ -46,10 +47,10 @@ struct Place {
 };
 
 __device__ __forceinline__ Place place(const Tiling& g, int rows_a_thread) {
-  const int strip = static_cast<int>(blockIdx.x) / g.chunks, chunk = static_cast<int>(blockIdx.x) - strip * g.chunks;
-  const int down = kThreadsG / g.across;
-  return {static_cast<int64_t>(strip) * (down * rows_a_thread) + threadIdx.x / g.across,
-          8 * (chunk * g.across + static_cast<int>(threadIdx.x) % g.across), down, min(g.across, 32)};
+  const int down = kThreadsG >> g.across, t = static_cast<int>(threadIdx.x);
+  const int64_t strip = static_cast<int64_t>(blockIdx.z) * gridDim.y + blockIdx.y;
+  return {strip * (down * rows_a_thread) + (t >> g.across),
+          8 * ((static_cast<int>(blockIdx.x) << g.across) + (t & ((1 << g.across) - 1))), down, min(1 << g.across, 32)};
 }
 
 constexpr float kGelu = 1.5957691216057308f;  // 2 sqrt(2 / pi)
@@ -248,37 +249,46 @@ __global__ void __launch_bounds__(kThreadsG) unpack_kernel(Rows8Args a, Tiling g
 // of them along the row where that is equal. Whole quads of lanes (32 columns).
 Tiling tiling(int64_t d) {
   const int units = static_cast<int>((d + 31) / 32 * 4);
-  Tiling best = {kThreadsG, (units + kThreadsG - 1) / kThreadsG};
-  for (int across = kThreadsG / 2; across >= 8; across /= 2) {
-    const int chunks = (units + across - 1) / across;
-    if (chunks * across < best.chunks * best.across) best = {across, chunks};
+  Tiling best = {};
+  for (int across = 8; across >= 3; --across) {
+    const int chunks = (units + (1 << across) - 1) >> across;
+    if (across == 8 || (chunks << across) < (best.chunks << best.across)) best = {across, chunks};
   }
   return best;
 }
 
 template <int R, typename Args>
-cudaError_t launch_tiled(void (*kernel)(Args, Tiling), const Args& a, const Tiling& g, cudaStream_t s) {
-  const int64_t per_block = static_cast<int64_t>(kThreadsG / g.across) * R;
-  const int64_t strips = (a.rows + per_block - 1) / per_block;
-  return launch_pdl(kernel, static_cast<unsigned>(strips * g.chunks), kThreadsG, s, a, g);
+cudaError_t launch_tiled(void (*kernel)(Args, Tiling), const Args& a, cudaStream_t s) {
+  const Tiling g = tiling(a.d);
+  const int64_t per_block = static_cast<int64_t>(kThreadsG >> g.across) * R;
+  const int64_t strips = (a.rows + per_block - 1) / per_block, y = std::min<int64_t>(strips, 65535);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(g.chunks), static_cast<unsigned>(y), static_cast<unsigned>((strips + y - 1) / y));
+  cfg.blockDim = dim3(kThreadsG);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, g);
 }
 
-constexpr int kRowsAThread = 2;
-
+// Rows a thread: two for the activation, whose three and four streams take the
+// registers, four for the two streams of 8 bits.
 template <int T, int Act>
 cudaError_t gated_forward(const GatedArgs& a, cudaStream_t s) {
-  constexpr int R = kRowsAThread;
+  constexpr int R = 2;
   const bool wide = wide_rows(a.y, a.d, a.y_stride, a.rows, T) && wide_rows(a.gate, a.d, a.gate_stride, a.rows, T) &&
                     (!a.up || wide_rows(a.up, a.d, a.up_stride, a.rows, T)) &&
                     (!a.gate8 || wide_rows8(a.gate8, a.d, a.gate8_stride, a.rows)) &&
                     (!a.up8 || wide_rows8(a.up8, a.d, a.up8_stride, a.rows));
-  return launch_tiled<R>(wide ? gated_forward_kernel<T, true, Act, R> : gated_forward_kernel<T, false, Act, R>, a,
-                         tiling(a.d), s);
+  return launch_tiled<R>(wide ? gated_forward_kernel<T, true, Act, R> : gated_forward_kernel<T, false, Act, R>, a, s);
 }
 
 template <int T, int Act>
 cudaError_t gated_backward(const GatedArgs& a, cudaStream_t s) {
-  constexpr int R = kRowsAThread;
+  constexpr int R = 2;
   const bool kept = a.gate_scale;
   const auto source = [&](const void* p, int64_t stride) {
     return !p || (kept ? wide_rows8(p, a.d, stride, a.rows) : wide_rows(p, a.d, stride, a.rows, T));
@@ -289,27 +299,25 @@ cudaError_t gated_backward(const GatedArgs& a, cudaStream_t s) {
                     (!a.y || wide_rows(a.y, a.d, a.y_stride, a.rows, T));
   const auto kernel = kept ? (wide ? gated_backward_kernel<T, true, true, Act, R> : gated_backward_kernel<T, false, true, Act, R>)
                            : (wide ? gated_backward_kernel<T, true, false, Act, R> : gated_backward_kernel<T, false, false, Act, R>);
-  return launch_tiled<R>(kernel, a, tiling(a.d), s);
+  return launch_tiled<R>(kernel, a, s);
 }
 
 template <int T>
 cudaError_t pack_blocks(const Rows8Args& a, cudaStream_t s) {
-  constexpr int R = kRowsAThread;
+  constexpr int R = 4;
   const bool wide = wide_rows(a.x_in, a.d, a.x_stride, a.rows, T) && wide_rows8(a.q, a.d, a.q_stride, a.rows);
-  return launch_tiled<R>(wide ? pack_blocks_kernel<T, true, R> : pack_blocks_kernel<T, false, R>, a, tiling(a.d), s);
+  return launch_tiled<R>(wide ? pack_blocks_kernel<T, true, R> : pack_blocks_kernel<T, false, R>, a, s);
 }
 
 template <int T>
 cudaError_t unpack(const Rows8Args& a, cudaStream_t s) {
-  constexpr int R = kRowsAThread;
+  constexpr int R = 4;
   const bool wide = wide_rows(a.x, a.d, a.x_stride, a.rows, T) && wide_rows8(a.q_in, a.d, a.q_stride, a.rows);
-  return launch_tiled<R>(wide ? unpack_kernel<T, true, R> : unpack_kernel<T, false, R>, a, tiling(a.d), s);
+  return launch_tiled<R>(wide ? unpack_kernel<T, true, R> : unpack_kernel<T, false, R>, a, s);
 }
 
 // Rows whose blocks a grid can count.
-bool tiled_ok(int64_t rows, int64_t d) {
-  return unit_shape_ok(rows, d) && rows <= INT32_MAX && rows * tiling(d).chunks <= INT32_MAX;
-}
+bool tiled_ok(int64_t rows, int64_t d) { return unit_shape_ok(rows, d) && rows <= INT32_MAX; }
 
 bool act_ok(int32_t act) { return act == MP_ACT_SILU || act == MP_ACT_GELU; }
 

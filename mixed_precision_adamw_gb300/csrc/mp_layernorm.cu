@@ -419,6 +419,36 @@ __global__ void __launch_bounds__(kLnThreads) ln_forward_long_kernel(LnArgs a) {
 // registers, and a block writes its sums once, part[block][0 or 1][d]; a
 // second, small launch adds the blocks' sums in block order.
 
+// Adds N per-lane values over the 32 lanes: N / 2 + N / 4 + ... + 1 shuffles
+// halve the values each lane carries, the rest finish the one left. Lane l
+// ends with the total of value many_index<N>(l).
+template <int N>
+__device__ __forceinline__ float many_sum(float (&v)[N]) {
+  const int lane = threadIdx.x % 32;
+  int o = 16;
+#pragma unroll
+  for (int n = N; n > 1; n /= 2) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) {
+      const float send = up ? v[i] : v[i + n / 2];
+      const float keep = up ? v[i + n / 2] : v[i];
+      v[i] = __fadd_rn(keep, __shfl_xor_sync(kAll, send, o));
+    }
+    o >>= 1;
+  }
+  float s = v[0];
+#pragma unroll
+  for (int q = 16 / N; q > 0; q >>= 1) s = __fadd_rn(s, __shfl_xor_sync(kAll, s, q));
+  return s;
+}
+
+// The value whose total lane l holds: the top log2(N) bits of l.
+template <int N>
+__device__ __forceinline__ int many_index(int lane) {
+  return lane / (32 / N);
+}
+
 // Rows of up to 8 * NV * L elements for the block's L computing threads, R rows
 // a round. The last warp stages the rounds' rows of x and dy, their mean and
 // rstd and the elements that the copies leave out, as stages become free; what

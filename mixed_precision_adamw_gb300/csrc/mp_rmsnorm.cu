@@ -457,33 +457,32 @@ __global__ void __launch_bounds__(256) rms_backward_short_kernel(RmsArgs a, floa
   }
 }
 
-// Longer rows: all but the last warp of a block compute, NV units a thread, R rows
-// a round; the last warp stages the rounds' rows of dy, h (and its scales) and dh,
-// and their rstd, as stages become free. One barrier a round joins the rows' sums
-// (which alternate between two buffers).
-constexpr int kBackwardThreads = 576;  // the most that share an SM's registers: 96 each
-
-struct StageMap {  // of one stage in bytes
-  uint32_t pitch, h_pitch, scale_pitch;  // a row of dy and dh; of h; of h's scales
-  uint32_t row, size;                    // all of one row; of R rows
+// Longer rows: groups of G warps take a row each, NV units a thread, from a ring of
+// staged rows (dy, h and its scales, dh) of their own, as in the forward pass. dy, xh and
+// dh stay in registers from the sum to dx, so a row's one barrier also says that its
+// stage has been read. At the end a block's groups add their weight gradients
+// through shared memory.
+struct StageMap {  // a stage in bytes
+  uint32_t pitch, h_pitch;  // a row of dy and dh; of h
+  uint32_t size;
 };
 
-template <int T, bool Wide, bool H8, int NV, int R>
-__global__ void __launch_bounds__(kBackwardThreads, 1)
-rms_backward_kernel(RmsArgs a, float* part, StageMap map, int stages) {
+template <int T, bool Wide, bool H8, int NV>
+__global__ void __launch_bounds__(kMaxThreads, 1)
+rms_backward_kernel(RmsArgs a, float* part, int G, StageMap map, int stages) {
   pdl_enter();
   using E = typename Elem<T>::type;
-  __shared__ float red[2][kMaxThreads / 32][R];
-  __shared__ float stats[kMaxStages][R];  // rstd of a stage's rows
-  __shared__ unsigned long long full[kMaxStages], freed[kMaxStages];
   extern __shared__ __align__(128) uint8_t smem[];
-  const int t = threadIdx.x, L = blockDim.x - 32, lane = t % 32, warp = t / 32, warps = L / 32;
-  const int64_t begin = a.rows * blockIdx.x / gridDim.x, end = a.rows * (blockIdx.x + 1) / gridDim.x;
-  const int64_t rounds = (end - begin + R - 1) / R, blocks = (a.d + 31) / 32;
+  __shared__ float red[2][kMaxThreads / 32];
+  __shared__ unsigned long long full[kMaxThreads / 32 * kMaxStages];
+  const int L = 32 * G, t = threadIdx.x % L, group = threadIdx.x / L, groups = blockDim.x / L;
   const int d = static_cast<int>(a.d);
-  if (t < stages) {
-    mbar_init(smem_u32(&full[t]), 1);
-    mbar_init(smem_u32(&freed[t]), warps);
+  const uint32_t blocks = (d + 31) / 32;
+  const bool has_dh = a.residual;
+  uint8_t* ring = smem + static_cast<size_t>(group) * stages * map.size;
+  const int64_t first = a.rows * blockIdx.x / gridDim.x + group, end = a.rows * (blockIdx.x + 1) / gridDim.x;
+  if (threadIdx.x < groups * stages) {
+    mbar_init(smem_u32(&full[threadIdx.x]), 1);
     mbar_init_fence();
   }
   __syncthreads();
@@ -493,64 +492,33 @@ rms_backward_kernel(RmsArgs a, float* part, StageMap map, int stages) {
   auto dy_row = [&](int64_t r) { return Pieces(dy + r * a.dy_stride, length); };
   auto dh_row = [&](int64_t r) { return Pieces(dh + r * a.residual_stride, length); };
   auto h_row = [&](int64_t r) {
-    return H8 ? Pieces(static_cast<const uint8_t*>(a.x) + r * a.x_stride, static_cast<uint32_t>(a.d))
+    return H8 ? Pieces(static_cast<const uint8_t*>(a.x) + r * a.x_stride, static_cast<uint32_t>(d))
               : Pieces(static_cast<const E*>(a.x) + r * a.x_stride, length);
   };
-  auto scale_row = [&](int64_t r) { return Pieces(a.x_scale + r * blocks, static_cast<uint32_t>(blocks)); };
-  if (warp == warps) {  // the staging warp
-    float stat = lane < R && begin + lane < end ? a.rstd_in[begin + lane] : 0.0f;
-    int stage = 0;
-    uint32_t phase = 1;
-    int64_t round = 0;
-    for (; round < rounds; ++round) {
-      const int64_t r0 = begin + round * R;
-      if (round >= stages && !__all_sync(kAll, mbar_wait(smem_u32(&freed[stage]), phase))) break;
-      const uint32_t bar = smem_u32(&full[stage]), to = smem_u32(smem + stage * map.size);
-      if (lane < R) stats[stage][lane] = stat;
-      __syncwarp();
-      if (lane == 0) {
-        uint32_t bytes = 0;
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-          if (r0 + i < end) {
-            bytes += dy_row(r0 + i).bytes + h_row(r0 + i).bytes;
-            if (H8) bytes += scale_row(r0 + i).bytes;
-            if (dh) bytes += dh_row(r0 + i).bytes;
-          }
-        mbar_expect_tx(bar, bytes);
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-          if (r0 + i < end) {
-            uint32_t at = to + i * map.row;
-            const Pieces p = dy_row(r0 + i), q = h_row(r0 + i);
-            bulk_load(at, p.src, p.bytes, bar);
-            at += map.pitch;
-            bulk_load(at, q.src, q.bytes, bar);
-            at += map.h_pitch;
-            if (H8) {
-              const Pieces s = scale_row(r0 + i);
-              bulk_load(at, s.src, s.bytes, bar);
-              at += map.scale_pitch;
-            }
-            if (dh) {
-              const Pieces g = dh_row(r0 + i);
-              bulk_load(at, g.src, g.bytes, bar);
-            }
-          }
-      }
-      const int64_t next = r0 + R + lane;
-      stat = lane < R && next < end ? a.rstd_in[next] : 0.0f;
-      if (++stage == stages) {
-        stage = 0;
-        phase ^= 1;
-      }
+  auto scale_row = [&](int64_t r) { return Pieces(a.x_scale + r * blocks, blocks); };
+  // In a stage: dy, dh (if any), h, h's scales.
+  const uint32_t h_at = has_dh ? 2 * map.pitch : map.pitch;
+  auto fetch = [&](int64_t r, int stage) {  // by the group's first thread
+    if (r >= end) return;
+    const uint32_t bar = smem_u32(&full[group * stages + stage]), to = smem_u32(ring + stage * map.size);
+    const Pieces p = dy_row(r), q = h_row(r);
+    uint32_t bytes = p.bytes + q.bytes;
+    if (has_dh) bytes += dh_row(r).bytes;
+    if (H8) bytes += scale_row(r).bytes;
+    mbar_expect_tx(bar, bytes);
+    bulk_load(to, p.src, p.bytes, bar);
+    if (has_dh) {
+      const Pieces g = dh_row(r);
+      bulk_load(to + map.pitch, g.src, g.bytes, bar);
     }
-    // copies in flight land before the block ends
-    if (lane == 0)
-      for (int64_t i = max(int64_t{0}, round - stages); i < round; ++i)
-        mbar_drain(smem_u32(&full[i % stages]), (i / stages) & 1);
-    return;
-  }
+    bulk_load(to + h_at, q.src, q.bytes, bar);
+    if (H8) {
+      const Pieces s = scale_row(r);
+      bulk_load(to + h_at + map.h_pitch, s.src, s.bytes, bar);
+    }
+  };
+  if (t == 0)
+    for (int i = 0; i < stages; ++i) fetch(first + static_cast<int64_t>(i) * groups, i);
   const float inv_d = __fdiv_rn(1.0f, static_cast<float>(d));
   F8 w[NV], dw[NV];
 #pragma unroll
@@ -558,101 +526,107 @@ rms_backward_kernel(RmsArgs a, float* part, StageMap map, int stages) {
     w[v] = load_weights(a, 8 * (t + v * L));
     dw[v] = zero8();
   }
+  float rstd_next = first < end ? a.rstd_in[first] : 0.0f;
   bool ok = true;
-  int stage = 0;
+  int stage = 0, parity = 0;
   uint32_t phase = 0;
+  int64_t gave_up = 0;
 #pragma unroll 1
-  for (int64_t round = 0; round < rounds; ++round) {
-    const int64_t r0 = begin + round * R;
-    const int live = static_cast<int>(min(static_cast<int64_t>(R), end - r0));
-    // A wait that gives up (only a fault can cause that) makes the sums NaN.
-    ok = ok && mbar_wait(smem_u32(&full[stage]), phase);
-    const uint8_t* base = smem + stage * map.size;
-    float sums[R];
-    F8 xh[R][NV], f[R][NV];
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      float2 s2 = make_float2(0.0f, 0.0f);
-      if (i < live) {
-        const uint8_t* at = base + i * map.row;
-        const uint8_t* ys = at + (Wide ? 0 : dy_row(r0 + i).offset);
-        // 8-bit rows are on an 8-byte grid at least
-        const uint8_t* hs = at + map.pitch + (Wide && !H8 ? 0 : h_row(r0 + i).offset);
-        const uint8_t* ss = H8 ? at + map.pitch + map.h_pitch + scale_row(r0 + i).offset : nullptr;
-        const float rstd = stats[stage][i];
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          const int c = 8 * (t + v * L);
-          Pack8<T> u;
-          if constexpr (H8) {
-            xh[i][v] = normalised(load_unit8<Wide>(hs, c, d), c < d ? ss[c / 32] : 127u, rstd);
-          } else {
-            load_unit<T, Wide>(u, reinterpret_cast<const E*>(hs), c, d);
-            xh[i][v] = normalised(u, rstd);
-          }
-          load_unit<T, Wide>(u, reinterpret_cast<const E*>(ys), c, d);
-          f[i][v] = get8(u);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            s2 = fma2(mul2(f[i][v].p[q], w[v].p[q]), xh[i][v].p[q], s2);
-            dw[v].p[q] = fma2(f[i][v].p[q], xh[i][v].p[q], dw[v].p[q]);
-          }
-        }
-      }
-      sums[i] = ok ? __fadd_rn(s2.x, s2.y) : __uint_as_float(0x7FC00000u);
+  for (int64_t r = first; r < end; r += groups, parity ^= 1) {
+    const float rstd = rstd_next;
+    if (r + groups < end) rstd_next = a.rstd_in[r + groups];
+    // a wait that gives up (only a fault can cause that) makes what follows NaN,
+    // and nothing more is fetched
+    if (ok && !mbar_wait(smem_u32(&full[group * stages + stage]), phase)) {
+      ok = false;
+      gave_up = r;
     }
-    float total = many_sum<R>(sums);
-    if (lane % (32 / R) == 0) red[round & 1][warp][many_index<R>(lane)] = total;
-    asm volatile("bar.sync 1, %0;" ::"r"(L) : "memory");
-    total = 0.0f;
-    for (int q = lane % (32 / R); q < warps; q += 32 / R)
-      total = __fadd_rn(total, red[round & 1][q][many_index<R>(lane)]);
+    const uint8_t* at = ring + stage * map.size;
+    const E* ys = reinterpret_cast<const E*>(at + (Wide ? 0 : dy_row(r).offset));
+    const E* gs = reinterpret_cast<const E*>(at + map.pitch + (Wide || !has_dh ? 0 : dh_row(r).offset));
+    // 8-bit rows are on an 8-byte grid at least
+    const uint8_t* hs = at + h_at + (Wide && !H8 ? 0 : h_row(r).offset);
+    const uint8_t* ss = H8 ? at + h_at + map.h_pitch + scale_row(r).offset : nullptr;
+    F8 xh[NV], f[NV];
+    Pack8<T> e[NV];
+    float2 s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int o = 16 / R; o > 0; o >>= 1) total = __fadd_rn(total, __shfl_xor_sync(kAll, total, o));
-    total = -__fmul_rn(total, inv_d);
+    for (int v = 0; v < NV; ++v) {
+      const int c = 8 * (t + v * L);
+      Pack8<T> u;
+      if constexpr (H8) {
+        xh[v] = normalised(load_unit8<Wide>(hs, c, d), c < d ? ss[static_cast<uint32_t>(c) / 32] : 127u, rstd);
+      } else {
+        load_unit<T, Wide>(u, reinterpret_cast<const E*>(hs), c, d);
+        xh[v] = normalised(u, rstd);
+      }
+      load_unit<T, Wide>(u, ys, c, d);
+      f[v] = get8(u);
+      if (has_dh)
+        load_unit<T, Wide>(e[v], gs, c, d);
+      else
+        e[v].zero();
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        dw[v].p[q] = fma2(f[v].p[q], xh[v].p[q], dw[v].p[q]);
+        f[v].p[q] = mul2(f[v].p[q], w[v].p[q]);
+        s2 = fma2(f[v].p[q], xh[v].p[q], s2);
+      }
+    }
+    float s = warp_sum(__fadd_rn(s2.x, s2.y));
+    if (!ok) s = __uint_as_float(0x7FC00000u);
+    if (G > 1) {
+      if (t % 32 == 0) red[parity][threadIdx.x / 32] = s;
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(L) : "memory");
+      s = 0.0f;
+      for (int i = 0; i < G; ++i) s = __fadd_rn(s, red[parity][group * G + i]);
+    } else {
+      __syncwarp();
+    }
+    if (t == 0 && ok) fetch(r + static_cast<int64_t>(stages) * groups, stage);
     if (a.y) {
+      const float k = -__fmul_rn(__fmul_rn(s, inv_d), rstd);
+      E* out = static_cast<E*>(a.y) + r * a.y_stride;
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const float mean = __shfl_sync(kAll, total, i * (32 / R));
-        if (i >= live) continue;
-        const uint8_t* gs = base + (i + 1) * map.row - map.pitch + (Wide || !dh ? 0 : dh_row(r0 + i).offset);
-        const float rstd = stats[stage][i], k = __fmul_rn(mean, rstd);
-        E* out = static_cast<E*>(a.y) + (r0 + i) * a.y_stride;
+      for (int v = 0; v < NV; ++v) {
+        F8 o = get8(e[v]);
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          const int c = 8 * (t + v * L);
-          Pack8<T> u;
-          F8 o = zero8();
-          if (dh) {
-            load_unit<T, Wide>(u, reinterpret_cast<const E*>(gs), c, d);
-            o = get8(u);
-          }
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            o.p[q] = fma2(mul2(f[i][v].p[q], w[v].p[q]), both(rstd), fma2(xh[i][v].p[q], both(k), o.p[q]));
-          put8(u, o);
-          store_unit<T, Wide>(u, out, c, d, true, 32);
-        }
+        for (int q = 0; q < 4; ++q) o.p[q] = fma2(f[v].p[q], both(rstd), fma2(xh[v].p[q], both(k), o.p[q]));
+        put8(e[v], o);
+        store_unit<T, Wide>(e[v], out, 8 * (t + v * L), d, true, 32);
       }
     }
-    __syncwarp();
-    // the stage has been read; after a wait that gave up its copies may still be in flight
-    if (lane == 0 && ok) mbar_arrive(smem_u32(&freed[stage]));
     if (++stage == stages) {
       stage = 0;
       phase ^= 1;
     }
   }
+  // the copies that were not waited for land before the block ends
+  if (!ok && t == 0) {
+    const int64_t round = (gave_up - first) / groups;
+    for (int64_t i = round; i < round + stages && first + i * groups < end; ++i)
+      mbar_drain(smem_u32(&full[group * stages + i % stages]), (i / stages) & 1);
+  }
   if (!part) return;
+  if (!ok)
+#pragma unroll
+    for (int v = 0; v < NV; ++v) dw[v] = mul8(dw[v], __uint_as_float(0x7FC00000u));
+  __syncthreads();  // no stage is read or filled any more
+  float* joined = reinterpret_cast<float*>(smem);
+  const int width = 8 * NV * L;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    float4* to = reinterpret_cast<float4*>(joined + group * width + 8 * (t + v * L));
+    to[0] = make_float4(dw[v].p[0].x, dw[v].p[0].y, dw[v].p[1].x, dw[v].p[1].y);
+    to[1] = make_float4(dw[v].p[2].x, dw[v].p[2].y, dw[v].p[3].x, dw[v].p[3].y);
+  }
+  __syncthreads();
   float* to = part + static_cast<int64_t>(blockIdx.x) * d;
-#pragma unroll
-  for (int v = 0; v < NV; ++v)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int j = 8 * (t + v * L) + e;
-      const float s = e % 2 ? dw[v].p[e / 2].y : dw[v].p[e / 2].x;
-      if (j < d) to[j] = ok ? s : __uint_as_float(0x7FC00000u);
-    }
+  for (int j = threadIdx.x; j < d; j += blockDim.x) {
+    float s = 0.0f;
+    for (int q = 0; q < groups; ++q) s = __fadd_rn(s, joined[q * width + j]);
+    to[j] = s;
+  }
 }
 
 // Rows longer than the registers hold: dx row by row, in two passes.
@@ -795,38 +769,25 @@ cudaError_t forward_of(int32_t type, const RmsArgs& a, const DeviceInfo& dev, cu
 // Threads and blocks of the backward pass, from rows and d alone: they fix the
 // order of the sums over rows and the workspace.
 struct BackwardPlan {
-  int parts, units, threads, per_sm;  // blocks; units a thread; threads that compute
+  int parts, G, groups;  // blocks; warps of a row; rows that a block has in hand
 };
 
+constexpr int kBackwardUnits = 2;  // a thread's
+
 BackwardPlan backward_plan(int64_t rows, int64_t d) {
-  BackwardPlan p = {0, 1, 256, 4};
+  BackwardPlan p = {0, 1, 1};
   int64_t cap = 64, per_block = 32;  // blocks; rows that make a further block worth its partial sum
   if (d <= kShortD) {
     cap = 4 * kSms;
     per_block = 2 * 256 / (d <= 64 ? 8 : d <= 128 ? 16 : 32);
   } else if (d <= kStagedD) {
-    const int64_t units = (d + 7) / 8;
-    p.units = units > kMaxThreads ? 2 : 1;
-    p.threads = static_cast<int>((units + 32 * p.units - 1) / (32 * p.units) * 32);
-    p.per_sm = std::max(1, std::min(5, 18 / (p.threads / 32 + 1)));
-    cap = p.per_sm * kSms;
-    per_block = 2;
+    p.G = static_cast<int>((d + 255 * kBackwardUnits) / (256 * kBackwardUnits));
+    p.groups = std::max(1, kMaxThreads / 32 / p.G);
+    cap = kSms;
+    per_block = p.groups;
   }
   p.parts = static_cast<int>(std::max<int64_t>(1, std::min(cap, (rows + per_block - 1) / per_block)));
   return p;
-}
-
-template <int T, bool Wide, bool H8, int NV, int R>
-cudaError_t backward_staged(const RmsArgs& a, const BackwardPlan& p, float* part, StageMap map, uint32_t room,
-                            cudaStream_t s) {
-  static std::atomic<bool> ready[64];
-  const auto kernel = rms_backward_kernel<T, Wide, H8, NV, R>;
-  const cudaError_t e = allow_shared(kernel, kSmShared - 4096, ready);
-  if (e != cudaSuccess) return e;
-  map.size = R * map.row;
-  const int stages = static_cast<int>(std::max(2u, std::min<uint32_t>(kMaxStages, room / map.size)));
-  return launch_pdl_smem(kernel, static_cast<unsigned>(p.parts), static_cast<unsigned>(p.threads) + 32,
-                         static_cast<size_t>(stages) * map.size, s, a, part, map, stages);
 }
 
 template <int T, bool Wide, bool H8, int L>
@@ -839,17 +800,20 @@ cudaError_t backward_wide(const RmsArgs& a, const BackwardPlan& p, float* part, 
   if (a.d <= 64) return backward_short<T, Wide, H8, 8>(a, p, part, s);
   if (a.d <= 128) return backward_short<T, Wide, H8, 16>(a, p, part, s);
   if (a.d <= kShortD) return backward_short<T, Wide, H8, 32>(a, p, part, s);
+  constexpr int NV = kBackwardUnits;
+  static std::atomic<bool> ready[64];
+  const auto kernel = rms_backward_kernel<T, Wide, H8, NV>;
+  const cudaError_t e = allow_shared(kernel, kSmShared - 4096, ready);
+  if (e != cudaSuccess) return e;
   StageMap map = {};
   map.pitch = pieces_pitch(a.d * (T == MP_FP32 ? 4 : 2));
   map.h_pitch = H8 ? pieces_pitch(a.d) : map.pitch;
-  map.scale_pitch = H8 ? pieces_pitch((a.d + 31) / 32) : 0;
-  map.row = map.pitch + map.h_pitch + map.scale_pitch + (a.residual ? map.pitch : 0);
-  // Rows a round: what registers hold next to the weights and their sums, two of one
-  // unit a thread or one of two; and what lets two rounds be staged.
-  const uint32_t room = kSmShared / static_cast<uint32_t>(p.per_sm) - 2048;
-  if (p.units == 2) return backward_staged<T, Wide, H8, 2, 1>(a, p, part, map, room, s);
-  if (4 * map.row <= room) return backward_staged<T, Wide, H8, 1, 2>(a, p, part, map, room, s);
-  return backward_staged<T, Wide, H8, 1, 1>(a, p, part, map, room, s);
+  map.size = (a.residual ? 2 : 1) * map.pitch + map.h_pitch + (H8 ? pieces_pitch((a.d + 31) / 32) : 0);
+  const uint32_t per_stage = p.groups * map.size;
+  const int stages = static_cast<int>(std::max(2u, std::min<uint32_t>(kMaxStages, (kSmShared - 4096) / per_stage)));
+  const uint32_t threads = 32 * p.G * p.groups;
+  const size_t smem = std::max<size_t>(static_cast<size_t>(stages) * per_stage, threads * 8 * NV * sizeof(float));
+  return launch_pdl_smem(kernel, static_cast<unsigned>(p.parts), threads, smem, s, a, part, p.G, map, stages);
 }
 
 template <int T, bool H8>

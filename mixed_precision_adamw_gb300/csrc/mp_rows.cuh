@@ -121,36 +121,6 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// Adds N per-lane values over the 32 lanes: N / 2 + N / 4 + ... + 1 shuffles
-// halve the values each lane carries, the rest finish the one left. Lane l
-// ends with the total of value many_index<N>(l).
-template <int N>
-__device__ __forceinline__ float many_sum(float (&v)[N]) {
-  const int lane = threadIdx.x % 32;
-  int o = 16;
-#pragma unroll
-  for (int n = N; n > 1; n /= 2) {
-    const bool up = lane & o;
-#pragma unroll
-    for (int i = 0; i < n / 2; ++i) {
-      const float send = up ? v[i] : v[i + n / 2];
-      const float keep = up ? v[i + n / 2] : v[i];
-      v[i] = __fadd_rn(keep, __shfl_xor_sync(kAll, send, o));
-    }
-    o >>= 1;
-  }
-  float s = v[0];
-#pragma unroll
-  for (int q = 16 / N; q > 0; q >>= 1) s = __fadd_rn(s, __shfl_xor_sync(kAll, s, q));
-  return s;
-}
-
-// The value whose total lane l holds: the top log2(N) bits of l.
-template <int N>
-__device__ __forceinline__ int many_index(int lane) {
-  return lane / (32 / N);
-}
-
 // ---- eight elements of a row ------------------------------------------------
 // A thread's unit of a row is eight elements, kept as stored until used. With
 // Wide they are consecutive (16-B loads and stores; the row must start on a
