@@ -15,7 +15,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import _check, _lib, _stream
+from . import _binding, _check, _lib, _raw_stream, _stream
 from .train import MP_FP32, MP_INT64, _F32, _INDEX_TYPES, _TYPES, _U8, _index_type, _matrix, _on, _rows, _vector, _weight_type
 
 MP_SCALE_ROW, MP_SCALE_BLOCK = 1, 2
@@ -52,6 +52,25 @@ def _declare():
 
 
 _declare()
+
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _current_stream(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+_current_stream = _raw_stream or _current_stream  # without a Stream object, where PyTorch can
+
+# _binding makes the ordinary calls (each function below begins with it) and
+# returns None for all others: those go through the checks here, which name
+# what is wrong.
+_binding.bind(torch.Tensor, torch.nn.Parameter,
+              (torch.bfloat16, torch.float16, torch.float32, torch.uint8, torch.float8_e4m3fn, torch.int32,
+               torch.int64), _device, _current_stream,
+              tuple(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in
+                    ("mp_rmsnorm_forward", "mp_rmsnorm_backward", "mp_rope", "mp_gated_forward",
+                     "mp_gated_backward", "mp_pack8", "mp_unpack8")))
 
 
 def _matrix8(t, scale, name: str, dev: int, rows: int, d: int):
@@ -91,25 +110,27 @@ def mp_rmsnorm_forward(y: Optional[torch.Tensor], x: torch.Tensor, weight: Optio
     backward pass), y8 (y in 8 bits, scales of either kind) and h8 (h in 8 bits for the
     backward pass, scales of 32 columns) are written if given; y may be None.
     y and h may be x or residual themselves."""
+    st = _binding.rmsnorm_forward(y, x, weight, eps, residual, h, rstd, y8, y8_scale, h8, h8_scale, stream)
+    if st is None:
+        st = _rmsnorm_forward(y, x, weight, eps, residual, h, rstd, y8, y8_scale, h8, h8_scale, stream)
+    if st:
+        _check(st, "mp_rmsnorm_forward")
+
+
+def _rmsnorm_forward(y, x, weight, eps, residual, h, rstd, y8, y8_scale, h8, h8_scale, stream) -> int:
     dev = torch.cuda.current_device()
     xp, xs, code = _matrix(x, "x", dev)
     rows, d = x.shape
     yp, ys, _ = (None, 0, 0) if y is None else _matrix(y, "y", dev, x)
     rp, rs, _ = (None, 0, 0) if residual is None else _matrix(residual, "residual", dev, x)
     hp, hs, _ = (None, 0, 0) if h is None else _matrix(h, "h", dev, x)
-    if y8 is None and h8 is None and y8_scale is None and h8_scale is None:
-        y8p = y8s = h8p = h8s = None
-        y8n = h8n = kind = 0
-    else:
-        y8p, y8n, y8s, kind = _matrix8(y8, y8_scale, "y8", dev, rows, d)
-        h8p, h8n, h8s, hkind = _matrix8(h8, h8_scale, "h8", dev, rows, d)
-        _block_scaled(hkind, "h8")
-    st = _lib.mp_rmsnorm_forward(
+    y8p, y8n, y8s, kind = _matrix8(y8, y8_scale, "y8", dev, rows, d)
+    h8p, h8n, h8s, hkind = _matrix8(h8, h8_scale, "h8", dev, rows, d)
+    _block_scaled(hkind, "h8")
+    return _lib.mp_rmsnorm_forward(
         yp, hp, _vector(rstd, "rstd", dev, rows, _F32), y8p, y8s, h8p, h8s, xp, rp,
         _vector(weight, "weight", dev, d, _TYPES), rows, d, ys, hs, y8n, h8n, xs, rs, eps, code,
         MP_FP32 if weight is None else _TYPES[weight.dtype], kind, _stream(stream))
-    if st:
-        _check(st, "mp_rmsnorm_forward")
 
 
 def mp_rmsnorm_workspace_bytes(rows: int, d: int) -> int:
@@ -126,6 +147,14 @@ def mp_rmsnorm_backward(dx: Optional[torch.Tensor], dweight: Optional[torch.Tens
     weight's gradient summed over the rows (written, not added to). h: the
     forward pass's h (or x), or h8 with h_scale. dx may be dy, dh or h itself. workspace: uint8 of
     mp_rmsnorm_workspace_bytes(rows, d) bytes, when dweight is given."""
+    st = _binding.rmsnorm_backward(dx, dweight, dy, h, weight, rstd, dh, h_scale, workspace, stream)
+    if st is None:
+        st = _rmsnorm_backward(dx, dweight, dy, h, weight, rstd, dh, h_scale, workspace, stream)
+    if st:
+        _check(st, "mp_rmsnorm_backward")
+
+
+def _rmsnorm_backward(dx, dweight, dy, h, weight, rstd, dh, h_scale, workspace, stream) -> int:
     dev = torch.cuda.current_device()
     dyp, dys, code = _matrix(dy, "dy", dev)
     rows, d = dy.shape
@@ -141,12 +170,10 @@ def mp_rmsnorm_backward(dx: Optional[torch.Tensor], dweight: Optional[torch.Tens
     if workspace is not None:
         wsn = workspace.numel()
         wsp = _vector(workspace, "workspace", dev, wsn, _U8)
-    st = _lib.mp_rmsnorm_backward(
+    return _lib.mp_rmsnorm_backward(
         dxp, _vector(dweight, "dweight", dev, d, _TYPES), dyp, dhp, hp, hsp, _vector(weight, "weight", dev, d, _TYPES),
         _vector(rstd, "rstd", dev, rows, _F32), rows, d, dxs, dys, dhs, hs, code, _weight_type(weight, dweight), wsp,
         wsn, _stream(stream))
-    if st:
-        _check(st, "mp_rmsnorm_backward")
 
 
 class RopeScaling:
@@ -216,6 +243,14 @@ def mp_rope(q_out: torch.Tensor, q: torch.Tensor, k_out: Optional[torch.Tensor],
     None: first_position, first_position + 1, ...). turns and factor are
     mp_rope_frequencies' (rotary_dim = 2 len(turns); a head's further columns are
     copied). inverse: the rotation back, which is the gradient. Outputs may be the inputs themselves."""
+    st = _binding.rope(q_out, q, k_out, k, turns, positions, first_position, interleaved, inverse, factor, stream)
+    if st is None:
+        st = _rope(q_out, q, k_out, k, turns, positions, first_position, interleaved, inverse, factor, stream)
+    if st:
+        _check(st, "mp_rope")
+
+
+def _rope(q_out, q, k_out, k, turns, positions, first_position, interleaved, inverse, factor, stream) -> int:
     dev = torch.cuda.current_device()
     qp, qts, qhs, code = _heads(q, "q", dev)
     qop, qots, qohs, _ = _heads(q_out, "q_out", dev, q)
@@ -236,13 +271,11 @@ def mp_rope(q_out: torch.Tensor, q: torch.Tensor, k_out: Optional[torch.Tensor],
         raise ValueError("k: missing")
     pairs = turns.numel()
     icode = MP_INT64 if positions is None else _index_type(positions, "positions")
-    st = _lib.mp_rope(
+    return _lib.mp_rope(
         qop, qp, kop, kp, _vector(turns, "turns", dev, pairs, (torch.int64,)),
         _vector(positions, "positions", dev, tokens, _INDEX_TYPES), first_position, tokens, q_heads, k_heads, dim,
         2 * pairs, qots, qohs, qts, qhs, kots, kohs, kts, khs, factor, interleaved, inverse, code, icode,
         _stream(stream))
-    if st:
-        _check(st, "mp_rope")
 
 
 def _activation(name: str) -> int:
@@ -259,6 +292,15 @@ def mp_gated_forward(y: torch.Tensor, gate: torch.Tensor, up: Optional[torch.Ten
     """Enqueue y = act(gate) * up (act(gate) without up), and gate and up in 8
     bits (scales of 32 columns) for the backward pass if wanted. y may be gate
     or up itself."""
+    act = _activation(activation)
+    st = _binding.gated_forward(y, gate, up, act, gate8, gate8_scale, up8, up8_scale, stream)
+    if st is None:
+        st = _gated_forward(y, gate, up, act, gate8, gate8_scale, up8, up8_scale, stream)
+    if st:
+        _check(st, "mp_gated_forward")
+
+
+def _gated_forward(y, gate, up, act, gate8, gate8_scale, up8, up8_scale, stream) -> int:
     dev = torch.cuda.current_device()
     gp, gs, code = _matrix(gate, "gate", dev)
     yp, ys, _ = _matrix(y, "y", dev, gate)
@@ -268,10 +310,8 @@ def mp_gated_forward(y: torch.Tensor, gate: torch.Tensor, up: Optional[torch.Ten
     u8p, u8n, u8s, ukind = _matrix8(up8, up8_scale, "up8", dev, rows, d)
     _block_scaled(gkind, "gate8")
     _block_scaled(ukind, "up8")
-    st = _lib.mp_gated_forward(yp, g8p, g8s, u8p, u8s, gp, up_, rows, d, ys, g8n, u8n, gs, us,
-                               _activation(activation), code, _stream(stream))
-    if st:
-        _check(st, "mp_gated_forward")
+    return _lib.mp_gated_forward(yp, g8p, g8s, u8p, u8s, gp, up_, rows, d, ys, g8n, u8n, gs, us, act, code,
+                                 _stream(stream))
 
 
 def mp_gated_backward(dgate: torch.Tensor, dup: Optional[torch.Tensor], dy: torch.Tensor, gate: torch.Tensor,
@@ -282,6 +322,15 @@ def mp_gated_backward(dgate: torch.Tensor, dup: Optional[torch.Tensor], dy: torc
     gate_scale and up_scale) from what the forward pass kept in 8 bits; and, if
     wanted, y = act(gate) * up again. dgate and dup may be dy, gate or up
     themselves."""
+    act = _activation(activation)
+    st = _binding.gated_backward(dgate, dup, dy, gate, up, act, gate_scale, up_scale, y, stream)
+    if st is None:
+        st = _gated_backward(dgate, dup, dy, gate, up, act, gate_scale, up_scale, y, stream)
+    if st:
+        _check(st, "mp_gated_backward")
+
+
+def _gated_backward(dgate, dup, dy, gate, up, act, gate_scale, up_scale, y, stream) -> int:
     dev = torch.cuda.current_device()
     dyp, dys, code = _matrix(dy, "dy", dev)
     dgp, dgs, _ = _matrix(dgate, "dgate", dev, dy)
@@ -301,32 +350,36 @@ def mp_gated_backward(dgate: torch.Tensor, dup: Optional[torch.Tensor], dy: torc
         _block_scaled(ukind, "up")
     dup_, dus, _ = (None, 0, 0) if dup is None else _matrix(dup, "dup", dev, dy)
     yp, ys, _ = (None, 0, 0) if y is None else _matrix(y, "y", dev, dy)
-    st = _lib.mp_gated_backward(dgp, dup_, yp, dyp, gp, gsp, up_, usp, rows, d, dgs, dus, ys, dys, gs, us,
-                                _activation(activation), code, _stream(stream))
-    if st:
-        _check(st, "mp_gated_backward")
+    return _lib.mp_gated_backward(dgp, dup_, yp, dyp, gp, gsp, up_, usp, rows, d, dgs, dus, ys, dys, gs, us, act, code,
+                                  _stream(stream))
 
 
 def mp_pack8(q: torch.Tensor, scale: torch.Tensor, x: torch.Tensor, *, stream=None) -> None:
     """Enqueue q, scale = x in 8 bits (scales of either kind)."""
-    dev = torch.cuda.current_device()
-    xp, xs, code = _matrix(x, "x", dev)
-    rows, d = x.shape
-    qp, qs, sp, kind = _matrix8(q, scale, "q", dev, rows, d)
-    st = _lib.mp_pack8(qp, sp, xp, rows, d, qs, xs, code, kind, _stream(stream))
+    st = _binding.pack8(q, scale, x, stream)
+    if st is None:
+        xp, xs, code, qp, qs, sp, kind = _rows8(x, q, scale)
+        st = _lib.mp_pack8(qp, sp, xp, x.shape[0], x.shape[1], qs, xs, code, kind, _stream(stream))
     if st:
         _check(st, "mp_pack8")
 
 
 def mp_unpack8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, *, stream=None) -> None:
     """Enqueue x = the values that q and scale stand for."""
-    dev = torch.cuda.current_device()
-    xp, xs, code = _matrix(x, "x", dev)
-    rows, d = x.shape
-    qp, qs, sp, kind = _matrix8(q, scale, "q", dev, rows, d)
-    st = _lib.mp_unpack8(xp, qp, sp, rows, d, xs, qs, code, kind, _stream(stream))
+    st = _binding.unpack8(x, q, scale, stream)
+    if st is None:
+        xp, xs, code, qp, qs, sp, kind = _rows8(x, q, scale)
+        st = _lib.mp_unpack8(xp, qp, sp, x.shape[0], x.shape[1], xs, qs, code, kind, _stream(stream))
     if st:
         _check(st, "mp_unpack8")
+
+
+def _rows8(x, q, scale):
+    dev = torch.cuda.current_device()
+    xp, xs, code = _matrix(x, "x", dev)
+    if q is None:
+        raise TypeError("q: expected a torch.Tensor")
+    return (xp, xs, code) + _matrix8(q, scale, "q", dev, *x.shape)
 
 
 __all__ = [

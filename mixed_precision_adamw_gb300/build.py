@@ -1,4 +1,5 @@
-"""Build libmpadamw.so in-tree with nvcc for GB300 (sm_103a).
+"""Build libmpadamw.so in-tree with nvcc for GB300 (sm_103a), and _binding.so, a
+CPython extension, with gcc.
 
 Each .cu translation unit is compiled in parallel, then linked into one
 shared library (CUDA runtime linked statically, so the library needs only the
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmpadamw.so")
+# the ordinary calls of include/mp_block.h from Python without ctypes
+BINDING = os.path.join(PKG, "_binding.so")
 # compute-free stream probes, a separate library that only the benchmark loads
 PROBE_LIB = os.path.join(PKG, "libmpprobe.so")
 
@@ -49,9 +53,10 @@ def _inputs():
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(PROBE_LIB):
+    built = (LIB, PROBE_LIB, BINDING)
+    if not all(os.path.exists(f) for f in built):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(PROBE_LIB))
+    t = min(os.path.getmtime(f) for f in built)
     return any(os.path.getmtime(f) > t for f in _inputs())
 
 
@@ -72,11 +77,28 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + len(PROBE_SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + len(PROBE_SOURCES) + 1) as ex:
+        binding = ex.submit(_binding)
         objs = list(ex.map(lambda s: _compile(s, extra), SOURCES + PROBE_SOURCES))
+        binding.result()
     _link(objs[:len(SOURCES)], LIB)
     _link(objs[len(SOURCES):], PROBE_LIB)
     return LIB
+
+
+def _binding():
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        raise RuntimeError("gcc not found: it is required to build _binding.so")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [cc, "-O2", "-std=c11", "-Wall", "-Wextra", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"],
+           "-I", INCLUDE, os.path.join(CSRC, "mp_binding.c"), "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed on mp_binding.c:\n{r.stdout}\n{r.stderr}")
+    if r.stderr.strip():
+        sys.stderr.write(r.stderr)
+    os.replace(tmp, BINDING)
 
 
 def _link(objs, out):

@@ -245,3 +245,16 @@ def test_frequency_refusals(mp, kw):  # noqa: F811
     with pytest.raises(mp.MpError) as e:
         mp.mp_rope_frequencies(r, base, scaling, device="cpu")
     assert e.value.status == mp.MP_ERR_RANGE
+
+
+def test_the_binding_leaves_the_rest_alone(mp):  # noqa: F811
+    # whatever is not plainly right is passed on, with no error left behind
+    from mixed_precision_adamw_gb300 import _binding as b
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    for args in ((), (1,) * 12, (None,) * 12, (x,) * 12):
+        assert b.rmsnorm_forward(*args) is None
+    for f, n in ((b.rmsnorm_backward, 10), (b.rope, 11), (b.gated_forward, 9), (b.gated_backward, 10), (b.pack8, 4),
+                 (b.unpack8, 4)):
+        for v in (None, 1, 1.0, "x", x, 1 << 80, object()):
+            assert f(*(v,) * n) is None
+        assert f() is None
