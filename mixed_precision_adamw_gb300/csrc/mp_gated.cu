@@ -42,15 +42,15 @@ struct Tiling {
 
 struct Place {
   int64_t r;  // of the thread's first unit; its rows are `down` apart
-  int c, down;
-  int run;  // neighbouring lanes of a row
+  int base, l, down;
 };
 
 __device__ __forceinline__ Place place(const Tiling& g, int rows_a_thread) {
-  const int down = kThreadsG >> g.across, t = static_cast<int>(threadIdx.x);
+  const int down = kThreadsG >> g.across, t = static_cast<int>(threadIdx.x), run = min(1 << g.across, 32);
   const int64_t strip = static_cast<int64_t>(blockIdx.z) * gridDim.y + blockIdx.y;
-  return {strip * (down * rows_a_thread) + (t >> g.across),
-          8 * ((static_cast<int>(blockIdx.x) << g.across) + (t & ((1 << g.across) - 1))), down, min(1 << g.across, 32)};
+  const int l = t & (run - 1), first = (t & ((1 << g.across) - 1)) - l;
+  return {strip * (down * rows_a_thread) + (t >> g.across), 8 * ((static_cast<int>(blockIdx.x) << g.across) + first),
+          l, down};
 }
 
 constexpr float kGelu = 1.5957691216057308f;  // 2 sqrt(2 / pi)
@@ -95,91 +95,96 @@ template <int T, bool Wide, int Act, int R>
 __global__ void __launch_bounds__(kThreadsG) gated_forward_kernel(GatedArgs a, Tiling g) {
   pdl_enter();
   using E = typename Elem<T>::type;
-  const Place at = place(g, R);
-  const int d = static_cast<int>(a.d), c = at.c;
+  const auto [r0, base, l, down] = place(g, R);
+  const int d = static_cast<int>(a.d);
   const int64_t blocks = (d + 31) / 32;
-  const E* gate = static_cast<const E*>(a.gate) + at.r * a.gate_stride;
-  const E* up = a.up ? static_cast<const E*>(a.up) + at.r * a.up_stride : nullptr;
-  Pack8<T> ga[R], ua[R];
+  const E* gate = static_cast<const E*>(a.gate) + r0 * a.gate_stride;
+  const E* up = a.up ? static_cast<const E*>(a.up) + r0 * a.up_stride : nullptr;
+  Raw<T, Wide> ga[R], ua[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const int ci = at.r + i * at.down < a.rows ? c : d;
-    load_unit<T, Wide>(ga[i], gate + i * at.down * a.gate_stride, ci, d);
-    if (up) load_unit<T, Wide>(ua[i], up + i * at.down * a.up_stride, ci, d);
+    const int n = r0 + i * down < a.rows ? d : 0;
+    ga[i].load(gate + i * down * a.gate_stride, base, l, n);
+    if (up) ua[i].load(up + i * down * a.up_stride, base, l, n);
   }
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const int64_t r = at.r + i * at.down;
+    const int64_t r = r0 + i * down;
     const bool live = r < a.rows;
-    F8 f = get8(ga[i]), u;
-    if (a.gate8)
-      put_block8<T, Wide>(f, quad_amax(ga[i]), a.gate8 + r * a.gate8_stride, a.gate8_scale + r * blocks, c, d, live,
-                          at.run);
+    float m[8 / kShare<T, Wide>];
+    Pack8<T> w = ga[i].unit();
+    F8 f = get8(w), u;
+    if (a.gate8) {
+      blocks_amax<T, Wide>(m, w);
+      put_block8<T, T, Wide>(f, m, a.gate8 + r * a.gate8_stride, a.gate8_scale + r * blocks, base, l, d, live);
+    }
     if (up) {
-      u = get8(ua[i]);
-      if (a.up8)
-        put_block8<T, Wide>(u, quad_amax(ua[i]), a.up8 + r * a.up8_stride, a.up8_scale + r * blocks, c, d, live,
-                            at.run);
+      w = ua[i].unit();
+      u = get8(w);
+      if (a.up8) {
+        blocks_amax<T, Wide>(m, w);
+        put_block8<T, T, Wide>(u, m, a.up8 + r * a.up8_stride, a.up8_scale + r * blocks, base, l, d, live);
+      }
     }
     f = mul8(f, sigma8<Act>(f));
     if (up) f = mul8(f, u);
-    put8(ga[i], f);
-    store_unit<T, Wide>(ga[i], static_cast<E*>(a.y) + r * a.y_stride, c, d, live, at.run);
+    put8(w, f);
+    if (live) store_unit<T, Wide>(w, static_cast<E*>(a.y) + r * a.y_stride, base, l, d);
   }
 }
 
 // ---- backward ---------------------------------------------------------------------
 template <int T, bool Wide, bool Kept, int Act, int R>
-__global__ void __launch_bounds__(kThreadsG) gated_backward_kernel(GatedArgs a, Tiling g) {
+__global__ void __launch_bounds__(kThreadsG, Wide && T != MP_FP32 ? 4 : 0) gated_backward_kernel(GatedArgs a, Tiling g) {
   pdl_enter();
   using E = typename Elem<T>::type;
-  const Place at = place(g, R);
-  const int d = static_cast<int>(a.d), c = at.c;
+  const auto [r0, base, l, down] = place(g, R);
+  const int d = static_cast<int>(a.d);
   const int64_t blocks = (d + 31) / 32;
-  Pack8<T> dy[R], ga[Kept ? 1 : R], ua[Kept ? 1 : R];
-  uint2 g8[Kept ? R : 1], u8[Kept ? R : 1];
-  uint32_t gs[Kept ? R : 1], us[Kept ? R : 1];
+  Raw<T, Wide> dy[R], ga[Kept ? 1 : R], ua[Kept ? 1 : R];
+  Raw8<T, Wide> g8[Kept ? R : 1], u8[Kept ? R : 1];
+  RawScales<T, Wide> gs[Kept ? R : 1], us[Kept ? R : 1];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const int64_t r = at.r + i * at.down;
-    const int ci = r < a.rows ? c : d;
-    load_unit<T, Wide>(dy[i], static_cast<const E*>(a.dy) + r * a.dy_stride, ci, d);
+    const int64_t r = r0 + i * down;
+    const int n = r < a.rows ? d : 0;
+    dy[i].load(static_cast<const E*>(a.dy) + r * a.dy_stride, base, l, n);
     if constexpr (Kept) {
-      const bool in = ci < d;
-      g8[i] = load_unit8<Wide>(static_cast<const uint8_t*>(a.gate) + r * a.gate_stride, ci, d);
-      gs[i] = in ? a.gate_scale[r * blocks + c / 32] : 127u;
+      g8[i].load(static_cast<const uint8_t*>(a.gate) + r * a.gate_stride, base, l, n);
+      gs[i].load(a.gate_scale + r * blocks, base, l, n);
       if (a.up) {
-        u8[i] = load_unit8<Wide>(static_cast<const uint8_t*>(a.up) + r * a.up_stride, ci, d);
-        us[i] = in ? a.up_scale[r * blocks + c / 32] : 127u;
+        u8[i].load(static_cast<const uint8_t*>(a.up) + r * a.up_stride, base, l, n);
+        us[i].load(a.up_scale + r * blocks, base, l, n);
       }
     } else {
-      load_unit<T, Wide>(ga[i], static_cast<const E*>(a.gate) + r * a.gate_stride, ci, d);
-      if (a.up) load_unit<T, Wide>(ua[i], static_cast<const E*>(a.up) + r * a.up_stride, ci, d);
+      ga[i].load(static_cast<const E*>(a.gate) + r * a.gate_stride, base, l, n);
+      if (a.up) ua[i].load(static_cast<const E*>(a.up) + r * a.up_stride, base, l, n);
     }
   }
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const int64_t r = at.r + i * at.down;
+    const int64_t r = r0 + i * down;
     const bool live = r < a.rows;
+    if (!Wide && !live) break;
     F8 f, u;
     if constexpr (Kept) {
-      f = mul8(e4m3_unpack(g8[i]), block_scale_value(gs[i]));
-      if (a.up) u = mul8(e4m3_unpack(u8[i]), block_scale_value(us[i]));
+      f = gs[i].values(g8[i].unit(), 1.0f);
+      if (a.up) u = us[i].values(u8[i].unit(), 1.0f);
     } else {
-      f = get8(ga[i]);
-      if (a.up) u = get8(ua[i]);
+      f = get8(ga[i].unit());
+      if (a.up) u = get8(ua[i].unit());
     }
-    const F8 d0 = get8(dy[i]), s = sigma8<Act>(f), act = mul8(f, s);
+    const F8 d0 = get8(dy[i].unit()), s = sigma8<Act>(f), act = mul8(f, s);
     Pack8<T> w;
     put8(w, mul8(a.up ? mul8(d0, u) : d0, slope8<Act>(f, s)));
-    store_unit<T, Wide>(w, static_cast<E*>(a.dgate) + r * a.dgate_stride, c, d, live, at.run);
-    if (a.dup) {
+    if (live) store_unit<T, Wide>(w, static_cast<E*>(a.dgate) + r * a.dgate_stride, base, l, d);
+    if (a.dup && live) {
       put8(w, mul8(d0, act));
-      store_unit<T, Wide>(w, static_cast<E*>(a.dup) + r * a.dup_stride, c, d, live, at.run);
+      store_unit<T, Wide>(w, static_cast<E*>(a.dup) + r * a.dup_stride, base, l, d);
     }
-    if (a.y) {
+    if (a.y && live) {
       put8(w, a.up ? mul8(act, u) : act);
-      store_unit<T, Wide>(w, static_cast<E*>(a.y) + r * a.y_stride, c, d, live, at.run);
+      store_unit<T, Wide>(w, static_cast<E*>(a.y) + r * a.y_stride, base, l, d);
     }
   }
 }
@@ -199,67 +204,137 @@ template <int T, bool Wide, int R>
 __global__ void __launch_bounds__(kThreadsG) pack_blocks_kernel(Rows8Args a, Tiling g) {
   pdl_enter();
   using E = typename Elem<T>::type;
-  const Place at = place(g, R);
-  const int d = static_cast<int>(a.d), c = at.c;
+  const auto [r0, base, l, down] = place(g, R);
+  const int d = static_cast<int>(a.d);
   const int64_t blocks = (d + 31) / 32;
-  const E* from = static_cast<const E*>(a.x_in) + at.r * a.x_stride;
-  uint8_t* to = a.q + at.r * a.q_stride;
-  uint8_t* scales = static_cast<uint8_t*>(a.scale) + at.r * blocks;
-  Pack8<T> x[R];
+  const E* from = static_cast<const E*>(a.x_in) + r0 * a.x_stride;
+  uint8_t* to = a.q + r0 * a.q_stride;
+  uint8_t* scales = static_cast<uint8_t*>(a.scale) + r0 * blocks;
+  Raw<T, Wide> x[R];
 #pragma unroll
-  for (int i = 0; i < R; ++i)
-    load_unit<T, Wide>(x[i], from + i * at.down * a.x_stride, at.r + i * at.down < a.rows ? c : d, d);
+  for (int i = 0; i < R; ++i) x[i].load(from + i * down * a.x_stride, base, l, r0 + i * down < a.rows ? d : 0);
 #pragma unroll
-  for (int i = 0; i < R; ++i)
-    put_block8<T, Wide>(get8(x[i]), quad_amax(x[i]), to + i * at.down * a.q_stride, scales + i * at.down * blocks, c,
-                        d, at.r + i * at.down < a.rows, at.run);
+  for (int i = 0; i < R; ++i) {
+    float m[8 / kShare<T, Wide>];
+    const Pack8<T> u = x[i].unit();
+    blocks_amax<T, Wide>(m, u);
+    put_block8<T, T, Wide>(get8(u), m, to + i * down * a.q_stride, scales + i * down * blocks, base, l, d,
+                           r0 + i * down < a.rows);
+  }
+}
+
+// A scale for each row: G warps a row, NV units a thread in registers from the
+// row's largest magnitude to its 8 bits.
+constexpr int kPackUnits = 4;
+
+template <int T, bool Wide, int NV>
+__global__ void __launch_bounds__(512) pack_rows_kernel(Rows8Args a, int G) {
+  pdl_enter();
+  using E = typename Elem<T>::type;
+  __shared__ float red[16];
+  const int warp = threadIdx.x / 32, l = threadIdx.x % 32, group = warp / G, w = warp - group * G;
+  const int d = static_cast<int>(a.d);
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32 / G) + group;
+  if (r >= a.rows) return;  // the group's warps together
+  const E* x = static_cast<const E*>(a.x_in) + r * a.x_stride;
+  Raw<T, Wide> raw[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) raw[v].load(x, 256 * (w + v * G), l, d);
+  Pack8<T> u[NV];
+  float m = 0.0f;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    u[v] = raw[v].unit();
+    m = amax8(m, get8(u[v]));
+  }
+  m = warp_max(m);
+  if (G > 1) {
+    if (l == 0) red[warp] = m;
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * G) : "memory");
+    for (int i = 0; i < G; ++i) m = max_nan(m, red[group * G + i]);
+  }
+  const float scale = row_scale(m);
+  float inverse;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(inverse) : "f"(scale));
+  if (w == 0 && l == 0) static_cast<float*>(a.scale)[r] = scale;
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+    store_unit8<T, Wide>(e4m3_pack(mul8(get8(u[v]), inverse)), a.q + r * a.q_stride, 256 * (w + v * G), l, d);
+}
+
+// Rows longer than that: read twice.
+template <int T>
+__global__ void __launch_bounds__(512) pack_long_rows_kernel(Rows8Args a) {
+  pdl_enter();
+  using E = Elem<T>;
+  __shared__ float red[16];
+  const int64_t r = blockIdx.x;
+  const typename E::type* x = static_cast<const typename E::type*>(a.x_in) + r * a.x_stride;
+  float m = 0.0f;
+  for (int64_t j = threadIdx.x; j < a.d; j += 512) m = max_nan(m, fabsf(E::get(x[j])));
+  m = warp_max(m);
+  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = m;
+  __syncthreads();
+  for (int i = 0; i < 16; ++i) m = max_nan(m, red[i]);
+  const float scale = row_scale(m);
+  float inverse;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(inverse) : "f"(scale));
+  if (threadIdx.x == 0) static_cast<float*>(a.scale)[r] = scale;
+  for (int64_t j = threadIdx.x; j < a.d; j += 512)
+    a.q[r * a.q_stride + j] = static_cast<uint8_t>(e4m3_pair(__fmul_rn(E::get(x[j]), inverse), 0.0f));
 }
 
 template <int T, bool Wide, int R>
 __global__ void __launch_bounds__(kThreadsG) unpack_kernel(Rows8Args a, Tiling g) {
   pdl_enter();
   using E = typename Elem<T>::type;
-  const Place at = place(g, R);
-  const int d = static_cast<int>(a.d), c = at.c;
+  const auto [r0, base, l, down] = place(g, R);
+  const int d = static_cast<int>(a.d);
   const int64_t blocks = (d + 31) / 32;
   const bool row = a.kind == MP_SCALE_ROW;
-  uint2 q[R];
-  float s[R];
+  const uint8_t* from = a.q_in + r0 * a.q_stride;
+  E* to = static_cast<E*>(a.x) + r0 * a.x_stride;
+  Raw8<T, Wide> q[R];
+  RawScales<T, Wide> s[R];
+  float rs[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const int64_t r = at.r + i * at.down;
-    const int ci = r < a.rows ? c : d;
-    q[i] = load_unit8<Wide>(a.q_in + r * a.q_stride, ci, d);
-    s[i] = ci >= d ? 0.0f
-           : row   ? static_cast<const float*>(a.scale)[r]
-                   : block_scale_value(static_cast<const uint8_t*>(a.scale)[r * blocks + c / 32]);
+    const int64_t r = r0 + i * down;
+    const int n = r < a.rows ? d : 0;
+    q[i].load(from + i * down * a.q_stride, base, l, n);
+    if (!row)
+      s[i].load(static_cast<const uint8_t*>(a.scale) + r * blocks, base, l, n);
+    else
+      rs[i] = n ? static_cast<const float*>(a.scale)[r] : 0.0f;
   }
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const int64_t r = at.r + i * at.down;
     Pack8<T> x;
-    put8(x, mul8(e4m3_unpack(q[i]), s[i]));
-    store_unit<T, Wide>(x, static_cast<E*>(a.x) + r * a.x_stride, c, d, r < a.rows, at.run);
+    put8(x, row ? mul8(e4m3_unpack(q[i].unit()), rs[i]) : s[i].values(q[i].unit(), 1.0f));
+    if (r0 + i * down < a.rows) store_unit<T, Wide>(x, to + i * down * a.x_stride, base, l, d);
   }
 }
 
 // ---- launches -----------------------------------------------------------------------
 
 // Threads of a block along a row of d elements: the fewest lanes left over, more
-// of them along the row where that is equal. Whole quads of lanes (32 columns).
-Tiling tiling(int64_t d) {
+// of them along the row where that is equal; at least 2^least, so that lanes that
+// share a scale are of one run.
+Tiling tiling(int64_t d, int least) {
   const int units = static_cast<int>((d + 31) / 32 * 4);
   Tiling best = {};
-  for (int across = 8; across >= 3; --across) {
+  for (int across = 8; across >= least; --across) {
     const int chunks = (units + (1 << across) - 1) >> across;
     if (across == 8 || (chunks << across) < (best.chunks << best.across)) best = {across, chunks};
   }
   return best;
 }
 
+inline int least_lanes(bool wide) { return wide ? 3 : 5; }
+
 template <int R, typename Args>
-cudaError_t launch_tiled(void (*kernel)(Args, Tiling), const Args& a, cudaStream_t s) {
-  const Tiling g = tiling(a.d);
+cudaError_t launch_tiled(void (*kernel)(Args, Tiling), const Args& a, int least, cudaStream_t s) {
+  const Tiling g = tiling(a.d, least);
   const int64_t per_block = static_cast<int64_t>(kThreadsG >> g.across) * R;
   const int64_t strips = (a.rows + per_block - 1) / per_block, y = std::min<int64_t>(strips, 65535);
   cudaLaunchAttribute attr[1];
@@ -283,7 +358,8 @@ cudaError_t gated_forward(const GatedArgs& a, cudaStream_t s) {
                     (!a.up || wide_rows(a.up, a.d, a.up_stride, a.rows, T)) &&
                     (!a.gate8 || wide_rows8(a.gate8, a.d, a.gate8_stride, a.rows)) &&
                     (!a.up8 || wide_rows8(a.up8, a.d, a.up8_stride, a.rows));
-  return launch_tiled<R>(wide ? gated_forward_kernel<T, true, Act, R> : gated_forward_kernel<T, false, Act, R>, a, s);
+  return launch_tiled<R>(wide ? gated_forward_kernel<T, true, Act, R> : gated_forward_kernel<T, false, Act, R>, a,
+                         least_lanes(wide), s);
 }
 
 template <int T, int Act>
@@ -299,21 +375,40 @@ cudaError_t gated_backward(const GatedArgs& a, cudaStream_t s) {
                     (!a.y || wide_rows(a.y, a.d, a.y_stride, a.rows, T));
   const auto kernel = kept ? (wide ? gated_backward_kernel<T, true, true, Act, R> : gated_backward_kernel<T, false, true, Act, R>)
                            : (wide ? gated_backward_kernel<T, true, false, Act, R> : gated_backward_kernel<T, false, false, Act, R>);
-  return launch_tiled<R>(kernel, a, s);
+  return launch_tiled<R>(kernel, a, least_lanes(wide), s);
 }
 
 template <int T>
 cudaError_t pack_blocks(const Rows8Args& a, cudaStream_t s) {
   constexpr int R = 4;
   const bool wide = wide_rows(a.x_in, a.d, a.x_stride, a.rows, T) && wide_rows8(a.q, a.d, a.q_stride, a.rows);
-  return launch_tiled<R>(wide ? pack_blocks_kernel<T, true, R> : pack_blocks_kernel<T, false, R>, a, s);
+  return launch_tiled<R>(wide ? pack_blocks_kernel<T, true, R> : pack_blocks_kernel<T, false, R>, a,
+                         least_lanes(wide), s);
+}
+
+template <int T, bool Wide>
+cudaError_t pack_rows_wide(const Rows8Args& a, cudaStream_t s) {
+  // four units a thread; one where a row is short
+  const int units = static_cast<int>((a.d + 7) / 8), nv = units <= 32 ? 1 : kPackUnits;
+  const int G = (units + 32 * nv - 1) / (32 * nv), groups = std::max(1, 8 / G);
+  const unsigned blocks = static_cast<unsigned>((a.rows + groups - 1) / groups);
+  return launch_pdl(nv == 1 ? pack_rows_kernel<T, Wide, 1> : pack_rows_kernel<T, Wide, kPackUnits>, blocks,
+                    static_cast<unsigned>(32 * G * groups), s, a, G);
+}
+
+template <int T>
+cudaError_t pack_rows(const Rows8Args& a, cudaStream_t s) {
+  if (a.d > 512 * 8 * kPackUnits)
+    return launch_pdl(pack_long_rows_kernel<T>, static_cast<unsigned>(a.rows), 512, s, a);
+  const bool wide = wide_rows(a.x_in, a.d, a.x_stride, a.rows, T) && wide_rows8(a.q, a.d, a.q_stride, a.rows);
+  return wide ? pack_rows_wide<T, true>(a, s) : pack_rows_wide<T, false>(a, s);
 }
 
 template <int T>
 cudaError_t unpack(const Rows8Args& a, cudaStream_t s) {
   constexpr int R = 4;
   const bool wide = wide_rows(a.x, a.d, a.x_stride, a.rows, T) && wide_rows8(a.q_in, a.d, a.q_stride, a.rows);
-  return launch_tiled<R>(wide ? unpack_kernel<T, true, R> : unpack_kernel<T, false, R>, a, s);
+  return launch_tiled<R>(wide ? unpack_kernel<T, true, R> : unpack_kernel<T, false, R>, a, least_lanes(wide), s);
 }
 
 // Rows whose blocks a grid can count.
@@ -322,9 +417,6 @@ bool tiled_ok(int64_t rows, int64_t d) { return unit_shape_ok(rows, d) && rows <
 bool act_ok(int32_t act) { return act == MP_ACT_SILU || act == MP_ACT_GELU; }
 
 }  // namespace
-
-cudaError_t launch_pack8_rows(uint8_t* q, float* scale, const void* x, int64_t rows, int64_t d, int64_t q_stride,
-                              int64_t x_stride, int32_t type, const DeviceInfo& dev, cudaStream_t s);
 
 }  // namespace mpk
 
@@ -449,25 +541,21 @@ extern "C" int mp_pack8(void* q, void* scale, const void* x, int64_t rows, int64
   const int st = rows8_check(q, scale, x, rows, d, q_stride, x_stride, type, kind);
   if (st != MP_OK || rows == 0) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Rows8Args a = {};
+  a.x_in = x;
+  a.q = static_cast<uint8_t*>(q);
+  a.scale = scale;
+  a.rows = rows;
+  a.d = d;
+  a.x_stride = x_stride;
+  a.q_stride = q_stride;
   cudaError_t e;
-  if (kind == MP_SCALE_ROW) {
-    DeviceInfo dev;
-    e = device_info(&dev);
-    if (e == cudaSuccess)
-      e = launch_pack8_rows(static_cast<uint8_t*>(q), static_cast<float*>(scale), x, rows, d, q_stride, x_stride, type,
-                            dev, s);
-  } else {
-    Rows8Args a = {};
-    a.x_in = x;
-    a.q = static_cast<uint8_t*>(q);
-    a.scale = scale;
-    a.rows = rows;
-    a.d = d;
-    a.x_stride = x_stride;
-    a.q_stride = q_stride;
+  if (kind == MP_SCALE_ROW)
+    e = type == MP_BF16 ? pack_rows<MP_BF16>(a, s)
+                        : type == MP_FP16 ? pack_rows<MP_FP16>(a, s) : pack_rows<MP_FP32>(a, s);
+  else
     e = type == MP_BF16 ? pack_blocks<MP_BF16>(a, s)
                         : type == MP_FP16 ? pack_blocks<MP_FP16>(a, s) : pack_blocks<MP_FP32>(a, s);
-  }
   return e == cudaSuccess ? MP_OK : record_cuda_error(e);
 }
 

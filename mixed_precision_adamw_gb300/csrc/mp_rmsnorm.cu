@@ -1,6 +1,5 @@
 // mp_rmsnorm.cu — RMS norm with the residual's addition, forward and backward,
-// with outputs and kept activations in 8 bits, and rows put away in 8 bits
-// with a scale for each.
+// with outputs and kept activations in 8 bits.
 //
 // A row is read once and stays in registers from the sum of its squares to its
 // outputs. All sums are fp32. Everything is bound by HBM: 8 B an element forward
@@ -40,15 +39,28 @@ struct RmsArgs {
   float eps;
   int weight_type;
   int y8_kind;
-  int plain;  // y8 alone, of x itself (no norm)
 };
 
-// The thread's weights of the unit at column c.
-__device__ __forceinline__ F8 load_weights(const RmsArgs& a, int c) {
+// The weights of a lane's slots.
+template <int T, bool Wide>
+__device__ __forceinline__ F8 load_weights(const RmsArgs& a, int base, int l) {
   float w[8];
+  const auto all = [&](auto load) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    w[e] = c + e < a.d ? (a.weight ? load_as(a.weight, c + e, a.weight_type) : 1.0f) : 0.0f;
+    for (int i = 0; i < 8; ++i) {
+      const int c = slot_column<T, Wide>(base, l, i);
+      w[i] = c < a.d ? load(c) : 0.0f;
+    }
+  };
+  const uint16_t* h = static_cast<const uint16_t*>(a.weight);
+  if (!a.weight)
+    all([](int) { return 1.0f; });
+  else if (a.weight_type == MP_FP32)
+    all([&](int c) { return static_cast<const float*>(a.weight)[c]; });
+  else if (a.weight_type == MP_BF16)
+    all([&](int c) { return Elem<MP_BF16>::get(h[c]); });
+  else
+    all([&](int c) { return Elem<MP_FP16>::get(h[c]); });
   F8 r;
 #pragma unroll
   for (int i = 0; i < 4; ++i) r.p[i] = make_float2(w[2 * i], w[2 * i + 1]);
@@ -56,25 +68,47 @@ __device__ __forceinline__ F8 load_weights(const RmsArgs& a, int c) {
 }
 
 // Weights widened into shared memory once a block: neither their type nor their
-// place (they may sit anywhere in a flat buffer) matters afterwards. A unit's
-// eight lie in two planes of four, so that a warp's lanes read neighbouring
-// 16 bytes.
-__device__ __forceinline__ void stage_weights(float4* sw, const RmsArgs& a, int units, int threads) {
-  for (int u = threadIdx.x; u < units; u += threads) {
-    const F8 w = load_weights(a, 8 * u);
-    sw[u] = make_float4(w.p[0].x, w.p[0].y, w.p[1].x, w.p[1].y);
-    sw[units + u] = make_float4(w.p[2].x, w.p[2].y, w.p[3].x, w.p[3].y);
-  }
+// place (they may sit anywhere in a flat buffer) matters afterwards. `n` columns,
+// a multiple of 256, those past the row 0. For wide rows a unit's eight lie in two
+// planes of four, so that a warp's lanes read neighbouring 16 bytes.
+template <bool Wide>
+__device__ __forceinline__ void stage_weights(float* sw, const RmsArgs& a, int n, int threads) {
+  // several loads on their way at a time, with no question of their type between them
+  const auto all = [&](auto load) {
+#pragma unroll 8
+    for (int j = threadIdx.x; j < n; j += threads) {
+      const int at = Wide ? (j / 4 % 2 * (n / 8) + j / 8) * 4 + j % 4 : j;
+      sw[at] = j < a.d ? load(j) : 0.0f;
+    }
+  };
+  const uint16_t* h = static_cast<const uint16_t*>(a.weight);
+  if (!a.weight)
+    all([](int) { return 1.0f; });
+  else if (a.weight_type == MP_FP32)
+    all([&](int j) { return static_cast<const float*>(a.weight)[j]; });
+  else if (a.weight_type == MP_BF16)
+    all([&](int j) { return Elem<MP_BF16>::get(h[j]); });
+  else
+    all([&](int j) { return Elem<MP_FP16>::get(h[j]); });
 }
 
-__device__ __forceinline__ F8 staged_weights(const float4* sw, int unit, int units) {
-  unit = min(unit, units - 1);
-  const float4 a = sw[unit], b = sw[units + unit];
+template <int T, bool Wide>
+__device__ __forceinline__ F8 staged_weights(const float* sw, int base, int l, int n) {
+  base = min(base, n - 256);
   F8 r;
-  r.p[0] = make_float2(a.x, a.y);
-  r.p[1] = make_float2(a.z, a.w);
-  r.p[2] = make_float2(b.x, b.y);
-  r.p[3] = make_float2(b.z, b.w);
+  if constexpr (Wide) {
+    const float4* p = reinterpret_cast<const float4*>(sw) + base / 8 + l;
+    const float4 a = p[0], b = p[n / 8];
+    r.p[0] = make_float2(a.x, a.y);
+    r.p[1] = make_float2(a.z, a.w);
+    r.p[2] = make_float2(b.x, b.y);
+    r.p[3] = make_float2(b.z, b.w);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      r.p[i] = T == MP_FP32 ? make_float2(sw[base + 64 * i + l], sw[base + 64 * i + 32 + l])
+                            : reinterpret_cast<const float2*>(sw)[base / 2 + 32 * i + l];
+  }
   return r;
 }
 
@@ -86,36 +120,41 @@ __device__ __forceinline__ void fill_nan(Pack8<T>& u) {
     u.fill(T == MP_BF16 ? 0x7FC0 : 0x7E00);
 }
 
-// A unit's outputs. All lanes of a warp call (live, run: as store_unit). `inverse`:
-// of the row's 8-bit scale.
+// A lane's outputs. All lanes of a warp call; where `live` is false nothing is
+// written. `inverse`: of the row's 8-bit scale.
 template <int T, bool Wide>
 __device__ __forceinline__ void put_unit(const RmsArgs& a, const Pack8<T>& u, const F8& w, float rstd, bool row8,
-                                         float inverse, int64_t r, int c, int d, bool live, int run) {
+                                         float inverse, int64_t r, int base, int l, int d, bool live) {
   using E = typename Elem<T>::type;
   const int64_t blocks = (d + 31) / 32;
   const F8 f = get8(u);
-  if (a.h) store_unit<T, Wide>(u, static_cast<E*>(a.h) + r * a.h_stride, c, d, live, run);
-  if (a.h8)
-    put_block8<T, Wide>(f, quad_amax(u), a.h8 + r * a.h8_stride, a.h8_scale + r * blocks, c, d, live, run);
+  float m[8 / kShare<T, Wide>];
+  if (a.h && live) store_unit<T, Wide>(u, static_cast<E*>(a.h) + r * a.h_stride, base, l, d);
+  if (a.h8) {
+    blocks_amax<T, Wide>(m, u);
+    put_block8<T, T, Wide>(f, m, a.h8 + r * a.h8_stride, a.h8_scale + r * blocks, base, l, d, live);
+  }
   if (!a.y && !a.y8) return;
   const F8 y = mul8(mul8(f, rstd), w);
-  if (a.y) {
+  if (a.y && live) {
     Pack8<T> o;
     put8(o, y);
-    store_unit<T, Wide>(o, static_cast<E*>(a.y) + r * a.y_stride, c, d, live, run);
+    store_unit<T, Wide>(o, static_cast<E*>(a.y) + r * a.y_stride, base, l, d);
   }
-  if (row8)
-    store_unit8<Wide>(e4m3_pack(mul8(y, inverse)), a.y8 + r * a.y8_stride, c, d, live, run);
-  else if (a.y8)
-    put_block8<MP_FP32, Wide>(y, quad_amax(y), a.y8 + r * a.y8_stride, static_cast<uint8_t*>(a.y8_scale) + r * blocks,
-                              c, d, live, run);
+  if (row8) {
+    if (live) store_unit8<T, Wide>(e4m3_pack(mul8(y, inverse)), a.y8 + r * a.y8_stride, base, l, d);
+  } else if (a.y8) {
+    blocks_amax<T, Wide>(m, y);
+    put_block8<T, MP_FP32, Wide>(y, m, a.y8 + r * a.y8_stride, static_cast<uint8_t*>(a.y8_scale) + r * blocks, base, l,
+                                 d, live);
+  }
 }
 
 // From a row's sums (to each of its threads): rstd and the inverse of its 8-bit
 // scale; the first thread writes what there is one of.
 __device__ __forceinline__ float row_results(const RmsArgs& a, float s, float m, float inv_d, bool row8, int64_t r,
                                              bool writes, float& inverse) {
-  const float rstd = a.plain ? 1.0f : rsqrtf(__fmaf_rn(s, inv_d, a.eps));
+  const float rstd = rsqrtf(__fmaf_rn(s, inv_d, a.eps));
   inverse = 0.0f;
   if (row8) {
     const float scale = row_scale(__fmul_rn(m, rstd));
@@ -132,16 +171,16 @@ template <int T, bool Wide, int L>
 __global__ void __launch_bounds__(256) rms_forward_short_kernel(RmsArgs a) {
   pdl_enter();
   using E = typename Elem<T>::type;
-  const int t = threadIdx.x % L, c = 8 * t, d = static_cast<int>(a.d);
+  const int t = threadIdx.x % L, d = static_cast<int>(a.d);
   const int64_t groups = 256 / L, step = gridDim.x * groups;
   const float inv_d = __fdiv_rn(1.0f, static_cast<float>(d));
   const bool row8 = a.y8 && a.y8_kind == MP_SCALE_ROW;
-  const F8 w = load_weights(a, c);
-  Pack8<T> xn, rn;
+  const F8 w = load_weights<T, Wide>(a, 0, t);
+  Raw<T, Wide> xn, rn;
   auto fetch = [&](int64_t r) {
-    const int at = r < a.rows ? c : d;
-    load_unit<T, Wide>(xn, static_cast<const E*>(a.x) + r * a.x_stride, at, d);
-    if (a.residual) load_unit<T, Wide>(rn, static_cast<const E*>(a.residual) + r * a.residual_stride, at, d);
+    const int n = r < a.rows ? d : 0;
+    xn.load(static_cast<const E*>(a.x) + r * a.x_stride, 0, t, n);
+    if (a.residual) rn.load(static_cast<const E*>(a.residual) + r * a.residual_stride, 0, t, n);
   };
   int64_t r = blockIdx.x * groups + threadIdx.x / L;
   const int64_t ahead = threadIdx.x % 32 / L;
@@ -150,8 +189,8 @@ __global__ void __launch_bounds__(256) rms_forward_short_kernel(RmsArgs a) {
 #pragma unroll 1
   for (; r - ahead < a.rows; r += step) {
     const bool live = r < a.rows;
-    Pack8<T> u = xn;
-    if (a.residual) put8(u, add8(get8(u), get8(rn)));
+    Pack8<T> u = xn.unit();
+    if (a.residual) put8(u, add8(get8(u), get8(rn.unit())));
     fetch(r + step);
     const F8 f = get8(u);
     float2 s2 = make_float2(0.0f, 0.0f);
@@ -165,7 +204,7 @@ __global__ void __launch_bounds__(256) rms_forward_short_kernel(RmsArgs a) {
       for (int o = L / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(kAll, m, o));
     float inverse;
     const float rstd = row_results(a, s, m, inv_d, row8, r, t == 0 && live, inverse);
-    put_unit<T, Wide>(a, u, w, rstd, row8, inverse, r, c, d, live, L);
+    put_unit<T, Wide>(a, u, w, rstd, row8, inverse, r, 0, t, d, live);
   }
 }
 
@@ -182,11 +221,11 @@ rms_forward_kernel(RmsArgs a, int G, uint32_t pitch, int stages) {
   __shared__ float2 red[2][kMaxThreads / 32];
   __shared__ unsigned long long full[kMaxThreads / 32 * kMaxStages];
   const int L = 32 * G, t = threadIdx.x % L, group = threadIdx.x / L, groups = blockDim.x / L;
-  const int d = static_cast<int>(a.d), units = (d + 7) / 8;
+  const int lane = t % 32, first_column = 8 * (t - lane), d = static_cast<int>(a.d), padded = (d + 255) / 256 * 256;
   const bool has_res = a.residual;
   const uint32_t stage_bytes = has_res ? 2 * pitch : pitch;
-  float4* sw = reinterpret_cast<float4*>(smem);
-  uint8_t* ring = smem + 32 * units + static_cast<size_t>(group) * stages * stage_bytes;
+  float* sw = reinterpret_cast<float*>(smem);
+  uint8_t* ring = smem + 4 * padded + static_cast<size_t>(group) * stages * stage_bytes;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + group;
   if (threadIdx.x < groups * stages) {
@@ -212,7 +251,7 @@ rms_forward_kernel(RmsArgs a, int G, uint32_t pitch, int stages) {
   };
   if (t == 0)
     for (int i = 0; i < stages; ++i) fetch(first + i * step, i);
-  stage_weights(sw, a, units, blockDim.x);
+  stage_weights<Wide>(sw, a, padded, blockDim.x);
   __syncthreads();
   const float inv_d = __fdiv_rn(1.0f, static_cast<float>(d));
   const bool row8 = a.y8 && a.y8_kind == MP_SCALE_ROW;
@@ -237,18 +276,17 @@ rms_forward_kernel(RmsArgs a, int G, uint32_t pitch, int stages) {
     float m = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int c = 8 * (t + v * L);
-      load_unit<T, Wide>(u[v], xs, c, d);
-      if (has_res) {
-        Pack8<T> q;
-        load_unit<T, Wide>(q, rs, c, d);
-        put8(u[v], add8(get8(u[v]), get8(q)));
-      }
+      const int base = first_column + 8 * v * L;
+      Raw<T, Wide> p, q;
+      p.load(xs, base, lane, d);
+      if (has_res) q.load(rs, base, lane, d);
+      u[v] = p.unit();
+      if (has_res) put8(u[v], add8(get8(u[v]), get8(q.unit())));
       if (!ok) fill_nan(u[v]);
       const F8 f = get8(u[v]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) s2 = fma2(f.p[i], f.p[i], s2);
-      if (row8) m = amax8(m, mul8(f, staged_weights(sw, t + v * L, units)));
+      if (row8) m = amax8(m, mul8(f, staged_weights<T, Wide>(sw, base, lane, padded)));
     }
     float s = warp_sum(__fadd_rn(s2.x, s2.y));
     if (row8) m = warp_max(m);
@@ -268,9 +306,11 @@ rms_forward_kernel(RmsArgs a, int G, uint32_t pitch, int stages) {
     float inverse;
     const float rstd = row_results(a, s, m, inv_d, row8, r, t == 0, inverse);
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
-      put_unit<T, Wide>(a, u[v], staged_weights(sw, t + v * L, units), rstd, row8, inverse, r, 8 * (t + v * L), d, true,
-                        32);
+    for (int v = 0; v < NV; ++v) {
+      const int base = first_column + 8 * v * L;
+      put_unit<T, Wide>(a, u[v], staged_weights<T, Wide>(sw, base, lane, padded), rstd, row8, inverse, r, base, lane, d,
+                        true);
+    }
     if (++stage == stages) {
       stage = 0;
       phase ^= 1;
@@ -308,13 +348,12 @@ __device__ __forceinline__ float long_max(float v, float* red) {
   return s;
 }
 
-template <int T>
+template <int V>
 __device__ __forceinline__ void long_block8(float f, uint8_t* row, uint8_t* scales, int64_t j, int64_t d) {
   const uint32_t byte = block_scale(warp_max(fabsf(f)));
   if (j >= d) return;
-  F8 g = zero8();
-  g.p[0].x = f;
-  row[j] = static_cast<uint8_t>(block_pack<T>(g, byte).x);
+  const float g = __fmul_rn(f, block_inverse(byte));
+  row[j] = static_cast<uint8_t>(e4m3_pair(block_top<V>(byte) ? below_256(g) : g, 0.0f));
   if (j % 32 == 0) scales[j / 32] = static_cast<uint8_t>(byte);
 }
 
@@ -342,8 +381,7 @@ __global__ void __launch_bounds__(kLongThreads) rms_forward_long_kernel(RmsArgs 
       s = __fmaf_rn(f, f, s);
       if (row8) m = max_nan(m, fabsf(__fmul_rn(f, weight(j))));
     }
-    const float rstd =
-        a.plain ? 1.0f : rsqrtf(__fmaf_rn(long_sum(s, red), __fdiv_rn(1.0f, static_cast<float>(a.d)), a.eps));
+    const float rstd = rsqrtf(__fmaf_rn(long_sum(s, red), __fdiv_rn(1.0f, static_cast<float>(a.d)), a.eps));
     float inverse = 0.0f;
     if (row8) {
       const float scale = row_scale(__fmul_rn(long_max(m, red), rstd));
@@ -372,15 +410,6 @@ __global__ void __launch_bounds__(kLongThreads) rms_forward_long_kernel(RmsArgs 
 // registers; a block writes its sums once, part[block][d], and a second, small
 // launch adds the blocks' sums in block order.
 
-// xh of a unit of h, as stored or in 8 bits.
-template <int T>
-__device__ __forceinline__ F8 normalised(const Pack8<T>& u, float rstd) {
-  return mul8(get8(u), rstd);
-}
-__device__ __forceinline__ F8 normalised(uint2 q, uint32_t scale, float rstd) {
-  return mul8(e4m3_unpack(q), __fmul_rn(block_scale_value(scale), rstd));
-}
-
 // Short rows, L lanes each.
 template <int T, bool Wide, bool H8, int L>
 __global__ void __launch_bounds__(256) rms_backward_short_kernel(RmsArgs a, float* part) {
@@ -388,27 +417,27 @@ __global__ void __launch_bounds__(256) rms_backward_short_kernel(RmsArgs a, floa
   using E = typename Elem<T>::type;
   constexpr int kGroups = 256 / L;
   __shared__ float joined[256 * 8];  // the groups' sums
-  const int t = threadIdx.x % L, group = threadIdx.x / L, c = 8 * t, d = static_cast<int>(a.d);
+  const int t = threadIdx.x % L, group = threadIdx.x / L, d = static_cast<int>(a.d);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups, blocks = (d + 31) / 32;
   const float inv_d = __fdiv_rn(1.0f, static_cast<float>(d));
-  const F8 w = load_weights(a, c);
+  const F8 w = load_weights<T, Wide>(a, 0, t);
   F8 dw = zero8();
-  Pack8<T> yn, gn, hn;
-  uint2 qn = make_uint2(0u, 0u);
-  uint32_t bn = 127u;
+  Raw<T, Wide> yn, gn, hn;
+  Raw8<T, Wide> qn;
+  RawScales<T, Wide> bn;
   float rstd_n = 0.0f;
   auto fetch = [&](int64_t r) {
     const bool live = r < a.rows;
-    const int at = live ? c : d;
+    const int n = live ? d : 0;
     rstd_n = live ? a.rstd_in[r] : 0.0f;
-    load_unit<T, Wide>(yn, static_cast<const E*>(a.dy) + r * a.dy_stride, at, d);
+    yn.load(static_cast<const E*>(a.dy) + r * a.dy_stride, 0, t, n);
     if constexpr (H8) {
-      qn = load_unit8<Wide>(static_cast<const uint8_t*>(a.x) + r * a.x_stride, at, d);
-      bn = at < d ? a.x_scale[r * blocks + at / 32] : 127u;
+      qn.load(static_cast<const uint8_t*>(a.x) + r * a.x_stride, 0, t, n);
+      bn.load(a.x_scale + r * blocks, 0, t, n);
     } else {
-      load_unit<T, Wide>(hn, static_cast<const E*>(a.x) + r * a.x_stride, at, d);
+      hn.load(static_cast<const E*>(a.x) + r * a.x_stride, 0, t, n);
     }
-    if (a.residual) load_unit<T, Wide>(gn, static_cast<const E*>(a.residual) + r * a.residual_stride, at, d);
+    if (a.residual) gn.load(static_cast<const E*>(a.residual) + r * a.residual_stride, 0, t, n);
   };
   int64_t r = static_cast<int64_t>(blockIdx.x) * kGroups + group;
   const int64_t ahead = threadIdx.x % 32 / L;
@@ -419,12 +448,12 @@ __global__ void __launch_bounds__(256) rms_backward_short_kernel(RmsArgs a, floa
     const float rstd = rstd_n;
     F8 xh;
     if constexpr (H8)
-      xh = normalised(qn, bn, rstd);
+      xh = bn.values(qn.unit(), rstd);
     else
-      xh = normalised(hn, rstd);
-    const F8 f = get8(yn), g = mul8(f, w);
+      xh = mul8(get8(hn.unit()), rstd);
+    const F8 f = get8(yn.unit()), g = mul8(f, w);
     F8 o = zero8();
-    if (a.residual) o = get8(gn);
+    if (a.residual) o = get8(gn.unit());
     fetch(r + step);
     float2 s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -435,19 +464,19 @@ __global__ void __launch_bounds__(256) rms_backward_short_kernel(RmsArgs a, floa
     float s = __fadd_rn(s2.x, s2.y);
 #pragma unroll
     for (int q = L / 2; q > 0; q >>= 1) s = __fadd_rn(s, __shfl_xor_sync(kAll, s, q));
-    if (!a.y) continue;
+    if (!a.y || !live) continue;
     const float k = -__fmul_rn(__fmul_rn(s, inv_d), rstd);
 #pragma unroll
     for (int i = 0; i < 4; ++i) o.p[i] = fma2(g.p[i], both(rstd), fma2(xh.p[i], both(k), o.p[i]));
     Pack8<T> u;
     put8(u, o);
-    store_unit<T, Wide>(u, static_cast<E*>(a.y) + r * a.y_stride, c, d, live, L);
+    store_unit<T, Wide>(u, static_cast<E*>(a.y) + r * a.y_stride, 0, t, d);
   }
   if (!part) return;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    joined[group * 8 * L + c + 2 * i] = dw.p[i].x;
-    joined[group * 8 * L + c + 2 * i + 1] = dw.p[i].y;
+    joined[group * 8 * L + slot_column<T, Wide>(0, t, 2 * i)] = dw.p[i].x;
+    joined[group * 8 * L + slot_column<T, Wide>(0, t, 2 * i + 1)] = dw.p[i].y;
   }
   __syncthreads();
   for (int j = threadIdx.x; j < d; j += 256) {
@@ -476,7 +505,7 @@ rms_backward_kernel(RmsArgs a, float* part, int G, StageMap map, int stages) {
   __shared__ float red[2][kMaxThreads / 32];
   __shared__ unsigned long long full[kMaxThreads / 32 * kMaxStages];
   const int L = 32 * G, t = threadIdx.x % L, group = threadIdx.x / L, groups = blockDim.x / L;
-  const int d = static_cast<int>(a.d);
+  const int lane = t % 32, first_column = 8 * (t - lane), d = static_cast<int>(a.d);
   const uint32_t blocks = (d + 31) / 32;
   const bool has_dh = a.residual;
   uint8_t* ring = smem + static_cast<size_t>(group) * stages * map.size;
@@ -523,7 +552,7 @@ rms_backward_kernel(RmsArgs a, float* part, int G, StageMap map, int stages) {
   F8 w[NV], dw[NV];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    w[v] = load_weights(a, 8 * (t + v * L));
+    w[v] = load_weights<T, Wide>(a, first_column + 8 * v * L, lane);
     dw[v] = zero8();
   }
   float rstd_next = first < end ? a.rstd_in[first] : 0.0f;
@@ -552,18 +581,25 @@ rms_backward_kernel(RmsArgs a, float* part, int G, StageMap map, int stages) {
     float2 s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int c = 8 * (t + v * L);
-      Pack8<T> u;
+      const int base = first_column + 8 * v * L;
+      Raw<T, Wide> y, h, g;
+      Raw8<T, Wide> q;
+      RawScales<T, Wide> b;
+      y.load(ys, base, lane, d);
       if constexpr (H8) {
-        xh[v] = normalised(load_unit8<Wide>(hs, c, d), c < d ? ss[static_cast<uint32_t>(c) / 32] : 127u, rstd);
+        q.load(hs, base, lane, d);
+        b.load(ss, base, lane, d);
       } else {
-        load_unit<T, Wide>(u, reinterpret_cast<const E*>(hs), c, d);
-        xh[v] = normalised(u, rstd);
+        h.load(reinterpret_cast<const E*>(hs), base, lane, d);
       }
-      load_unit<T, Wide>(u, ys, c, d);
-      f[v] = get8(u);
+      if (has_dh) g.load(gs, base, lane, d);
+      f[v] = get8(y.unit());
+      if constexpr (H8)
+        xh[v] = b.values(q.unit(), rstd);
+      else
+        xh[v] = mul8(get8(h.unit()), rstd);
       if (has_dh)
-        load_unit<T, Wide>(e[v], gs, c, d);
+        e[v] = g.unit();
       else
         e[v].zero();
 #pragma unroll
@@ -593,7 +629,7 @@ rms_backward_kernel(RmsArgs a, float* part, int G, StageMap map, int stages) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) o.p[q] = fma2(f[v].p[q], both(rstd), fma2(xh[v].p[q], both(k), o.p[q]));
         put8(e[v], o);
-        store_unit<T, Wide>(e[v], out, 8 * (t + v * L), d, true, 32);
+        store_unit<T, Wide>(e[v], out, first_column + 8 * v * L, lane, d);
       }
     }
     if (++stage == stages) {
@@ -615,11 +651,13 @@ rms_backward_kernel(RmsArgs a, float* part, int G, StageMap map, int stages) {
   float* joined = reinterpret_cast<float*>(smem);
   const int width = 8 * NV * L;
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    float4* to = reinterpret_cast<float4*>(joined + group * width + 8 * (t + v * L));
-    to[0] = make_float4(dw[v].p[0].x, dw[v].p[0].y, dw[v].p[1].x, dw[v].p[1].y);
-    to[1] = make_float4(dw[v].p[2].x, dw[v].p[2].y, dw[v].p[3].x, dw[v].p[3].y);
-  }
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float* to = joined + group * width;
+      to[slot_column<T, Wide>(first_column + 8 * v * L, lane, 2 * i)] = dw[v].p[i].x;
+      to[slot_column<T, Wide>(first_column + 8 * v * L, lane, 2 * i + 1)] = dw[v].p[i].y;
+    }
   __syncthreads();
   float* to = part + static_cast<int64_t>(blockIdx.x) * d;
   for (int j = threadIdx.x; j < d; j += blockDim.x) {
@@ -685,21 +723,28 @@ __global__ void __launch_bounds__(kLongThreads) rms_dw_long_kernel(RmsArgs a, fl
   part[c * a.d + j] = s;
 }
 
-// dweight from `parts` blocks' sums: 32 columns a block, 32 threads a column,
-// each adding every 32nd block's sum.
-constexpr int kFinishSlices = 32;
+// dweight from `parts` blocks' sums: 32 columns a block, 16 threads a column, each
+// adding every 16th block's sum, ten of them on their way at a time.
+constexpr int kFinishSlices = 16, kFinishAhead = 10;
 
 __global__ void __launch_bounds__(32 * kFinishSlices) rms_finish_kernel(void* dweight, const float* part, int64_t d,
                                                                         int parts, int weight_type) {
   pdl_enter();
-  __shared__ float red[kFinishSlices][33];
+  __shared__ float red[kFinishSlices][32];
   const int c = threadIdx.x % 32, slice = threadIdx.x / 32;
   const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + c;
   float s = 0.0f;
-  if (j < d) {
-#pragma unroll 8
-    for (int p = slice; p < parts; p += kFinishSlices) s = __fadd_rn(s, part[static_cast<int64_t>(p) * d + j]);
-  }
+  if (j < d)
+    for (int p = slice; p < parts; p += kFinishAhead * kFinishSlices) {
+      float v[kFinishAhead];
+#pragma unroll
+      for (int i = 0; i < kFinishAhead; ++i) {
+        const int q = p + i * kFinishSlices;
+        v[i] = q < parts ? part[static_cast<int64_t>(q) * d + j] : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < kFinishAhead; ++i) s = __fadd_rn(s, v[i]);
+    }
   red[slice][c] = s;
   __syncthreads();
   if (slice || j >= d) return;
@@ -723,7 +768,7 @@ cudaError_t forward_staged(const RmsArgs& a, int G, const DeviceInfo& dev, cudaS
   const cudaError_t e = allow_shared(rms_forward_kernel<T, Wide, NV>, kSmShared - 4096, ready);
   if (e != cudaSuccess) return e;
   const uint32_t pitch = pieces_pitch(a.d * (T == MP_FP32 ? 4 : 2)), row = (a.residual ? 2 : 1) * pitch;
-  const uint32_t weights = static_cast<uint32_t>((a.d + 7) / 8 * 32), room = kSmShared - 4096 - weights;
+  const uint32_t weights = static_cast<uint32_t>((a.d + 255) / 256 * 1024), room = kSmShared - 4096 - weights;
   // one block an SM: as many groups as have two stages each
   const int groups = static_cast<int>(std::max<uint32_t>(1, std::min<uint32_t>(kMaxThreads / (32 * G), room / (2 * row))));
   const int stages = static_cast<int>(std::max<uint32_t>(2, std::min<uint32_t>(kMaxStages, room / (groups * row))));
@@ -735,15 +780,21 @@ cudaError_t forward_staged(const RmsArgs& a, int G, const DeviceInfo& dev, cudaS
 
 template <int T, bool Wide>
 cudaError_t forward_wide(const RmsArgs& a, const DeviceInfo& dev, cudaStream_t s) {
-  if (a.d <= 64) return forward_short<T, Wide, 8>(a, dev, s);
-  if (a.d <= 128) return forward_short<T, Wide, 16>(a, dev, s);
+  if constexpr (Wide) {  // other rows take whole warps
+    if (a.d <= 64) return forward_short<T, Wide, 8>(a, dev, s);
+    if (a.d <= 128) return forward_short<T, Wide, 16>(a, dev, s);
+  }
   if (a.d <= kShortD) return forward_short<T, Wide, 32>(a, dev, s);
-  // Four units a thread, so that what a row costs each of its threads is shared by
-  // many elements; fewer where there are too few rows to fill the GPU with as many warps.
   const int units = static_cast<int>((a.d + 7) / 8);
-  const auto warps = [&](int nv) { return (units + 32 * nv - 1) / (32 * nv); };
+  const auto warps = [&](int nv) { return (units + 32 * nv - 1) / (32 * nv); };      // of a row
+  const auto busy = [&](int nv) { return kMaxThreads / 32 / warps(nv) * warps(nv); };  // of a block
+  // Few rows: one or two units a thread, so that more warps share them.
   if (warps(1) <= kMaxThreads / 32 && a.rows * warps(2) < 8 * dev.sms) return forward_staged<T, Wide, 1>(a, warps(1), dev, s);
   if (a.rows * warps(4) < 8 * dev.sms || units <= 64) return forward_staged<T, Wide, 2>(a, warps(2), dev, s);
+  // Many: four, so that what a row costs each of its threads is shared by many elements. Rows
+  // off the grid: two, as four take more code than the instruction caches hold, unless
+  // they leave a block with few warps.
+  if (!Wide && busy(2) >= 12) return forward_staged<T, Wide, 2>(a, warps(2), dev, s);
   return forward_staged<T, Wide, 4>(a, warps(4), dev, s);
 }
 
@@ -772,7 +823,10 @@ struct BackwardPlan {
   int parts, G, groups;  // blocks; warps of a row; rows that a block has in hand
 };
 
-constexpr int kBackwardUnits = 2;  // a thread's
+// A thread's. Two fill the registers: with three (held packed until dx) and so fuller
+// blocks for rows of 2500 to 6000, 16471 x 2592 bf16 from 8 bits took 66 us instead of
+// 69, but 8192 x 4097 78 instead of 58.
+constexpr int kBackwardUnits = 2;
 
 BackwardPlan backward_plan(int64_t rows, int64_t d) {
   BackwardPlan p = {0, 1, 1};
@@ -781,8 +835,8 @@ BackwardPlan backward_plan(int64_t rows, int64_t d) {
     cap = 4 * kSms;
     per_block = 2 * 256 / (d <= 64 ? 8 : d <= 128 ? 16 : 32);
   } else if (d <= kStagedD) {
-    p.G = static_cast<int>((d + 255 * kBackwardUnits) / (256 * kBackwardUnits));
-    p.groups = std::max(1, kMaxThreads / 32 / p.G);
+    p.G = static_cast<int>((d + 256 * kBackwardUnits - 1) / (256 * kBackwardUnits));
+    p.groups = kMaxThreads / 32 / p.G;
     cap = kSms;
     per_block = p.groups;
   }
@@ -795,12 +849,8 @@ cudaError_t backward_short(const RmsArgs& a, const BackwardPlan& p, float* part,
   return launch_pdl(rms_backward_short_kernel<T, Wide, H8, L>, static_cast<unsigned>(p.parts), 256, s, a, part);
 }
 
-template <int T, bool Wide, bool H8>
-cudaError_t backward_wide(const RmsArgs& a, const BackwardPlan& p, float* part, cudaStream_t s) {
-  if (a.d <= 64) return backward_short<T, Wide, H8, 8>(a, p, part, s);
-  if (a.d <= 128) return backward_short<T, Wide, H8, 16>(a, p, part, s);
-  if (a.d <= kShortD) return backward_short<T, Wide, H8, 32>(a, p, part, s);
-  constexpr int NV = kBackwardUnits;
+template <int T, bool Wide, bool H8, int NV>
+cudaError_t backward_staged(const RmsArgs& a, const BackwardPlan& p, float* part, cudaStream_t s) {
   static std::atomic<bool> ready[64];
   const auto kernel = rms_backward_kernel<T, Wide, H8, NV>;
   const cudaError_t e = allow_shared(kernel, kSmShared - 4096, ready);
@@ -814,6 +864,16 @@ cudaError_t backward_wide(const RmsArgs& a, const BackwardPlan& p, float* part, 
   const uint32_t threads = 32 * p.G * p.groups;
   const size_t smem = std::max<size_t>(static_cast<size_t>(stages) * per_stage, threads * 8 * NV * sizeof(float));
   return launch_pdl_smem(kernel, static_cast<unsigned>(p.parts), threads, smem, s, a, part, p.G, map, stages);
+}
+
+template <int T, bool Wide, bool H8>
+cudaError_t backward_wide(const RmsArgs& a, const BackwardPlan& p, float* part, cudaStream_t s) {
+  if constexpr (Wide) {
+    if (a.d <= 64) return backward_short<T, Wide, H8, 8>(a, p, part, s);
+    if (a.d <= 128) return backward_short<T, Wide, H8, 16>(a, p, part, s);
+  }
+  if (a.d <= kShortD) return backward_short<T, Wide, H8, 32>(a, p, part, s);
+  return backward_staged<T, Wide, H8, kBackwardUnits>(a, p, part, s);
 }
 
 template <int T, bool H8>
@@ -847,21 +907,6 @@ cudaError_t backward_h(const RmsArgs& a, void* dweight, float* part, const Devic
 }
 
 }  // namespace
-
-cudaError_t launch_pack8_rows(uint8_t* q, float* scale, const void* x, int64_t rows, int64_t d, int64_t q_stride,
-                              int64_t x_stride, int32_t type, const DeviceInfo& dev, cudaStream_t s) {
-  RmsArgs a = {};
-  a.y8 = q;
-  a.y8_scale = scale;
-  a.y8_kind = MP_SCALE_ROW;
-  a.x = x;
-  a.rows = rows;
-  a.d = d;
-  a.y8_stride = q_stride;
-  a.x_stride = x_stride;
-  a.plain = 1;
-  return forward_of(type, a, dev, s);
-}
 
 }  // namespace mpk
 

@@ -1,12 +1,19 @@
-// mp_units.cuh — eight-column units of rows at any alignment, and rows in 8
+// mp_units.cuh — eight columns a lane of rows at any alignment, and rows in 8
 // bits (e4m3 values with scales), for the operators of a block between its
 // matrix products.
 //
-// A thread's unit is eight neighbouring columns that start at a multiple of
-// eight, so the 32 columns that share a power-of-two scale are four
-// neighbouring lanes'. Rows on the 16-byte grid (Wide) are read and written in
-// 16-byte pieces. Of other rows a unit is cut out of the pieces that it lies
-// in: each is read once more by a neighbouring lane, out of L1.
+// A run of `run` neighbouring lanes (a warp; of wide rows also half or a quarter of
+// one) takes 8 * run neighbouring columns of a row from `base` on; lane l of the
+// run has eight of them, in slots 0 to 7:
+//  Wide rows (on the 16-byte grid): columns base + 8 l to base + 8 l + 7, one
+//    16-byte access (two for fp32). Four lanes share a scale of 32 columns.
+//  Other rows, 16-bit: pairs of columns, pair i at base + 64 i + 2 l, so that a
+//    warp's lanes touch neighbouring 4-byte words whatever the row's place; only
+//    on an odd one is a pair two accesses. 16 lanes share a scale.
+//  Other rows, fp32: slot i is column base + 32 i + l. A warp shares a scale.
+// (Cutting eight neighbours out of the two or three 16-byte pieces that they lie in,
+// and handing pieces to the neighbour for the stores, takes more instructions than
+// these narrow accesses: gated forward of 32768 x 2731, fp32 229 us so and 151 this way.)
 #pragma once
 
 #include "mp_block.h"
@@ -125,175 +132,228 @@ __device__ __forceinline__ float amax8(float m, const F8& a) {
 
 // ---- units ----------------------------------------------------------------------
 
-// Columns c to c + 7 of a row of n, zeros from n on.
+// The column of slot i.
+template <int T, bool Wide>
+__device__ __forceinline__ int slot_column(int base, int l, int i) {
+  if (Wide) return base + 8 * l + i;
+  return T == MP_FP32 ? base + 32 * i + l : base + 64 * (i / 2) + 2 * l + i % 2;
+}
+
+// A lane's columns of a row of n as they come in, zeros from n on; unit() puts them
+// together, so that a wait for the loads comes there and not between them.
+template <int T, bool Wide>
+struct Raw {  // 16-bit, not wide
+  uint32_t a[4], b[4];  // a pair, or its first and second column
+
+  __device__ __forceinline__ void load(const uint16_t* row, int base, int l, int n) {
+    const uint16_t* p = row + base + 2 * l;
+    const bool even = reinterpret_cast<uintptr_t>(row) % 4 == 0;
+    if (base + 256 <= n) {
+      if (even) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[i] = *reinterpret_cast<const uint32_t*>(p + 64 * i);
+          b[i] = 0u;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[i] = p[64 * i];
+          b[i] = p[64 * i + 1];
+        }
+      }
+    } else {
+      const int left = n - base - 2 * l;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i] = 64 * i < left ? p[64 * i] : 0u;
+        b[i] = 64 * i + 1 < left ? p[64 * i + 1] : 0u;
+      }
+    }
+  }
+  __device__ __forceinline__ Pack8<T> unit() const {
+    Pack8<T> u;
+    u.v = make_uint4(a[0] | b[0] << 16, a[1] | b[1] << 16, a[2] | b[2] << 16, a[3] | b[3] << 16);
+    return u;
+  }
+};
+
+template <>
+struct Raw<MP_FP32, false> {
+  float f[8];
+
+  __device__ __forceinline__ void load(const float* row, int base, int l, int n) {
+    const float* p = row + base + l;
+    if (base + 256 <= n) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = p[32 * i];
+    } else {
+      const int left = n - base - l;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = 32 * i < left ? p[32 * i] : 0.0f;
+    }
+  }
+  __device__ __forceinline__ Pack8<MP_FP32> unit() const {
+    Pack8<MP_FP32> u;
+    u.put(f);
+    return u;
+  }
+};
+
 template <int T>
-__device__ __forceinline__ void load_across(Pack8<T>& u, const typename Elem<T>::type* row, int c, int n) {
-  using E = typename Elem<T>::type;
-  constexpr int kPiece = 16 / sizeof(E);
-  const E* p = row + c;
-  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-  const int off = static_cast<int>(at % 16 / sizeof(E));
-  const uint4* base = reinterpret_cast<const uint4*>(at - at % 16);
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  // a piece is read if it holds a column of the row
-  const uint4 a = c < n ? base[0] : zero;
-  if constexpr (T == MP_FP32) {
-    const uint4 b = c + kPiece - off < n ? base[1] : zero;
-    const uint4 d = off && c + 2 * kPiece - off < n ? base[2] : zero;
-    const uint32_t w[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, d.x, d.y, d.z, d.w};
-    uint32_t t[10];
+struct Raw<T, true> {
+  Pack8<T> u;
+
+  __device__ __forceinline__ void load(const typename Elem<T>::type* row, int base, int l, int n) {
+    const int c = base + 8 * l;
+    if (c < n)
+      u.load(row + c);
+    else
+      u.zero();
+  }
+  __device__ __forceinline__ Pack8<T> unit() const { return u; }
+};
+
+template <>
+struct Raw<MP_FP32, true> {
+  Pack8<MP_FP32> u;
+
+  __device__ __forceinline__ void load(const float* row, int base, int l, int n) {
+    const int c = base + 8 * l;
+    if (c < n)
+      u.load(row + c);
+    else
+      u.zero();
+  }
+  __device__ __forceinline__ Pack8<MP_FP32> unit() const { return u; }
+};
+
+template <int T, bool Wide>
+__device__ __forceinline__ void store_unit(const Pack8<T>& u, typename Elem<T>::type* row, int base, int l, int n) {
+  if constexpr (Wide) {
+    const int c = base + 8 * l;
+    if (c < n) u.store(row + c);
+  } else if constexpr (T == MP_FP32) {
+    float* p = row + base + l;
     float f[8];
+    u.get(f);
+    if (base + 256 <= n) {
 #pragma unroll
-    for (int i = 0; i < 10; ++i) t[i] = off & 2 ? w[i + 2] : w[i];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(off & 1 ? t[i + 1] : t[i]);
-    if (c + 8 > n)
+      for (int i = 0; i < 8; ++i) p[32 * i] = f[i];
+    } else {
+      const int left = n - base - l;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (c + i >= n) f[i] = 0.0f;
-    u.put(f);
-  } else {
-    const uint4 b = off && c + kPiece - off < n ? base[1] : zero;
-    u.across(p, a, b);
-    if (c + 8 > n) {
-      const int left = c < n ? n - c : 0;
-      uint32_t w[4] = {u.v.x, u.v.y, u.v.z, u.v.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = 2 * i + 1 < left ? w[i] : 2 * i < left ? w[i] & 0xFFFFu : 0u;
-      u.v = make_uint4(w[0], w[1], w[2], w[3]);
+        if (32 * i < left) p[32 * i] = f[i];
     }
-  }
-}
-
-template <int T, bool Wide>
-__device__ __forceinline__ void load_unit(Pack8<T>& u, const typename Elem<T>::type* row, int c, int n) {
-  if (!Wide)
-    load_across(u, row, c, n);
-  else if (c < n)
-    u.load(row + c);
-  else
-    u.zero();
-}
-
-// Writes the units of a warp. All lanes call; runs of `run` neighbouring lanes hold
-// neighbouring units of one row (the lanes whose `live` is false, whole runs,
-// write nothing). Rows off the 16-byte grid: a lane gets the end of its neighbour's
-// unit by shuffles and writes the 16-byte piece that its own first columns lie
-// in; what no whole piece holds (a run's ends, a row's end) is written by elements. Written by
-// elements throughout, each of eight stores of a warp touches all its sectors:
-// 1021 x 2731 fp16 backward 21.9 us that way.
-template <int T, bool Wide>
-__device__ __forceinline__ void store_unit(const Pack8<T>& u, typename Elem<T>::type* row, int c, int n,
-                                           bool live, int run) {
-  using E = typename Elem<T>::type;
-  if constexpr (Wide) {
-    if (live && c < n) u.store(row + c);
   } else {
-    constexpr int kPiece = 16 / sizeof(E);
-    const int lane = threadIdx.x % 32;
-    const bool first = lane % run == 0, last = (lane + 1) % run == 0;
-    E* at = row + c;
-    const int p = static_cast<int>(reinterpret_cast<uintptr_t>(at) % 16 / sizeof(E));
-    // whether the piece that column c (or the next unit's) lies in is in the row and in the warp
-    const bool whole = (p == 0 || !first) && c - p + kPiece <= n;
-    const bool next = p == 0 || (!last && c + 8 - p + kPiece <= n);
-    uint32_t own = 0;  // elements to be written one by one
-    if constexpr (T == MP_FP32) {
-      float f[8], w[11];
-      u.get(f);
+    uint16_t* p = row + base + 2 * l;
+    const uint32_t w[4] = {u.v.x, u.v.y, u.v.z, u.v.w};
+    if (base + 256 <= n && reinterpret_cast<uintptr_t>(row) % 4 == 0) {
 #pragma unroll
-      for (int i = 0; i < 3; ++i) w[i] = __shfl_up_sync(kAll, f[5 + i], 1);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[3 + i] = f[i];
-      float t[9], o[8];  // o: columns c - p to c - p + 7
-#pragma unroll
-      for (int i = 0; i < 9; ++i) t[i] = p & 2 ? w[i] : w[i + 2];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = p & 1 ? t[i] : t[i + 1];
-      const bool second = c - p + 8 <= n;  // all of it the lane's own
-      if (live && whole) *reinterpret_cast<float4*>(at - p) = make_float4(o[0], o[1], o[2], o[3]);
-      if (live && second) *reinterpret_cast<float4*>(at - p + 4) = make_float4(o[4], o[5], o[6], o[7]);
-      own = (whole ? 0u : (1u << (4 - p)) - 1u) | (second ? 0u : 0xF0u >> p & 0xFFu) |
-            (next ? 0u : 0xFF00u >> p & 0xFFu);
-      if (live && own)
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if ((own >> e & 1) && c + e < n) at[e] = f[e];
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t*>(p + 64 * i) = w[i];
     } else {
-      uint4 before;
-      before.x = __shfl_up_sync(kAll, u.v.x, 1);
-      before.y = __shfl_up_sync(kAll, u.v.y, 1);
-      before.z = __shfl_up_sync(kAll, u.v.z, 1);
-      before.w = __shfl_up_sync(kAll, u.v.w, 1);
-      Pack8<T> o = u;
-      // eight elements, 8 - p into the neighbour's unit
-      if (p) o.across(reinterpret_cast<const E*>(static_cast<uintptr_t>(16 - 2 * p)), before, u.v);
-      if (live && whole) o.store(at - p);
-      own = (whole ? 0u : (1u << (8 - p)) - 1u) | (next ? 0u : 0xFF00u >> p & 0xFFu);
-      if (live && own) {
-        const uint32_t w[4] = {u.v.x, u.v.y, u.v.z, u.v.w};
+      const int left = n - base - 2 * l;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if ((own >> e & 1) && c + e < n)
-            at[e] = static_cast<uint16_t>(e % 2 ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu);
+      for (int i = 0; i < 4; ++i) {
+        if (64 * i < left) p[64 * i] = static_cast<uint16_t>(w[i]);
+        if (64 * i + 1 < left) p[64 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
       }
     }
   }
 }
 
-// The same of eight bytes.
-template <bool Wide>
-__device__ __forceinline__ uint2 load_unit8(const uint8_t* row, int c, int n) {
-  const uint2 zero = make_uint2(0u, 0u);
-  if constexpr (Wide) {
-    return c < n ? *reinterpret_cast<const uint2*>(row + c) : zero;
-  } else {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
-    const int off = static_cast<int>(at % 8);
-    const uint2* base = reinterpret_cast<const uint2*>(at - off);
-    const uint2 a = c < n ? base[0] : zero;
-    const uint2 b = off && c + 8 - off < n ? base[1] : zero;
-    const uint32_t t[4] = {a.x, a.y, b.x, b.y};
-    const bool one = off & 4;
-    const uint32_t w[3] = {one ? t[1] : t[0], one ? t[2] : t[1], one ? t[3] : t[2]};
-    const uint32_t shift = 8 * (off & 3);
-    uint2 q = make_uint2(__funnelshift_r(w[0], w[1], shift), __funnelshift_r(w[1], w[2], shift));
-    if (c + 8 > n) {
-      const int left = c < n ? n - c : 0;
-      q.x = left >= 4 ? q.x : q.x & ((1u << (8 * left)) - 1u);
-      q.y = left <= 4 ? 0u : q.y & ((1u << (8 * (left - 4))) - 1u);
-    }
-    return q;
-  }
-}
+// The same of bytes, in the slots that elements of type T have.
+template <int T, bool Wide>
+struct Raw8 {  // 16-bit, not wide
+  uint32_t a[4], b[4];
 
-template <bool Wide>
-__device__ __forceinline__ void store_unit8(uint2 q, uint8_t* row, int c, int n, bool live, int run) {
-  if constexpr (Wide) {
-    if (live && c < n) *reinterpret_cast<uint2*>(row + c) = q;
-  } else {
-    const int lane = threadIdx.x % 32;
-    const bool first = lane % run == 0, last = (lane + 1) % run == 0;
-    uint8_t* at = row + c;
-    const int p = static_cast<int>(reinterpret_cast<uintptr_t>(at) % 8);
-    const bool whole = (p == 0 || !first) && c - p + 8 <= n;
-    const bool next = p == 0 || (!last && c + 16 - p <= n);
-    const uint2 before = make_uint2(__shfl_up_sync(kAll, q.x, 1), __shfl_up_sync(kAll, q.y, 1));
-    if (live && whole) {
-      uint2 o = q;
-      if (p) {
-        const uint32_t w[3] = {p > 4 ? before.x : before.y, p > 4 ? before.y : q.x, p > 4 ? q.x : q.y};
-        // the last p bytes of the neighbour's unit, then the lane's own
-        const uint32_t shift = 8 * ((8 - p) & 3);
-        o = make_uint2(__funnelshift_r(w[0], w[1], shift), __funnelshift_r(w[1], w[2], shift));
-      }
-      *reinterpret_cast<uint2*>(at - p) = o;
-    }
-    const uint32_t own = (whole ? 0u : (1u << (8 - p)) - 1u) | (next ? 0u : 0xFF00u >> p & 0xFFu);
-    if (live && own)
+  __device__ __forceinline__ void load(const uint8_t* row, int base, int l, int n) {
+    const uint8_t* p = row + base + 2 * l;
+    const bool even = reinterpret_cast<uintptr_t>(row) % 2 == 0;
+    if (base + 256 <= n) {
+      if (even) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if ((own >> e & 1) && c + e < n) at[e] = static_cast<uint8_t>((e < 4 ? q.x : q.y) >> (8 * (e % 4)));
+        for (int i = 0; i < 4; ++i) {
+          a[i] = *reinterpret_cast<const uint16_t*>(p + 64 * i);
+          b[i] = 0u;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[i] = p[64 * i];
+          b[i] = p[64 * i + 1];
+        }
+      }
+    } else {
+      const int left = n - base - 2 * l;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i] = 64 * i < left ? p[64 * i] : 0u;
+        b[i] = 64 * i + 1 < left ? p[64 * i + 1] : 0u;
+      }
+    }
+  }
+  __device__ __forceinline__ uint2 unit() const {
+    return make_uint2(a[0] | b[0] << 8 | a[1] << 16 | b[1] << 24, a[2] | b[2] << 8 | a[3] << 16 | b[3] << 24);
+  }
+};
+
+template <>
+struct Raw8<MP_FP32, false> {
+  uint32_t b[8];
+
+  __device__ __forceinline__ void load(const uint8_t* row, int base, int l, int n) {
+    const uint8_t* p = row + base + l;
+    const int left = n - base - l;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = 32 * i < left ? p[32 * i] : 0u;
+  }
+  __device__ __forceinline__ uint2 unit() const {
+    return make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24);
+  }
+};
+
+struct Raw8Wide {
+  uint2 q;
+
+  __device__ __forceinline__ void load(const uint8_t* row, int base, int l, int n) {
+    const int c = base + 8 * l;
+    q = c < n ? *reinterpret_cast<const uint2*>(row + c) : make_uint2(0u, 0u);
+  }
+  __device__ __forceinline__ uint2 unit() const { return q; }
+};
+
+template <int T>
+struct Raw8<T, true> : Raw8Wide {};
+template <>
+struct Raw8<MP_FP32, true> : Raw8Wide {};
+
+template <int T, bool Wide>
+__device__ __forceinline__ void store_unit8(uint2 q, uint8_t* row, int base, int l, int n) {
+  if constexpr (Wide) {
+    const int c = base + 8 * l;
+    if (c < n) *reinterpret_cast<uint2*>(row + c) = q;
+  } else if constexpr (T == MP_FP32) {
+    uint8_t* p = row + base + l;
+    const int left = n - base - l;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (32 * i < left) p[32 * i] = static_cast<uint8_t>((i < 4 ? q.x : q.y) >> (8 * (i % 4)));
+  } else {
+    uint8_t* p = row + base + 2 * l;
+    const uint32_t w[4] = {q.x, q.x >> 16, q.y, q.y >> 16};
+    if (base + 256 <= n && reinterpret_cast<uintptr_t>(row) % 2 == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint16_t*>(p + 64 * i) = static_cast<uint16_t>(w[i]);
+    } else {
+      const int left = n - base - 2 * l;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (64 * i < left) p[64 * i] = static_cast<uint8_t>(w[i]);
+        if (64 * i + 1 < left) p[64 * i + 1] = static_cast<uint8_t>(w[i] >> 8);
+      }
+    }
   }
 }
 
@@ -362,57 +422,140 @@ __device__ __forceinline__ float block_scale_value(uint32_t byte) {
   return byte == kScaleNan ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte ? byte << 23 : 0x00400000u);
 }
 
-// Eight values of an element type T over their block's scale, in 8 bits. Where
-// the block's scale is the type's largest exponent's, values up to 255.9 of it
-// would round to 256, above what the type holds.
-template <int T>
-__device__ __forceinline__ uint2 block_pack(const F8& f, uint32_t byte) {
-  constexpr uint32_t kTop = T == MP_FP16 ? 127u + 15u - 7u : 127u + 127u - 7u;
-  // an exact product: the inverse is a power of two as well
-  const float inverse = byte == kScaleNan ? __uint_as_float(0x7FC00000u) : __uint_as_float((254u - byte) << 23);
-  F8 g = mul8(f, inverse);
-  if (byte == kTop) {
+// Slots whose columns share a scale: all eight, a pair, one.
+template <int T, bool Wide>
+constexpr int kShare = Wide ? 8 : T == MP_FP32 ? 1 : 2;
+
+// The inverse of a scale, itself a power of two, so that products with it are exact.
+__device__ __forceinline__ float block_inverse(uint32_t byte) {
+  return __uint_as_float(byte == kScaleNan ? 0x7FC00000u : (254u - byte) << 23);
+}
+
+// Where the block's scale is that of the largest exponent of the element type V,
+// values up to 255.9 of it would round to 256, above what the type holds.
+template <int V>
+__device__ __forceinline__ bool block_top(uint32_t byte) {
+  return byte == (V == MP_FP16 ? 127u + 15u - 7u : 127u + 127u - 7u);
+}
+__device__ __forceinline__ float below_256(float f) { return fminf(fmaxf(f, -240.0f), 240.0f); }
+
+// The largest magnitudes of the blocks that a lane's slots are in, NaN if one is NaN
+// (all lanes of the warp call): of values in fp32, and of 16-bit ones as
+// integers, two at a time: without the sign, patterns rise with the magnitude, infinities
+// next and NaN last.
+template <int T, bool Wide>
+__device__ __forceinline__ void blocks_amax(float (&m)[8 / kShare<T, Wide>], const F8& f) {
+  if constexpr (Wide) {
+    m[0] = amax8(0.0f, f);
+    m[0] = max_nan(m[0], __shfl_xor_sync(kAll, m[0], 1));
+    m[0] = max_nan(m[0], __shfl_xor_sync(kAll, m[0], 2));
+  } else if constexpr (T == MP_FP32) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      g.p[i] = make_float2(fminf(fmaxf(g.p[i].x, -240.0f), 240.0f), fminf(fmaxf(g.p[i].y, -240.0f), 240.0f));
+    for (int i = 0; i < 4; ++i) {
+      m[2 * i] = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(f.p[i].x) & 0x7FFFFFFFu));
+      m[2 * i + 1] = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(f.p[i].y) & 0x7FFFFFFFu));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = amax2(0.0f, f.p[i]);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) m[i] = max_nan(m[i], __shfl_xor_sync(kAll, m[i], o));
+    }
   }
-  return e4m3_pack(g);
 }
 
-// The largest magnitude of four neighbouring lanes' units, NaN if one is NaN (all
-// lanes of the warp call). Of 16-bit types as integers, two at a time: without
-// the sign, patterns rise with the magnitude, infinities next and NaN last.
-__device__ __forceinline__ float quad_amax(const F8& f) {
-  float m = amax8(0.0f, f);
-  m = max_nan(m, __shfl_xor_sync(kAll, m, 1));
-  return max_nan(m, __shfl_xor_sync(kAll, m, 2));
-}
-
-template <int T>
-__device__ __forceinline__ float quad_amax(const Pack8<T>& u) {
+template <int T, bool Wide>
+__device__ __forceinline__ void blocks_amax(float (&m)[8 / kShare<T, Wide>], const Pack8<T>& u) {
   if constexpr (T == MP_FP32) {
-    return quad_amax(get8(u));
+    blocks_amax<T, Wide>(m, get8(u));
   } else {
     constexpr uint32_t kMask = 0x7FFF7FFFu;
-    uint32_t m = __vimax3_u16x2(u.v.x & kMask, u.v.y & kMask, u.v.z & kMask);
-    m = __vmaxu2(m, u.v.w & kMask);
-    m = __vmaxu2(m, __shfl_xor_sync(kAll, m, 1));
-    m = __vmaxu2(m, __shfl_xor_sync(kAll, m, 2));
-    return Elem<T>::get(static_cast<uint16_t>(max(m & 0xFFFFu, m >> 16)));
+    if constexpr (Wide) {
+      uint32_t w = __vimax3_u16x2(u.v.x & kMask, u.v.y & kMask, u.v.z & kMask);
+      w = __vmaxu2(w, u.v.w & kMask);
+      w = __vmaxu2(w, __shfl_xor_sync(kAll, w, 1));
+      w = __vmaxu2(w, __shfl_xor_sync(kAll, w, 2));
+      m[0] = Elem<T>::get(static_cast<uint16_t>(max(w & 0xFFFFu, w >> 16)));
+    } else {
+      // pairs 0 and 1, 2 and 3 side by side
+      const auto side = [](uint32_t a, uint32_t b) {
+        return __vmaxu2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632)) & kMask;
+      };
+      uint32_t a = side(u.v.x & kMask, u.v.y & kMask), b = side(u.v.z & kMask, u.v.w & kMask);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) {
+        a = __vmaxu2(a, __shfl_xor_sync(kAll, a, o));
+        b = __vmaxu2(b, __shfl_xor_sync(kAll, b, o));
+      }
+      m[0] = Elem<T>::get(static_cast<uint16_t>(a));
+      m[1] = Elem<T>::get(static_cast<uint16_t>(a >> 16));
+      m[2] = Elem<T>::get(static_cast<uint16_t>(b));
+      m[3] = Elem<T>::get(static_cast<uint16_t>(b >> 16));
+    }
   }
 }
 
-// Puts the unit at column c of a row, eight values f whose block's largest
-// magnitude is amax, away in 8 bits with the block's scale. Four neighbouring lanes hold
-// a block's four units; units past the row are zeros and write nothing. live, run: as
-// store_unit.
-template <int T, bool Wide>
-__device__ __forceinline__ void put_block8(const F8& f, float amax, uint8_t* row, uint8_t* scales, int c, int n,
-                                           bool live, int run) {
-  const uint32_t byte = block_scale(amax);
-  store_unit8<Wide>(block_pack<T>(f, byte), row, c, n, live, run);
-  if (live && c < n && c % 32 == 0) scales[c / 32] = static_cast<uint8_t>(byte);
+// Puts a lane's eight values f (of element type V, whose blocks' largest magnitudes
+// are m) away in 8 bits with the blocks' scales. Slots past the row are zeros;
+// where `live` is false nothing is written.
+template <int T, int V, bool Wide>
+__device__ __forceinline__ void put_block8(const F8& f, const float (&m)[8 / kShare<T, Wide>], uint8_t* row,
+                                           uint8_t* scales, int base, int l, int n, bool live) {
+  constexpr int kS = kShare<T, Wide>;
+  uint32_t byte[8 / kS];
+  float inverse[8 / kS];
+  bool top = false;
+#pragma unroll
+  for (int i = 0; i < 8 / kS; ++i) {
+    byte[i] = block_scale(m[i]);
+    inverse[i] = block_inverse(byte[i]);
+    top = top || block_top<V>(byte[i]);
+  }
+  F8 g;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) g.p[i] = mul2(f.p[i], make_float2(inverse[2 * i / kS], inverse[(2 * i + 1) / kS]));
+  if (top) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (block_top<V>(byte[2 * i / kS])) g.p[i].x = below_256(g.p[i].x);
+      if (block_top<V>(byte[(2 * i + 1) / kS])) g.p[i].y = below_256(g.p[i].y);
+    }
+  }
+  if (!live) return;
+  store_unit8<T, Wide>(e4m3_pack(g), row, base, l, n);
+  if (l % (32 / kS) == 0) {
+    const int c = slot_column<T, Wide>(base, l, 0);
+    uint8_t* p = scales + static_cast<uint32_t>(c) / 32;
+#pragma unroll
+    for (int i = 0; i < 8 / kS; ++i)
+      if (c + 32 * kS * i < n) p[kS * i] = static_cast<uint8_t>(byte[i]);
+  }
 }
+
+// The scales of a lane's slots, a byte for each share, and the values that its 8 bits
+// stand for, times `factor`.
+template <int T, bool Wide>
+struct RawScales {
+  static constexpr int kS = kShare<T, Wide>;
+  uint32_t b[8 / kS];
+
+  __device__ __forceinline__ void load(const uint8_t* scales, int base, int l, int n) {
+    const int c = slot_column<T, Wide>(base, l, 0);
+    const uint8_t* p = scales + static_cast<uint32_t>(c) / 32;
+#pragma unroll
+    for (int i = 0; i < 8 / kS; ++i) b[i] = c + 32 * kS * i < n ? p[kS * i] : 0u;
+  }
+  __device__ __forceinline__ F8 values(uint2 q, float factor) const {
+    float s[8 / kS];
+#pragma unroll
+    for (int i = 0; i < 8 / kS; ++i) s[i] = __fmul_rn(block_scale_value(b[i]), factor);
+    F8 r = e4m3_unpack(q);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.p[i] = mul2(r.p[i], make_float2(s[2 * i / kS], s[(2 * i + 1) / kS]));
+    return r;
+  }
+};
 
 // ---- a scale for each row -----------------------------------------------------------
 

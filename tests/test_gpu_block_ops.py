@@ -119,6 +119,13 @@ def test_rmsnorm_classes(mp, d, dtype):  # noqa: F811
     rms_case(mp, 701, d, dtype, dtype)
 
 
+@pytest.mark.parametrize("dtype", [BF, FF])
+@pytest.mark.parametrize("d", [257, 513, 769, 1025, 2049, 2561, 4097, 5121, 6145, 7681, 8191, 8193])
+def test_rmsnorm_one_column_more(mp, d, dtype):  # noqa: F811
+    # one column past what a number of warps holds
+    rms_case(mp, 33, d, dtype, dtype)
+
+
 @pytest.mark.parametrize("d", [48, 1600, 1365, 9000])
 @pytest.mark.parametrize("dtype", [BF, FF])
 def test_rmsnorm_in_place_and_optional_outputs(mp, d, dtype):  # noqa: F811
