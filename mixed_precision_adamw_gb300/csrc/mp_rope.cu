@@ -16,8 +16,8 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int64_t kRopeSms = 152;
-constexpr int kMaxHeads = 1024;    // of queries, and of keys
-constexpr int kMaxHeadDim = 1024;  // so that heads * items * items < 2^32 (divisions by items)
+constexpr int kMaxHeads = 1024;  // of queries, and of keys
+constexpr int kMaxHeadDim = 1024;
 
 struct RopeSide {  // queries or keys
   void* out;
@@ -26,23 +26,19 @@ struct RopeSide {  // queries or keys
 };
 
 struct RopeArgs {
-  RopeSide q, k;
+  RopeSide side[2];
+  int heads[2];
   const uint64_t* turns;
   const void* positions;
   int64_t first, tokens;
-  int q_heads, heads;  // heads: of queries and keys
-  int pairs;           // rotary_dim / 2
-  int items;           // of a head
-  int per_block;       // tokens
-  uint32_t by_items, by_token;  // multipliers of the divisions by items and by heads * items
+  int head_dim, pairs;   // pairs: rotary_dim / 2
+  int items;             // of a head, each a lane's
+  int tokens_per_block;
+  uint32_t by_items, by_heads;  // multipliers of the divisions by items and by the number of heads
   float factor;
   int index_type;
   int inverse;
 };
-
-// n / d with m = ceil(2^32 / d), for n d < 2^32; d = 1 has m = 0.
-__device__ __forceinline__ uint32_t divide(uint32_t n, uint32_t m) { return m ? __umulhi(n, m) : n; }
-inline uint32_t divisor(uint32_t d) { return d == 1 ? 0u : static_cast<uint32_t>((uint64_t{1} << 32) / d + 1); }
 
 // (cos, sin) of `turn` / 2^64 turns.
 __device__ __forceinline__ float2 cos_sin(uint64_t turn) {
@@ -59,18 +55,9 @@ __device__ __forceinline__ float2 cos_sin(uint64_t turn) {
   return quadrant & 2 ? make_float2(-c, -s) : make_float2(c, s);
 }
 
-// Items of a head: with Wide, first the rotated units, then units that are
-// copied. Half layout: a rotated unit is eight columns and their partners half a
-// rotation further; interleaved: eight columns, four pairs. Otherwise an item is
-// a pair, or a copied column.
-template <int T, bool Wide, bool Interleaved>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
-  pdl_enter();
-  using E = Elem<T>;
-  using S = typename E::type;
-  extern __shared__ float2 angle[];  // [token of the block][pair]
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.per_block;
-  const int tokens = static_cast<int>(min(static_cast<int64_t>(a.per_block), a.tokens - t0));
+// The angles of `tokens` tokens from t0 on, in shared memory: (cos, sin) * factor,
+// [token][pair].
+__device__ __forceinline__ void make_angles(float2* angle, const RopeArgs& a, int64_t t0, int tokens) {
   for (int i = threadIdx.x; i < tokens * a.pairs; i += kRopeThreads) {
     const int token = i / a.pairs;
     const int64_t p = a.positions ? load_index(a.positions, t0 + token, a.index_type) : a.first + t0 + token;
@@ -78,69 +65,257 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
     if (a.inverse) cs.y = -cs.y;
     angle[i] = make_float2(__fmul_rn(cs.x, a.factor), __fmul_rn(cs.y, a.factor));
   }
-  __syncthreads();
-  const uint32_t per_token = static_cast<uint32_t>(a.heads) * a.items;
-  const int rotated = Wide ? (Interleaved ? a.pairs / 4 : a.pairs / 8) : a.pairs;
-  for (uint32_t n = threadIdx.x; n < tokens * per_token; n += kRopeThreads) {
-    const uint32_t token = a.per_block == 1 ? 0u : divide(n, a.by_token), rest = n - token * per_token;
-    int head = static_cast<int>(divide(rest, a.by_items));
-    const int item = static_cast<int>(rest - static_cast<uint32_t>(head) * a.items);
-    const bool is_k = head >= a.q_heads;
-    if (is_k) head -= a.q_heads;
-    const RopeSide& side = is_k ? a.k : a.q;
-    const S* in = static_cast<const S*>(side.in) + (t0 + token) * side.in_token + head * side.in_head;
-    S* out = static_cast<S*>(side.out) + (t0 + token) * side.out_token + head * side.out_head;
-    const float2* cs = angle + token * a.pairs;
-    if (Wide) {
-      Pack8<T> x;
-      if (item >= rotated) {
-        if (in == out) continue;
-        const int c = 2 * a.pairs + 8 * (item - rotated);
-        x.load(in + c);
-        x.store(out + c);
-        continue;
+}
+
+// A pair's column rotated by (cos, sin): the first with its partner's sign turned.
+__device__ __forceinline__ float turned(float own, float other, float2 w) {
+  return __fmaf_rn(other, w.y, __fmul_rn(own, w.x));
+}
+__device__ __forceinline__ void rotate(float& x, float& y, float2 w) {
+  const float u = x, v = y;
+  x = turned(u, -v, w);
+  y = turned(v, u, w);
+}
+
+// What a lane has of a head at a time, eight columns an access, on the 16-byte grid.
+//
+// Half layout, whole vectors of pairs: two vectors, eight pairs (or of the copied columns).
+template <int T>
+struct HalfItem {
+  using E = typename Elem<T>::type;
+  static constexpr int kBlocks = T == MP_FP32 ? 6 : 8;  // of an SM
+  Pack8<T> x, y;
+
+  static __device__ __forceinline__ int rest(const RopeArgs& a) { return (a.head_dim - 2 * a.pairs) / 8; }
+  // columns of the second vector after the first's, 0 if there is none
+  static __device__ __forceinline__ int first(const RopeArgs& a, int item) {
+    const int j = item - a.pairs / 8;
+    return j < 0 ? 8 * item : 2 * a.pairs + 8 * j;
+  }
+  static __device__ __forceinline__ int apart(const RopeArgs& a, int item) {
+    const int j = item - a.pairs / 8, n = rest(a), half = (n + 1) / 2;
+    return j < 0 ? a.pairs : j + half < n ? 8 * half : 0;
+  }
+  __device__ __forceinline__ void load(const RopeArgs& a, const E* head, int item) {
+    const E* p = head + first(a, item);
+    const int q = apart(a, item);
+    x.load(p);
+    if (q) y.load(p + q);
+  }
+  __device__ __forceinline__ void finish(const RopeArgs& a, E* head, const float2* cs, int item) {
+    E* p = head + first(a, item);
+    const int q = apart(a, item);
+    if (item < a.pairs / 8) {
+      float f[8], g[8];
+      x.get(f);
+      y.get(g);
+      const float4* w = reinterpret_cast<const float4*>(cs + 8 * item);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 v = w[i];
+        rotate(f[2 * i], g[2 * i], make_float2(v.x, v.y));
+        rotate(f[2 * i + 1], g[2 * i + 1], make_float2(v.z, v.w));
       }
-      float f[8];
-      x.load(in + 8 * item);
-      if (Interleaved) {
-        x.get(f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 w = cs[4 * item + i];
-          const float u = f[2 * i], v = f[2 * i + 1];
-          f[2 * i] = __fmaf_rn(u, w.x, -__fmul_rn(v, w.y));
-          f[2 * i + 1] = __fmaf_rn(u, w.y, __fmul_rn(v, w.x));
-        }
-        x.put(f);
-        x.store(out + 8 * item);
-      } else {
-        Pack8<T> y;
-        float g[8];
-        y.load(in + a.pairs + 8 * item);
-        x.get(f);
-        y.get(g);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 w = cs[8 * item + i];
-          const float u = f[i], v = g[i];
-          f[i] = __fmaf_rn(u, w.x, -__fmul_rn(v, w.y));
-          g[i] = __fmaf_rn(u, w.y, __fmul_rn(v, w.x));
-        }
-        x.put(f);
-        y.put(g);
-        x.store(out + 8 * item);
-        y.store(out + a.pairs + 8 * item);
+      x.put(f);
+      y.put(g);
+    }
+    x.store(p);
+    if (q) y.store(p + q);
+  }
+};
+
+// Half layout, any number of pairs: eight columns, and their partners, which lie
+// off the grid: cut out of the two 16-byte pieces that they are in, or, of columns on
+// both sides of the middle or the end of the rotation and of fp32, one by one.
+template <int T>
+struct AnyHalfItem {
+  using E = typename Elem<T>::type;
+  static constexpr int kBlocks = 5;
+  Pack8<T> x;
+  uint32_t p[8];
+
+  static __device__ __forceinline__ bool pieces(const RopeArgs& a, int c) {
+    return T != MP_FP32 && (c + 8 <= a.pairs || (c >= a.pairs && c + 8 <= 2 * a.pairs));
+  }
+  __device__ __forceinline__ void load(const RopeArgs& a, const E* head, int item) {
+    const int c = 8 * item, h = a.pairs;
+    x.load(head + c);
+    if (c >= 2 * h) return;
+    if (pieces(a, c)) {
+      const E* q = head + (c < h ? c + h : c - h);
+      const uintptr_t at = reinterpret_cast<uintptr_t>(q);
+      const uint4* base = reinterpret_cast<const uint4*>(at - at % 16);
+      const uint4 lo = base[0];
+      p[0] = lo.x, p[1] = lo.y, p[2] = lo.z, p[3] = lo.w;
+      if (at % 16) {  // otherwise the second piece may be beyond the head
+        const uint4 hi = base[1];
+        p[4] = hi.x, p[5] = hi.y, p[6] = hi.z, p[7] = hi.w;
       }
     } else {
-      if (item >= rotated) {
-        if (in != out) out[a.pairs + item] = in[a.pairs + item];
-        continue;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int k = c + e;
+        p[e] = 0;
+        if (k < 2 * h) {
+          const E v = head[k < h ? k + h : k - h];
+          p[e] = T == MP_FP32 ? __float_as_uint(v) : static_cast<uint32_t>(v);
+        }
       }
-      const int i = Interleaved ? 2 * item : item, j = Interleaved ? i + 1 : item + a.pairs;
-      const float2 w = cs[item];
-      const float u = E::get(in[i]), v = E::get(in[j]);
-      out[i] = E::put(__fmaf_rn(u, w.x, -__fmul_rn(v, w.y)));
-      out[j] = E::put(__fmaf_rn(u, w.y, __fmul_rn(v, w.x)));
+    }
+  }
+  // One path for all of a warp's lanes but for the partners' reading: the first half's, the
+  // second half's and the mixed units' code one after the other took 87 us where
+  // this takes 77 (16384 x 40 heads of 80, 50 columns rotated; a pair at a time 139).
+  __device__ __forceinline__ void finish(const RopeArgs& a, E* head, const float2* cs, int item) {
+    const int c = 8 * item, h = a.pairs;
+    if (c < 2 * h) {
+      float f[8], g[8];
+      x.get(f);
+      if constexpr (T == MP_FP32) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = __uint_as_float(p[e]);
+      } else {
+        Pack8<T> y;
+        if (pieces(a, c))
+          y.across(head + (c < h ? c + h : c - h), make_uint4(p[0], p[1], p[2], p[3]),
+                   make_uint4(p[4], p[5], p[6], p[7]));  // on the same place of the grid as in load()
+        else
+          y.v = make_uint4(p[0] | p[1] << 16, p[2] | p[3] << 16, p[4] | p[5] << 16, p[6] | p[7] << 16);
+        y.get(g);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int k = c + e;
+        const bool first = k < h;
+        const float t = turned(f[e], first ? -g[e] : g[e], cs[first ? k : min(k - h, h - 1)]);
+        f[e] = k < 2 * h ? t : f[e];
+      }
+      x.put(f);
+    }
+    x.store(head + c);
+  }
+};
+
+// Interleaved: two vectors, four pairs each.
+template <int T>
+struct InterleavedItem {
+  using E = typename Elem<T>::type;
+  static constexpr int kBlocks = T == MP_FP32 ? 6 : 8;
+  Pack8<T> x[2];
+
+  static __device__ __forceinline__ bool second(const RopeArgs& a, int item) {
+    return 8 * (item + a.items) < a.head_dim;
+  }
+  __device__ __forceinline__ void load(const RopeArgs& a, const E* head, int item) {
+    x[0].load(head + 8 * item);
+    if (second(a, item)) x[1].load(head + 8 * (item + a.items));
+  }
+  __device__ __forceinline__ void finish(const RopeArgs& a, E* head, const float2* cs, int item) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int j = item + k * a.items;
+      if (k && !second(a, item)) break;
+      if (4 * j < a.pairs) {
+        float f[8];
+        x[k].get(f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (4 * j + i < a.pairs) rotate(f[2 * i], f[2 * i + 1], cs[4 * j + i]);
+        x[k].put(f);
+      }
+      x[k].store(head + 8 * j);
+    }
+  }
+};
+
+// n / d with m = floor(2^32 / d) + 1, for n d < 2^32; d = 1 has m = 0.
+__device__ __forceinline__ int divide(int n, uint32_t m) {
+  return m ? static_cast<int>(__umulhi(static_cast<uint32_t>(n), m)) : n;
+}
+inline uint32_t divisor(int d) { return d == 1 ? 0u : static_cast<uint32_t>((uint64_t{1} << 32) / d + 1); }
+
+// A block takes a few tokens, a lane one item at a time of all their heads, those of
+// queries and keys counted together. With 32 to 40 registers six to eight blocks an SM
+// hide each other's angles and loads: 16384 x (32 + 8) x 128 bf16 in 52 us; holding
+// four items a lane, loaded before the angles, 67.
+template <int T, typename Item>
+__global__ void __launch_bounds__(kRopeThreads, Item::kBlocks) rope_kernel(RopeArgs a) {
+  pdl_enter();
+  using S = typename Elem<T>::type;
+  extern __shared__ __align__(16) float2 angle[];  // [token of the block][pair]
+  const int heads = a.heads[0] + a.heads[1];
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens_per_block;
+  const int tokens = static_cast<int>(min(static_cast<int64_t>(a.tokens_per_block), a.tokens - t0));
+  make_angles(angle, a, t0, tokens);
+  __syncthreads();
+  for (int n = threadIdx.x; n < tokens * heads * a.items; n += kRopeThreads) {
+    const int row = divide(n, a.by_items), item = n - row * a.items;
+    const int token = a.tokens_per_block == 1 ? 0 : divide(row, a.by_heads);
+    int head = row - token * heads;
+    const bool is_k = head >= a.heads[0];
+    if (is_k) head -= a.heads[0];
+    const RopeSide& s = a.side[is_k];
+    Item part;
+    part.load(a, static_cast<const S*>(s.in) + (t0 + token) * s.in_token + head * s.in_head, item);
+    part.finish(a, static_cast<S*>(s.out) + (t0 + token) * s.out_token + head * s.out_head, angle + token * a.pairs,
+                item);
+  }
+}
+
+// Heads off the 16-byte grid: a pair, or two columns that are copied, at a time. A
+// thread has one of every slots-th head of a block's tokens, queries first, so that
+// per head it only moves its pointers on.
+template <int T, bool Interleaved>
+__global__ void __launch_bounds__(kRopeThreads) rope_pairs_kernel(RopeArgs a) {
+  pdl_enter();
+  using E = Elem<T>;
+  using S = typename E::type;
+  extern __shared__ __align__(16) float2 angle[];
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens_per_block;
+  const int tokens = static_cast<int>(min(static_cast<int64_t>(a.tokens_per_block), a.tokens - t0));
+  make_angles(angle, a, t0, tokens);
+  __syncthreads();
+  const int lanes = min(a.items, kRopeThreads), slots = kRopeThreads / lanes, slot = threadIdx.x / lanes;
+  if (slot >= slots) return;
+  const int rest = a.head_dim - 2 * a.pairs, half = (rest + 1) / 2;
+  for (int item = threadIdx.x - slot * lanes; item < a.items; item += lanes) {
+    const int j = item - a.pairs;
+    const bool turns = j < 0, second = turns || j + half < rest;
+    const int c0 = turns ? (Interleaved ? 2 * item : item) : 2 * a.pairs + j;
+    const int c1 = turns ? (Interleaved ? c0 + 1 : c0 + a.pairs) : c0 + half;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const RopeSide& s = a.side[k];
+      const int heads = a.heads[k];
+      if (heads == 0 || (!turns && s.in == s.out)) continue;
+      int token = slot / heads, head = slot - token * heads;
+      const int dt = slots / heads, dh = slots - dt * heads;
+      const S* in = static_cast<const S*>(s.in) + (t0 + token) * s.in_token + head * s.in_head;
+      S* out = static_cast<S*>(s.out) + (t0 + token) * s.out_token + head * s.out_head;
+      const int64_t in_step = dt * s.in_token + dh * s.in_head, in_wrap = s.in_token - heads * s.in_head;
+      const int64_t out_step = dt * s.out_token + dh * s.out_head, out_wrap = s.out_token - heads * s.out_head;
+      while (token < tokens) {
+        S x = in[c0], y = {};
+        if (second) y = in[c1];
+        if (turns) {
+          float f = E::get(x), g = E::get(y);
+          rotate(f, g, angle[token * a.pairs + item]);
+          x = E::put(f);
+          y = E::put(g);
+        }
+        out[c0] = x;
+        if (second) out[c1] = y;
+        token += dt;
+        head += dh;
+        in += in_step;
+        out += out_step;
+        if (head >= heads) {
+          head -= heads;
+          ++token;
+          in += in_wrap;
+          out += out_wrap;
+        }
+      }
     }
   }
 }
@@ -168,7 +343,8 @@ bool side_aligned(const RopeSide& s, int heads, int32_t type) {
   return heads == 0 || (type_aligned(s.out, type) && type_aligned(s.in, type));
 }
 
-bool side_wide(const RopeSide& s, int heads, int64_t tokens, int32_t type) {
+// Whether a side's heads lie on the 16-byte grid.
+bool side_wide(const RopeSide& s, int64_t tokens, int heads, int32_t type) {
   const int64_t unit = type == MP_FP32 ? 4 : 8;
   const auto ok = [&](const void* p, int64_t token, int64_t head) {
     return aligned_to(p, 16) && (tokens <= 1 || token % unit == 0) && (heads <= 1 || head % unit == 0);
@@ -176,24 +352,38 @@ bool side_wide(const RopeSide& s, int heads, int64_t tokens, int32_t type) {
   return heads == 0 || (ok(s.out, s.out_token, s.out_head) && ok(s.in, s.in_token, s.in_head));
 }
 
-template <int T>
-cudaError_t rope(RopeArgs& a, int head_dim, int k_heads, bool interleaved, cudaStream_t s) {
-  const bool wide = side_wide(a.q, a.q_heads, a.tokens, T) && side_wide(a.k, k_heads, a.tokens, T) &&
-                    head_dim % 8 == 0 && a.pairs % (interleaved ? 4 : 8) == 0;
-  const int rest = head_dim - 2 * a.pairs;
-  a.items = wide ? (interleaved ? a.pairs / 4 : a.pairs / 8) + rest / 8 : a.pairs + rest;
-  const int64_t per_token = static_cast<int64_t>(a.heads) * a.items;
-  // Tokens of a block: several rounds of its threads, angles within 16 KB.
-  a.per_block = static_cast<int>(std::max<int64_t>(
-      1, std::min<int64_t>({(4 * kRopeThreads + per_token - 1) / per_token, 2048 / a.pairs, a.tokens / (2 * kRopeSms)})));
-  a.by_items = divisor(static_cast<uint32_t>(a.items));
-  a.by_token = divisor(static_cast<uint32_t>(per_token));
-  const int64_t blocks = (a.tokens + a.per_block - 1) / a.per_block;
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  const size_t smem = static_cast<size_t>(a.per_block) * a.pairs * sizeof(float2);
-  const auto kernel = wide ? (interleaved ? rope_kernel<T, true, true> : rope_kernel<T, true, false>)
-                           : (interleaved ? rope_kernel<T, false, true> : rope_kernel<T, false, false>);
+// Tokens of a block: several rounds of its threads, angles within 16 KB, fewer where
+// there are few tokens for all SMs.
+int tokens_of_block(const RopeArgs& a) {
+  const int64_t per_token = static_cast<int64_t>(a.heads[0] + a.heads[1]) * a.items;
+  return static_cast<int>(std::max<int64_t>(
+      1, std::min<int64_t>({(4 * kRopeThreads + per_token - 1) / per_token, 2048 / a.pairs, a.tokens / (8 * kRopeSms)})));
+}
+
+cudaError_t rope_launch(void (*kernel)(RopeArgs), RopeArgs& a, int items, cudaStream_t s) {
+  a.items = items;
+  a.tokens_per_block = tokens_of_block(a);
+  // n < tokens heads items, below 1024 + heads items: n items < 2^32
+  a.by_items = divisor(items);
+  a.by_heads = divisor(a.heads[0] + a.heads[1]);
+  const int64_t blocks = (a.tokens + a.tokens_per_block - 1) / a.tokens_per_block;
+  const size_t smem = static_cast<size_t>(a.tokens_per_block) * a.pairs * sizeof(float2);
   return launch_pdl_smem(kernel, static_cast<unsigned>(blocks), kRopeThreads, smem, s, a);
+}
+
+template <int T>
+cudaError_t rope(RopeArgs& a, bool interleaved, cudaStream_t s) {
+  const int rest = a.head_dim - 2 * a.pairs;
+  const bool over = (a.heads[0] && a.side[0].in == a.side[0].out) || (a.heads[1] && a.side[1].in == a.side[1].out);
+  if (a.head_dim % 8 == 0 && side_wide(a.side[0], a.tokens, a.heads[0], T) &&
+      side_wide(a.side[1], a.tokens, a.heads[1], T)) {
+    if (interleaved) return rope_launch(rope_kernel<T, InterleavedItem<T>>, a, (a.head_dim / 8 + 1) / 2, s);
+    if (a.pairs % 8 == 0) return rope_launch(rope_kernel<T, HalfItem<T>>, a, a.pairs / 8 + (rest / 8 + 1) / 2, s);
+    // over its input a pair has to be one lane's
+    if (!over) return rope_launch(rope_kernel<T, AnyHalfItem<T>>, a, a.head_dim / 8, s);
+  }
+  return rope_launch(interleaved ? rope_pairs_kernel<T, true> : rope_pairs_kernel<T, false>, a,
+                     a.pairs + (rest + 1) / 2, s);
 }
 
 }  // namespace
@@ -208,34 +398,36 @@ extern "C" int mp_rope(void* q_out, const void* q, void* k_out, const void* k, c
                        int32_t index_type, void* stream) {
   using namespace mpk;
   RopeArgs a = {};
-  a.q = {q_out, q, q_out_token_stride, q_out_head_stride, q_token_stride, q_head_stride};
-  a.k = {k_out, k, k_out_token_stride, k_out_head_stride, k_token_stride, k_head_stride};
-  if (!type_ok(type) || !index_type_ok(index_type) || tokens < 0 || tokens > INT32_MAX || q_heads < 0 || q_heads > kMaxHeads ||
-      k_heads < 0 || k_heads > kMaxHeads || q_heads + k_heads == 0 || head_dim < 2 || head_dim > kMaxHeadDim ||
-      rotary_dim < 2 || rotary_dim > head_dim || rotary_dim % 2 || !std::isfinite(factor) ||
-      !side_ok(a.q, tokens, q_heads, head_dim) || !side_ok(a.k, tokens, k_heads, head_dim))
+  a.side[0] = {q_out, q, q_out_token_stride, q_out_head_stride, q_token_stride, q_head_stride};
+  a.side[1] = {k_out, k, k_out_token_stride, k_out_head_stride, k_token_stride, k_head_stride};
+  if (!type_ok(type) || !index_type_ok(index_type) || tokens < 0 || tokens > INT32_MAX || q_heads < 0 ||
+      q_heads > kMaxHeads || k_heads < 0 || k_heads > kMaxHeads || q_heads + k_heads == 0 || head_dim < 2 ||
+      head_dim > kMaxHeadDim || rotary_dim < 2 || rotary_dim > head_dim || rotary_dim % 2 || !std::isfinite(factor) ||
+      !side_ok(a.side[0], tokens, q_heads, head_dim) || !side_ok(a.side[1], tokens, k_heads, head_dim))
     return MP_ERR_RANGE;
   if (tokens == 0) return MP_OK;
   if (!turns || (q_heads && (!q_out || !q)) || (k_heads && (!k_out || !k))) return MP_ERR_NULL;
-  if (!side_alias_ok(a.q, tokens, q_heads) || !side_alias_ok(a.k, tokens, k_heads) || (q_heads && k_heads && q_out == k_out))
+  if (!side_alias_ok(a.side[0], tokens, q_heads) || !side_alias_ok(a.side[1], tokens, k_heads) ||
+      (q_heads && k_heads && q_out == k_out))
     return MP_ERR_RANGE;
-  if (!side_aligned(a.q, q_heads, type) || !side_aligned(a.k, k_heads, type) || !aligned_to(turns, 8) ||
+  if (!side_aligned(a.side[0], q_heads, type) || !side_aligned(a.side[1], k_heads, type) || !aligned_to(turns, 8) ||
       !index_aligned(positions, index_type))
     return MP_ERR_ALIGN;
+  a.heads[0] = q_heads;
+  a.heads[1] = k_heads;
   a.turns = turns;
   a.positions = positions;
   a.first = first_position;
   a.tokens = tokens;
-  a.q_heads = q_heads;
-  a.heads = q_heads + k_heads;
+  a.head_dim = head_dim;
   a.pairs = rotary_dim / 2;
   a.factor = factor;
   a.index_type = index_type;
   a.inverse = inverse != 0;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = type == MP_BF16   ? rope<MP_BF16>(a, head_dim, k_heads, interleaved != 0, s)
-                        : type == MP_FP16 ? rope<MP_FP16>(a, head_dim, k_heads, interleaved != 0, s)
-                                          : rope<MP_FP32>(a, head_dim, k_heads, interleaved != 0, s);
+  const cudaError_t e = type == MP_BF16   ? rope<MP_BF16>(a, interleaved != 0, s)
+                        : type == MP_FP16 ? rope<MP_FP16>(a, interleaved != 0, s)
+                                          : rope<MP_FP32>(a, interleaved != 0, s);
   return e == cudaSuccess ? MP_OK : record_cuda_error(e);
 }
 
