@@ -18,7 +18,8 @@ constexpr int64_t kStagedD = 8192; // longest row that a block's registers hold
 constexpr int kMaxThreads = 512;
 constexpr int kLongThreads = 512;
 constexpr int64_t kSms = 152;
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 4;       // of the forward pass's rings
+constexpr int kBackwardStages = 3;  // 8192 x 4096 bf16 47 us, with two 47 and with four 49
 constexpr uint32_t kSmShared = 227 * 1024;  // an SM's shared memory for blocks
 
 struct RmsArgs {
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(256) rms_forward_short_kernel(RmsArgs a) {
   for (; r - ahead < a.rows; r += step) {
     const bool live = r < a.rows;
     Pack8<T> u = xn.unit();
-    if (a.residual) put8(u, add8(get8(u), get8(rn.unit())));
+    if (a.residual) u = sum_of(u, rn.unit());
     fetch(r + step);
     const F8 f = get8(u);
     float2 s2 = make_float2(0.0f, 0.0f);
@@ -281,7 +282,14 @@ rms_forward_kernel(RmsArgs a, int G, uint32_t pitch, int stages) {
       p.load(xs, base, lane, d);
       if (has_res) q.load(rs, base, lane, d);
       u[v] = p.unit();
-      if (has_res) put8(u[v], add8(get8(u[v]), get8(q.unit())));
+      if (has_res) {
+        // the same sums; with four units a thread the widened ones ran faster (16384 x 4096 to
+        // 8 bits 75 us against 81), with two the others (8192 x 8192 81 against 85)
+        if (NV == 4)
+          put8(u[v], add8(get8(u[v]), get8(q.unit())));
+        else
+          u[v] = sum_of(u[v], q.unit());
+      }
       if (!ok) fill_nan(u[v]);
       const F8 f = get8(u[v]);
 #pragma unroll
@@ -585,6 +593,7 @@ rms_backward_kernel(RmsArgs a, float* part, int G, StageMap map, int stages) {
       Raw<T, Wide> y, h, g;
       Raw8<T, Wide> q;
       RawScales<T, Wide> b;
+      if (Wide && has_dh) g.load(gs, base, lane, d);  // the order of the loads that ran fastest, of either kind
       y.load(ys, base, lane, d);
       if constexpr (H8) {
         q.load(hs, base, lane, d);
@@ -592,7 +601,7 @@ rms_backward_kernel(RmsArgs a, float* part, int G, StageMap map, int stages) {
       } else {
         h.load(reinterpret_cast<const E*>(hs), base, lane, d);
       }
-      if (has_dh) g.load(gs, base, lane, d);
+      if (!Wide && has_dh) g.load(gs, base, lane, d);
       f[v] = get8(y.unit());
       if constexpr (H8)
         xh[v] = b.values(q.unit(), rstd);
@@ -723,9 +732,9 @@ __global__ void __launch_bounds__(kLongThreads) rms_dw_long_kernel(RmsArgs a, fl
   part[c * a.d + j] = s;
 }
 
-// dweight from `parts` blocks' sums: 32 columns a block, 16 threads a column, each
-// adding every 16th block's sum, ten of them on their way at a time.
-constexpr int kFinishSlices = 16, kFinishAhead = 10;
+// dweight from `parts` blocks' sums: 32 columns a block, 32 threads a column, each
+// adding every 32nd block's sum, five of them on their way at a time.
+constexpr int kFinishSlices = 32, kFinishAhead = 5;
 
 __global__ void __launch_bounds__(32 * kFinishSlices) rms_finish_kernel(void* dweight, const float* part, int64_t d,
                                                                         int parts, int weight_type) {
@@ -791,10 +800,13 @@ cudaError_t forward_wide(const RmsArgs& a, const DeviceInfo& dev, cudaStream_t s
   // Few rows: one or two units a thread, so that more warps share them.
   if (warps(1) <= kMaxThreads / 32 && a.rows * warps(2) < 8 * dev.sms) return forward_staged<T, Wide, 1>(a, warps(1), dev, s);
   if (a.rows * warps(4) < 8 * dev.sms || units <= 64) return forward_staged<T, Wide, 2>(a, warps(2), dev, s);
-  // Many: four, so that what a row costs each of its threads is shared by many elements. Rows
-  // off the grid: two, as four take more code than the instruction caches hold, unless
-  // they leave a block with few warps.
-  if (!Wide && busy(2) >= 12) return forward_staged<T, Wide, 2>(a, warps(2), dev, s);
+  // Many: four, so that what a row costs each of its threads is shared by many elements. Two
+  // for rows that fill the lanes so, with a residual and no second reduction or
+  // quantising of y (8192 x 4096 bf16 43 us, with four 48; but 32768 x 1600 76 against 68, without a
+  // residual 35 against 31, y in 8 bits 45 against 40). Rows off the grid: two, as four take more
+  // code than the instruction caches hold, unless they leave a block with few warps.
+  const bool full = units == 64 * warps(2) && a.residual && a.y && !a.y8;
+  if (Wide ? full : busy(2) >= 12) return forward_staged<T, Wide, 2>(a, warps(2), dev, s);
   return forward_staged<T, Wide, 4>(a, warps(4), dev, s);
 }
 
@@ -860,7 +872,7 @@ cudaError_t backward_staged(const RmsArgs& a, const BackwardPlan& p, float* part
   map.h_pitch = H8 ? pieces_pitch(a.d) : map.pitch;
   map.size = (a.residual ? 2 : 1) * map.pitch + map.h_pitch + (H8 ? pieces_pitch((a.d + 31) / 32) : 0);
   const uint32_t per_stage = p.groups * map.size;
-  const int stages = static_cast<int>(std::max(2u, std::min<uint32_t>(kMaxStages, (kSmShared - 4096) / per_stage)));
+  const int stages = static_cast<int>(std::max(2u, std::min<uint32_t>(kBackwardStages, (kSmShared - 4096) / per_stage)));
   const uint32_t threads = 32 * p.G * p.groups;
   const size_t smem = std::max<size_t>(static_cast<size_t>(stages) * per_stage, threads * 8 * NV * sizeof(float));
   return launch_pdl_smem(kernel, static_cast<unsigned>(p.parts), threads, smem, s, a, part, p.G, map, stages);

@@ -118,6 +118,29 @@ __device__ __forceinline__ void put8(Pack8<T>& u, const F8& a) {
   u.put(f);
 }
 
+// Sums rounded to the type. Of 16-bit types in one instruction a pair, whose single
+// rounding is that of the fp32 sum's: two of them whose sum lies on both sides of
+// a midpoint are less than 16 bits apart, and such a sum is exact in fp32.
+template <int T>
+__device__ __forceinline__ Pack8<T> sum_of(const Pack8<T>& a, const Pack8<T>& b) {
+  Pack8<T> r;
+  if constexpr (T == MP_FP32) {
+    put8(r, add8(get8(a), get8(b)));
+  } else {
+    const uint32_t x[4] = {a.v.x, a.v.y, a.v.z, a.v.w}, y[4] = {b.v.x, b.v.y, b.v.z, b.v.w};
+    uint32_t z[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (T == MP_BF16)
+        asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(z[i]) : "r"(x[i]), "r"(y[i]));
+      else
+        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(z[i]) : "r"(x[i]), "r"(y[i]));
+    }
+    r.v = make_uint4(z[0], z[1], z[2], z[3]);
+  }
+  return r;
+}
+
 // The largest of m and the magnitudes of a, NaN if one is NaN.
 __device__ __forceinline__ float amax2(float m, float2 a) {
   float r;
