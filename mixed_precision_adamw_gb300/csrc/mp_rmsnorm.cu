@@ -125,30 +125,47 @@ __device__ __forceinline__ void fill_nan(Pack8<T>& u) {
     u.fill(T == MP_BF16 ? 0x7FC0 : 0x7E00);
 }
 
+// Which of the optional inputs and outputs a call has. A few sets are template
+// arguments (Set, the bits below), so that a thread's units are one straight piece of
+// code whose instructions overlap; others ask at run time (Set = -1). Wide rows:
+// y or 8 bits alone (8192 x 4096 bf16, y: 23.5 us, asking 31). With a residual asking is
+// as fast or faster (8192 x 8192 81 us, 94 without), except off the grid (8192 x 4097: 72, 65 without).
+enum : int { kHasRes = 1, kHasH = 2, kHasY = 4, kHasRow8 = 8, kHasBlock8 = 16, kHasH8 = 32 };
+
+__host__ __device__ inline int set_of(const RmsArgs& a) {
+  return (a.residual ? kHasRes : 0) | (a.h ? kHasH : 0) | (a.y ? kHasY : 0) |
+         (!a.y8 ? 0 : a.y8_kind == MP_SCALE_ROW ? kHasRow8 : kHasBlock8) | (a.h8 ? kHasH8 : 0);
+}
+
+template <int Set>
+__device__ __forceinline__ bool has(int bit, int set) {
+  return (Set < 0 ? set : Set) & bit;
+}
+
 // A lane's outputs. All lanes of a warp call; where `live` is false nothing is
 // written. `inverse`: of the row's 8-bit scale.
-template <int T, bool Wide>
-__device__ __forceinline__ void put_unit(const RmsArgs& a, const Pack8<T>& u, const F8& w, float rstd, bool row8,
+template <int T, bool Wide, int Set>
+__device__ __forceinline__ void put_unit(const RmsArgs& a, int set, const Pack8<T>& u, const F8& w, float rstd,
                                          float inverse, int64_t r, int base, int l, int d, bool live) {
   using E = typename Elem<T>::type;
   const int64_t blocks = (d + 31) / 32;
   const F8 f = get8(u);
   float m[8 / kShare<T, Wide>];
-  if (a.h && live) store_unit<T, Wide>(u, static_cast<E*>(a.h) + r * a.h_stride, base, l, d);
-  if (a.h8) {
+  if (has<Set>(kHasH, set) && live) store_unit<T, Wide>(u, static_cast<E*>(a.h) + r * a.h_stride, base, l, d);
+  if (has<Set>(kHasH8, set)) {
     blocks_amax<T, Wide>(m, u);
     put_block8<T, T, Wide>(f, m, a.h8 + r * a.h8_stride, a.h8_scale + r * blocks, base, l, d, live);
   }
-  if (!a.y && !a.y8) return;
+  if (!has<Set>(kHasY | kHasRow8 | kHasBlock8, set)) return;
   const F8 y = mul8(mul8(f, rstd), w);
-  if (a.y && live) {
+  if (has<Set>(kHasY, set) && live) {
     Pack8<T> o;
     put8(o, y);
     store_unit<T, Wide>(o, static_cast<E*>(a.y) + r * a.y_stride, base, l, d);
   }
-  if (row8) {
+  if (has<Set>(kHasRow8, set)) {
     if (live) store_unit8<T, Wide>(e4m3_pack(mul8(y, inverse)), a.y8 + r * a.y8_stride, base, l, d);
-  } else if (a.y8) {
+  } else if (has<Set>(kHasBlock8, set)) {
     blocks_amax<T, Wide>(m, y);
     put_block8<T, MP_FP32, Wide>(y, m, a.y8 + r * a.y8_stride, static_cast<uint8_t*>(a.y8_scale) + r * blocks, base, l,
                                  d, live);
@@ -179,7 +196,8 @@ __global__ void __launch_bounds__(256) rms_forward_short_kernel(RmsArgs a) {
   const int t = threadIdx.x % L, d = static_cast<int>(a.d);
   const int64_t groups = 256 / L, step = gridDim.x * groups;
   const float inv_d = __fdiv_rn(1.0f, static_cast<float>(d));
-  const bool row8 = a.y8 && a.y8_kind == MP_SCALE_ROW;
+  const int set = set_of(a);
+  const bool row8 = set & kHasRow8;
   const F8 w = load_weights<T, Wide>(a, 0, t);
   Raw<T, Wide> xn, rn;
   auto fetch = [&](int64_t r) {
@@ -209,7 +227,7 @@ __global__ void __launch_bounds__(256) rms_forward_short_kernel(RmsArgs a) {
       for (int o = L / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(kAll, m, o));
     float inverse;
     const float rstd = row_results(a, s, m, inv_d, row8, r, t == 0 && live, inverse);
-    put_unit<T, Wide>(a, u, w, rstd, row8, inverse, r, 0, t, d, live);
+    put_unit<T, Wide, -1>(a, set, u, w, rstd, inverse, r, 0, t, d, live);
   }
 }
 
@@ -217,7 +235,7 @@ __global__ void __launch_bounds__(256) rms_forward_short_kernel(RmsArgs a) {
 // of staged rows of their own. A group's warps meet at a named barrier of their
 // own once a row, for its sum; by then they have read the stage, which is filled
 // again.
-template <int T, bool Wide, int NV>
+template <int T, bool Wide, int NV, int Set>
 __global__ void __launch_bounds__(kMaxThreads, 1)
 rms_forward_kernel(RmsArgs a, int G, uint32_t pitch, int stages) {
   pdl_enter();
@@ -227,7 +245,8 @@ rms_forward_kernel(RmsArgs a, int G, uint32_t pitch, int stages) {
   __shared__ unsigned long long full[kMaxThreads / 32 * kMaxStages];
   const int L = 32 * G, t = threadIdx.x % L, group = threadIdx.x / L, groups = blockDim.x / L;
   const int lane = t % 32, first_column = 8 * (t - lane), d = static_cast<int>(a.d), padded = (d + 255) / 256 * 256;
-  const bool has_res = a.residual;
+  const int set = set_of(a);
+  const bool has_res = has<Set>(kHasRes, set), row8 = has<Set>(kHasRow8, set);
   const uint32_t stage_bytes = has_res ? 2 * pitch : pitch;
   float* sw = reinterpret_cast<float*>(smem);
   uint8_t* ring = smem + 4 * padded + static_cast<size_t>(group) * stages * stage_bytes;
@@ -259,7 +278,6 @@ rms_forward_kernel(RmsArgs a, int G, uint32_t pitch, int stages) {
   stage_weights<Wide>(sw, a, padded, blockDim.x);
   __syncthreads();
   const float inv_d = __fdiv_rn(1.0f, static_cast<float>(d));
-  const bool row8 = a.y8 && a.y8_kind == MP_SCALE_ROW;
   bool ok = true;
   int stage = 0, parity = 0;
   uint32_t phase = 0;
@@ -320,8 +338,8 @@ rms_forward_kernel(RmsArgs a, int G, uint32_t pitch, int stages) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int base = first_column + 8 * v * L;
-      put_unit<T, Wide>(a, u[v], staged_weights<T, Wide>(sw, base, lane, padded), rstd, row8, inverse, r, base, lane, d,
-                        true);
+      put_unit<T, Wide, Set>(a, set, u[v], staged_weights<T, Wide>(sw, base, lane, padded), rstd, inverse, r, base, lane,
+                             d, true);
     }
     if (++stage == stages) {
       stage = 0;
@@ -775,10 +793,10 @@ cudaError_t forward_short(const RmsArgs& a, const DeviceInfo& dev, cudaStream_t 
   return launch_pdl(rms_forward_short_kernel<T, Wide, L>, static_cast<unsigned>(blocks), 256, s, a);
 }
 
-template <int T, bool Wide, int NV>
-cudaError_t forward_staged(const RmsArgs& a, int G, const DeviceInfo& dev, cudaStream_t s) {
+template <int T, bool Wide, int NV, int Set>
+cudaError_t forward_staged_set(const RmsArgs& a, int G, const DeviceInfo& dev, cudaStream_t s) {
   static std::atomic<bool> ready[64];
-  const cudaError_t e = allow_shared(rms_forward_kernel<T, Wide, NV>, kSmShared - 4096, ready);
+  const cudaError_t e = allow_shared(rms_forward_kernel<T, Wide, NV, Set>, kSmShared - 4096, ready);
   if (e != cudaSuccess) return e;
   const uint32_t pitch = pieces_pitch(a.d * (T == MP_FP32 ? 4 : 2)), row = (a.residual ? 2 : 1) * pitch;
   const uint32_t weights = static_cast<uint32_t>((a.d + 255) / 256 * 1024), room = kSmShared - 4096 - weights;
@@ -786,9 +804,20 @@ cudaError_t forward_staged(const RmsArgs& a, int G, const DeviceInfo& dev, cudaS
   const int groups = static_cast<int>(std::max<uint32_t>(1, std::min<uint32_t>(kMaxThreads / (32 * G), room / (2 * row))));
   const int stages = static_cast<int>(std::max<uint32_t>(2, std::min<uint32_t>(kMaxStages, room / (groups * row))));
   const int64_t blocks = std::min<int64_t>((a.rows + groups - 1) / groups, dev.sms);
-  return launch_pdl_smem(rms_forward_kernel<T, Wide, NV>, static_cast<unsigned>(blocks),
+  return launch_pdl_smem(rms_forward_kernel<T, Wide, NV, Set>, static_cast<unsigned>(blocks),
                          static_cast<unsigned>(32 * G * groups), weights + static_cast<size_t>(stages) * groups * row,
                          s, a, G, pitch, stages);
+}
+
+template <int T, bool Wide, int NV>
+cudaError_t forward_staged(const RmsArgs& a, int G, const DeviceInfo& dev, cudaStream_t s) {
+  if constexpr (NV > 1) {
+    constexpr int kOther = Wide ? kHasRow8 : kHasRes | kHasH | kHasY;
+    const int set = set_of(a);
+    if (set == kHasY) return forward_staged_set<T, Wide, NV, kHasY>(a, G, dev, s);
+    if (set == kOther) return forward_staged_set<T, Wide, NV, kOther>(a, G, dev, s);
+  }
+  return forward_staged_set<T, Wide, NV, -1>(a, G, dev, s);
 }
 
 template <int T, bool Wide>
@@ -809,7 +838,7 @@ cudaError_t forward_wide(const RmsArgs& a, const DeviceInfo& dev, cudaStream_t s
   // quantising of y (8192 x 4096 bf16 43 us, with four 48; but 32768 x 1600 76 against 68, without a
   // residual 35 against 31, y in 8 bits 45 against 40). Rows off the grid: two, as four take more
   // code than the instruction caches hold, unless they leave a block with few warps.
-  const bool full = units == 64 * warps(2) && a.residual && a.y && !a.y8;
+  const bool full = units == 64 * warps(2) && busy(2) >= 14 && a.residual && a.y && !a.y8;
   if (Wide ? full : busy(2) >= 12) return forward_staged<T, Wide, 2>(a, warps(2), dev, s);
   return forward_staged<T, Wide, 4>(a, warps(4), dev, s);
 }
