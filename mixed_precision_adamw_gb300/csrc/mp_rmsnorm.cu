@@ -40,6 +40,7 @@ struct RmsArgs {
   const void* dy;
   const void* weight;
   const float* rstd_in;
+  void* dweight;  // written by the one block that there is; nullptr: blocks' sums go to the workspace
   int64_t rows, d, y_stride, h_stride, y8_stride, h8_stride, x_stride, residual_stride, dy_stride;
   float eps;
   int weight_type;
@@ -512,7 +513,10 @@ __global__ void __launch_bounds__(kShortThreads<T, Wide>) rms_backward_short_ker
   for (int j = threadIdx.x; j < d; j += kThreads) {
     float s = 0.0f;
     for (int q = 0; q < kGroups; ++q) s = __fadd_rn(s, joined[q * 8 * L + j]);
-    part[static_cast<int64_t>(blockIdx.x) * d + j] = s;
+    if (a.dweight)
+      store_as(a.dweight, j, a.weight_type, s);
+    else
+      part[static_cast<int64_t>(blockIdx.x) * d + j] = s;
   }
 }
 
@@ -698,7 +702,10 @@ rms_backward_kernel(RmsArgs a, float* part, int G, StageMap map, int stages) {
   for (int j = threadIdx.x; j < d; j += blockDim.x) {
     float s = 0.0f;
     for (int q = 0; q < groups; ++q) s = __fadd_rn(s, joined[q * width + j]);
-    to[j] = s;
+    if (a.dweight)
+      store_as(a.dweight, j, a.weight_type, s);
+    else
+      to[j] = s;
   }
 }
 
@@ -889,7 +896,9 @@ BackwardPlan backward_plan(int64_t rows, int64_t d) {
     cap = kSms;
     per_block = p.groups;
   }
-  p.parts = static_cast<int>(std::max<int64_t>(1, std::min(cap, (rows + per_block - 1) / per_block)));
+  // Few rows: one block, which needs no second launch (1 x 4096 bf16 4.2 us instead of 5.9).
+  const bool one = d <= kStagedD && rows <= 2 * per_block;
+  p.parts = one ? 1 : static_cast<int>(std::max<int64_t>(1, std::min(cap, (rows + per_block - 1) / per_block)));
   return p;
 }
 
@@ -930,8 +939,10 @@ cudaError_t backward_wide(const RmsArgs& a, const BackwardPlan& p, float* part, 
 }
 
 template <int T, bool H8>
-cudaError_t backward(const RmsArgs& a, void* dweight, float* part, const DeviceInfo& dev, cudaStream_t s) {
+cudaError_t backward(RmsArgs a, void* dweight, float* part, const DeviceInfo& dev, cudaStream_t s) {
   const BackwardPlan p = backward_plan(a.rows, a.d);
+  const bool one = p.parts == 1 && a.d <= kStagedD;
+  if (one) a.dweight = dweight;
   cudaError_t e = cudaSuccess;
   if (a.d <= kStagedD) {
     const bool wide = wide_rows(a.dy, a.d, a.dy_stride, a.rows, T) &&
@@ -948,7 +959,7 @@ cudaError_t backward(const RmsArgs& a, void* dweight, float* part, const DeviceI
       e = launch_pdl(rms_dx_long_kernel<T, H8>, static_cast<unsigned>(std::min<int64_t>(a.rows, 4 * dev.sms)),
                      kLongThreads, s, a);
   }
-  if (e == cudaSuccess && dweight)
+  if (e == cudaSuccess && dweight && !one)
     e = launch_pdl(rms_finish_kernel, static_cast<unsigned>((a.d + 31) / 32), 32 * kFinishSlices, s, dweight,
                    static_cast<const float*>(part), a.d, p.parts, a.weight_type);
   return e;
