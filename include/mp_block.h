@@ -17,12 +17,16 @@
  *
  * An output may be the same matrix (address and stride) as an input of the same
  * element size where said; otherwise outputs overlap neither inputs nor one another.
+ * Rows are read in whole aligned pieces of up to 16 bytes, which may hold bytes
+ * beside them; those are not used.
+ * Waits inside a kernel (RMS norm's) end after a second at most. Should one run out
+ * (a fault of the GPU), every element that it touches is NaN.
  *
  * Rows in 8 bits: e4m3 values (1 sign, 4 exponent, 3 mantissa bits, bias 7, no
  * infinities, 448 the largest) and their scales, value = e4m3 * scale, as mp_scale8_t says:
- *  MP_SCALE_ROW    float[rows]: scale = max(amax / 448, 2^-126), amax the row's
- *                  largest magnitude. A row that holds NaN or an infinity has
- *                  scale NaN and reads back as NaN throughout.
+ *  MP_SCALE_ROW    float[rows]: scale = max(amax / 448, 2^-126) to a few roundings,
+ *                  amax the row's largest magnitude. A row that holds NaN or an
+ *                  infinity has scale NaN and reads back as NaN throughout.
  *  MP_SCALE_BLOCK  uint8[rows, ceil(d / 32)], contiguous: for every 32 columns
  *                  (the last block may be shorter) a power of two, held as its
  *                  exponent + 127: the least one with amax <= 448 * scale, or

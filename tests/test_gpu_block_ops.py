@@ -549,6 +549,105 @@ def test_rope_is_a_rotation(mp):  # noqa: F811
         assert ((lhs - rhs).abs() <= 20 * R.U * (pair.double() * (z.abs() + t.abs()).double()).sum((1, 2))).all()
 
 
+# --- each matrix on a place of its own, rows far apart -------------------------------------------
+
+def somewhere(t, k):
+    """A copy of a matrix at the k-th of several kinds of places; bytes for 8-bit rows."""
+    pad, off = ((0, 0), (8, 8), (1, 0), (3, 5), (16, 16), (2, 2), (0, 1))[k % 7]
+    return placed(t, pad, off)
+
+
+def like8(rows, d, k):
+    pad, off = ((0, 0), (8, 8), (1, 0), (3, 5), (16, 16), (2, 2), (0, 1))[k % 7]
+    return Guarded8(rows, d, pad, off)
+
+
+@pytest.mark.parametrize("dtype", [BF, FF])
+@pytest.mark.parametrize("d", [64, 200, 1360, 1365, 4096])
+@pytest.mark.parametrize("k", range(7))
+def test_unlike_places(mp, k, d, dtype):  # noqa: F811
+    g = gen(k)
+    rows = 11
+    vals = [randn((rows, d), g, 1.0, dtype) for _ in range(4)]
+    x, res, dy, dh = (somewhere(v, k + i) for i, v in enumerate(vals))
+    w = randn((d + 1,), g, 1.0, dtype)[k % 2:][:d]
+    h, y, rstd = somewhere(vals[0], k + 4), somewhere(vals[0], k + 5), f32(rows)
+    h8, y8, hs, ys = like8(rows, d, k + 6), like8(rows, d, k + 1), scales(rows, d, "block"), scales(rows, d, "row")
+    mp.mp_rmsnorm_forward(y, x, w, residual=res, h=h, rstd=rstd, y8=y8.view, y8_scale=ys, h8=h8.view, h8_scale=hs)
+    stored = (vals[0].float() + vals[1].float()).to(dtype)
+    (ry, rr), (ty, tr) = R.rms_forward(stored, w, 1e-5)
+    assert torch.equal(h, stored)
+    R.assert_within(y, ry, R.rounded(ry, ty, dtype), "y")
+    R.assert_within(rstd, rr, tr, "rstd")
+    R.check_row8(contiguous8(y8.view), ys, ry, ty, "y8")
+    R.check_block8(contiguous8(h8.view), hs, stored.double(), 0.0 * ry, dtype, "h8")
+    ws = torch.empty(mp.mp_rmsnorm_workspace_bytes(rows, d), dtype=torch.uint8, device="cuda")
+    for src, sc, hd in ((h, None, stored.double()), (h8.view, hs, R.unpack(contiguous8(h8.view), hs))):
+        dx, dw = somewhere(vals[0], k + 3), torch.empty_like(w)
+        mp.mp_rmsnorm_backward(dx, dw, dy, src, w, rstd, dh=dh, h_scale=sc, workspace=ws)
+        (rdx, rdw), (tdx, tdw) = R.rms_backward(vals[2], vals[3], hd, w, rstd)
+        R.assert_within(dx, rdx, R.rounded(rdx, tdx, dtype), "dx")
+        R.assert_within(dw, rdw, R.rounded(rdw, tdw, dtype), "dweight")
+    u8, us = like8(rows, d, k + 2), scales(rows, d, "block")
+    mp.mp_gated_forward(y, x, res, gate8=h8.view, gate8_scale=hs, up8=u8.view, up8_scale=us)
+    ref, tol = R.gated(None, vals[0].double(), vals[1].double(), "silu")
+    R.assert_within(y, ref["y"], R.rounded(ref["y"], tol["y"], dtype), "gated y")
+    for a, b, kw, ad, bd in ((x, res, {}, vals[0].double(), vals[1].double()),
+                             (h8.view, u8.view, dict(gate_scale=hs, up_scale=us),
+                              R.unpack(contiguous8(h8.view), hs), R.unpack(contiguous8(u8.view), us))):
+        da, db = somewhere(vals[0], k + 4), somewhere(vals[0], k + 6)
+        mp.mp_gated_backward(da, db, dy, a, b, y=y, **kw)
+        ref, tol = R.gated(vals[2], ad, bd, "silu")
+        for name, got in (("dgate", da), ("dup", db), ("y", y)):
+            R.assert_within(got, ref[name], R.rounded(ref[name], tol[name], dtype), name)
+    for o in (h8, y8, u8):
+        o.check("8 bits")
+
+
+@pytest.mark.parametrize("d", [1600, 1365])
+def test_rows_far_apart(mp, d):  # noqa: F811
+    # offsets of elements pass 2^31, of bytes 2^32
+    g = gen(20)
+    rows, stride = 5, (1 << 29) + 8 * (d % 2 == 0)
+    buf = torch.empty(rows * stride, dtype=BF, device="cuda")
+    out = torch.empty(rows * stride, dtype=BF, device="cuda")
+
+    def far(t):
+        return t.view(rows, stride)[:, :d]
+
+    x, y = far(buf), far(out)
+    x.copy_(randn((rows, d), g, 1.0, BF))
+    c, want, w = x.contiguous(), torch.empty(rows, d, dtype=BF, device="cuda"), randn((d,), g, 1.0, BF)
+    rstd, r2 = f32(rows), f32(rows)
+    mp.mp_rmsnorm_forward(y, x, w, rstd=rstd)
+    mp.mp_rmsnorm_forward(want, c, w, rstd=r2)
+    (ry, _), (ty, _) = R.rms_forward(c, w, 1e-5)
+    for got in (y, want):  # of other strides, of other variants: both right
+        R.assert_within(got, ry, R.rounded(ry, ty, BF), "y")
+    dx, dw = y, f32(d)
+    ws = torch.empty(mp.mp_rmsnorm_workspace_bytes(rows, d), dtype=torch.uint8, device="cuda")
+    mp.mp_rmsnorm_backward(dx, dw.to(BF), x, x, w, rstd, workspace=ws)
+    (rdx, _), (tdx, _) = R.rms_backward(c, None, c.double(), w, rstd)
+    R.assert_within(dx, rdx, R.rounded(rdx, tdx, BF), "dx")
+    mp.mp_gated_forward(y, x, x)
+    mp.mp_gated_forward(want, c, c)
+    assert torch.equal(y, want)
+    q, s = torch.empty(rows, d, dtype=E4, device="cuda"), scales(rows, d, "block")
+    mp.mp_pack8(q, s, x)
+    mp.mp_unpack8(y, q, s)
+    q2, s2 = torch.empty(rows, d, dtype=E4, device="cuda"), scales(rows, d, "block")
+    mp.mp_pack8(q2, s2, c)
+    mp.mp_unpack8(want, q2, s2)
+    assert torch.equal(y, want) and torch.equal(s, s2)
+    turns, _ = mp.mp_rope_frequencies(64)
+    n = d // 64
+    mp.mp_rope(y[:, :n * 64].unflatten(1, (n, 64)), x[:, :n * 64].unflatten(1, (n, 64)), None, None, turns,
+               first_position=7)
+    o = torch.empty(rows, n, 64, dtype=BF, device="cuda")
+    mp.mp_rope(o, c[:, :n * 64].reshape(rows, n, 64), None, None, turns, first_position=7)
+    assert torch.equal(y[:, :n * 64].unflatten(1, (n, 64)), o)
+
+
 # --- streams, graphs, two at once ---------------------------------------------------------------
 
 def test_on_another_stream(mp):  # noqa: F811
