@@ -330,8 +330,6 @@ Tiling tiling(int64_t d, int least) {
   return best;
 }
 
-inline int least_lanes(bool wide) { return wide ? 3 : 5; }
-
 template <int R, typename Args>
 cudaError_t launch_tiled(void (*kernel)(Args, Tiling), const Args& a, int least, cudaStream_t s) {
   const Tiling g = tiling(a.d, least);
@@ -350,21 +348,28 @@ cudaError_t launch_tiled(void (*kernel)(Args, Tiling), const Args& a, int least,
 }
 
 // Rows a thread: two for the activation, whose three and four streams take the
-// registers, four for the two streams of 8 bits.
+// registers, four for the two streams of 8 bits. A unit off the grid is loaded
+// as several words, which hold more registers until they are put together: its
+// backward pass takes one row (32768 x 2731 bf16 in 153 us instead of 185,
+// 1021 x 2731 fp16 in 5.7 instead of 6.3), its 8 bits two (unpacking 16384 x
+// 4097 into fp32 in 72 us instead of 98, packing 2047 x 1365 bf16 in 4.2
+// instead of 5.4, 16384 x 4097 in 62 instead of 60). The forward pass keeps two
+// there (94 us instead of 104), and on the grid one row costs every kernel of
+// many rows (the backward pass of 8192 x 14336 164 us, with one 208).
+constexpr int kRows = 2, kBackwardRowsOther = 1, kRows8 = 4, kRows8Other = 2;
+
 template <int T, int Act>
 cudaError_t gated_forward(const GatedArgs& a, cudaStream_t s) {
-  constexpr int R = 2;
   const bool wide = wide_rows(a.y, a.d, a.y_stride, a.rows, T) && wide_rows(a.gate, a.d, a.gate_stride, a.rows, T) &&
                     (!a.up || wide_rows(a.up, a.d, a.up_stride, a.rows, T)) &&
                     (!a.gate8 || wide_rows8(a.gate8, a.d, a.gate8_stride, a.rows)) &&
                     (!a.up8 || wide_rows8(a.up8, a.d, a.up8_stride, a.rows));
-  return launch_tiled<R>(wide ? gated_forward_kernel<T, true, Act, R> : gated_forward_kernel<T, false, Act, R>, a,
-                         least_lanes(wide), s);
+  return wide ? launch_tiled<kRows>(gated_forward_kernel<T, true, Act, kRows>, a, 3, s)
+              : launch_tiled<kRows>(gated_forward_kernel<T, false, Act, kRows>, a, 5, s);
 }
 
 template <int T, int Act>
 cudaError_t gated_backward(const GatedArgs& a, cudaStream_t s) {
-  constexpr int R = 2;
   const bool kept = a.gate_scale;
   const auto source = [&](const void* p, int64_t stride) {
     return !p || (kept ? wide_rows8(p, a.d, stride, a.rows) : wide_rows(p, a.d, stride, a.rows, T));
@@ -373,17 +378,18 @@ cudaError_t gated_backward(const GatedArgs& a, cudaStream_t s) {
                     source(a.up, a.up_stride) && (!a.dgate || wide_rows(a.dgate, a.d, a.dgate_stride, a.rows, T)) &&
                     (!a.dup || wide_rows(a.dup, a.d, a.dup_stride, a.rows, T)) &&
                     (!a.y || wide_rows(a.y, a.d, a.y_stride, a.rows, T));
-  const auto kernel = kept ? (wide ? gated_backward_kernel<T, true, true, Act, R> : gated_backward_kernel<T, false, true, Act, R>)
-                           : (wide ? gated_backward_kernel<T, true, false, Act, R> : gated_backward_kernel<T, false, false, Act, R>);
-  return launch_tiled<R>(kernel, a, least_lanes(wide), s);
+  if (kept)
+    return wide ? launch_tiled<kRows>(gated_backward_kernel<T, true, true, Act, kRows>, a, 3, s)
+                : launch_tiled<kBackwardRowsOther>(gated_backward_kernel<T, false, true, Act, kBackwardRowsOther>, a, 5, s);
+  return wide ? launch_tiled<kRows>(gated_backward_kernel<T, true, false, Act, kRows>, a, 3, s)
+              : launch_tiled<kBackwardRowsOther>(gated_backward_kernel<T, false, false, Act, kBackwardRowsOther>, a, 5, s);
 }
 
 template <int T>
 cudaError_t pack_blocks(const Rows8Args& a, cudaStream_t s) {
-  constexpr int R = 4;
   const bool wide = wide_rows(a.x_in, a.d, a.x_stride, a.rows, T) && wide_rows8(a.q, a.d, a.q_stride, a.rows);
-  return launch_tiled<R>(wide ? pack_blocks_kernel<T, true, R> : pack_blocks_kernel<T, false, R>, a,
-                         least_lanes(wide), s);
+  return wide ? launch_tiled<kRows8>(pack_blocks_kernel<T, true, kRows8>, a, 3, s)
+              : launch_tiled<kRows8Other>(pack_blocks_kernel<T, false, kRows8Other>, a, 5, s);
 }
 
 template <int T, bool Wide>
@@ -406,9 +412,9 @@ cudaError_t pack_rows(const Rows8Args& a, cudaStream_t s) {
 
 template <int T>
 cudaError_t unpack(const Rows8Args& a, cudaStream_t s) {
-  constexpr int R = 4;
   const bool wide = wide_rows(a.x, a.d, a.x_stride, a.rows, T) && wide_rows8(a.q_in, a.d, a.q_stride, a.rows);
-  return launch_tiled<R>(wide ? unpack_kernel<T, true, R> : unpack_kernel<T, false, R>, a, least_lanes(wide), s);
+  return wide ? launch_tiled<kRows8>(unpack_kernel<T, true, kRows8>, a, 3, s)
+              : launch_tiled<kRows8Other>(unpack_kernel<T, false, kRows8Other>, a, 5, s);
 }
 
 // Rows whose blocks a grid can count.
