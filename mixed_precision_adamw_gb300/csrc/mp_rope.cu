@@ -33,6 +33,7 @@ struct RopeArgs {
   int64_t first, tokens;
   int head_dim, pairs;   // pairs: rotary_dim / 2
   int items;             // of a head, each a lane's
+  int angles;            // in shared memory, of a token
   int tokens_per_block;
   uint32_t by_items, by_heads;  // multipliers of the divisions by items and by the number of heads
   float factor;
@@ -56,16 +57,23 @@ __device__ __forceinline__ float2 cos_sin(uint64_t turn) {
 }
 
 // The angles of `tokens` tokens from t0 on, in shared memory: (cos, sin) * factor,
-// [token][pair].
-__device__ __forceinline__ void make_angles(float2* angle, const RopeArgs& a, int64_t t0, int tokens) {
+// put(token's, pair, (cos, sin)).
+template <typename Put>
+__device__ __forceinline__ void make_angles(float2* angle, const RopeArgs& a, int64_t t0, int tokens, Put put) {
   for (int i = threadIdx.x; i < tokens * a.pairs; i += kRopeThreads) {
     const int token = i / a.pairs;
     const int64_t p = a.positions ? load_index(a.positions, t0 + token, a.index_type) : a.first + t0 + token;
     float2 cs = cos_sin(static_cast<uint64_t>(p) * a.turns[i - token * a.pairs]);
     if (a.inverse) cs.y = -cs.y;
-    angle[i] = make_float2(__fmul_rn(cs.x, a.factor), __fmul_rn(cs.y, a.factor));
+    put(angle + token * a.angles, i - token * a.pairs, make_float2(__fmul_rn(cs.x, a.factor), __fmul_rn(cs.y, a.factor)));
   }
 }
+
+// One for each pair.
+struct PairAngles {
+  static __host__ __device__ int angles(const RopeArgs& a) { return a.pairs; }
+  static __device__ __forceinline__ void put(const RopeArgs&, float2* angle, int pair, float2 w) { angle[pair] = w; }
+};
 
 // A pair's column rotated by (cos, sin): the first with its partner's sign turned.
 __device__ __forceinline__ float turned(float own, float other, float2 w) {
@@ -81,9 +89,10 @@ __device__ __forceinline__ void rotate(float& x, float& y, float2 w) {
 //
 // Half layout, whole vectors of pairs: two vectors, eight pairs (or of the copied columns).
 template <int T>
-struct HalfItem {
+struct HalfItem : PairAngles {
   using E = typename Elem<T>::type;
   static constexpr int kBlocks = T == MP_FP32 ? 6 : 8;  // of an SM
+  static constexpr int kRounds = T == MP_FP32 ? 2 : 4;  // of a block's threads
   Pack8<T> x, y;
 
   static __device__ __forceinline__ int rest(const RopeArgs& a) { return (a.head_dim - 2 * a.pairs) / 8; }
@@ -124,73 +133,112 @@ struct HalfItem {
   }
 };
 
+// The partners of columns c to c + 7, c a multiple of 8 below 2 h, h = pairs, in the
+// half layout: what lies h after the columns up to h and h before the others, cut out of
+// the 16-byte pieces that it is in. Only of columns on both sides of h are three
+// pieces needed: two after, and the head's first. A piece is of the head
+// altogether or not at all. Columns past the rotation get anything.
+template <int T>
+struct Partners {
+  uint4 lo, hi, first;
+
+  __device__ __forceinline__ void load(const RopeArgs& a, const uint16_t* head, int c) {
+    const int h = a.pairs, q = c < h ? c + h : c - h;
+    const uint4* base = reinterpret_cast<const uint4*>(head);
+    lo = base[q / 8];
+    hi = q % 8 && q / 8 + 1 < a.head_dim / 8 ? base[q / 8 + 1] : make_uint4(0u, 0u, 0u, 0u);
+    if (c < h && c + 8 > h) first = base[0];
+  }
+  __device__ __forceinline__ F8 get(const RopeArgs& a, int c) const {
+    const int h = a.pairs, m = h - c;
+    Pack8<T> y;
+    y.across(place(c < h ? c + h : c - h), lo, hi);
+    if (m > 0 && m < 8) {
+      Pack8<T> z;
+      z.across(place(8 - m), make_uint4(0u, 0u, 0u, 0u), first);
+      y.v = make_uint4(joined(y.v.x, z.v.x, m), joined(y.v.y, z.v.y, m - 2), joined(y.v.z, z.v.z, m - 4),
+                       joined(y.v.w, z.v.w, m - 6));
+    }
+    return get8(y);
+  }
+  // A column's place on the grid that the pieces lie on.
+  static __device__ __forceinline__ const uint16_t* place(int column) {
+    return reinterpret_cast<const uint16_t*>(static_cast<uintptr_t>(2 * column));
+  }
+  // The first m of a's two columns, the others of b.
+  static __device__ __forceinline__ uint32_t joined(uint32_t a, uint32_t b, int m) {
+    return m >= 2 ? a : m <= 0 ? b : __byte_perm(a, b, 0x7610);
+  }
+};
+
+template <>
+struct Partners<MP_FP32> {
+  float p[8];
+
+  __device__ __forceinline__ void load(const RopeArgs& a, const float* head, int c) {
+    const int h = a.pairs;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int k = c + e;
+      p[e] = k < 2 * h ? head[k < h ? k + h : k - h] : 0.0f;
+    }
+  }
+  __device__ __forceinline__ F8 get(const RopeArgs&, int) const {
+    F8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.p[i] = make_float2(p[2 * i], p[2 * i + 1]);
+    return r;
+  }
+};
+
 // Half layout, any number of pairs: eight columns, and their partners, which lie
-// off the grid: cut out of the two 16-byte pieces that they are in, or, of columns on
-// both sides of the middle or the end of the rotation and of fp32, one by one.
+// off the grid.
 template <int T>
 struct AnyHalfItem {
   using E = typename Elem<T>::type;
-  static constexpr int kBlocks = 5;
+  static constexpr int kBlocks = 5, kRounds = T == MP_FP32 ? 4 : 8;
   Pack8<T> x;
-  uint32_t p[8];
+  Partners<T> partners;
 
-  static __device__ __forceinline__ bool pieces(const RopeArgs& a, int c) {
-    return T != MP_FP32 && (c + 8 <= a.pairs || (c >= a.pairs && c + 8 <= 2 * a.pairs));
+  // One angle for each column, the sine with the sign that the partner has in its sum:
+  // (cos, cos, sin, sin) of two neighbours, those that the items have at one place
+  // side by side, for access without bank conflicts (16384 x 40 heads of 80, 50
+  // columns rotated, bf16: 71 us with the pairs' angles in a row, 56 this way; a pair at
+  // a time 139).
+  static __host__ __device__ int angles(const RopeArgs& a) { return a.head_dim; }
+  static __device__ __forceinline__ void put(const RopeArgs& a, float2* angle, int pair, float2 w) {
+    const auto at = [&](int c, float sine) {
+      float* p = reinterpret_cast<float*>(angle) + 4 * (c % 8 / 2 * a.items + c / 8) + c % 2;
+      p[0] = w.x;
+      p[2] = sine;
+    };
+    at(pair, -w.y);
+    at(pair + a.pairs, w.y);
   }
+
   __device__ __forceinline__ void load(const RopeArgs& a, const E* head, int item) {
-    const int c = 8 * item, h = a.pairs;
-    x.load(head + c);
-    if (c >= 2 * h) return;
-    if (pieces(a, c)) {
-      const E* q = head + (c < h ? c + h : c - h);
-      const uintptr_t at = reinterpret_cast<uintptr_t>(q);
-      const uint4* base = reinterpret_cast<const uint4*>(at - at % 16);
-      const uint4 lo = base[0];
-      p[0] = lo.x, p[1] = lo.y, p[2] = lo.z, p[3] = lo.w;
-      if (at % 16) {  // otherwise the second piece may be beyond the head
-        const uint4 hi = base[1];
-        p[4] = hi.x, p[5] = hi.y, p[6] = hi.z, p[7] = hi.w;
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int k = c + e;
-        p[e] = 0;
-        if (k < 2 * h) {
-          const E v = head[k < h ? k + h : k - h];
-          p[e] = T == MP_FP32 ? __float_as_uint(v) : static_cast<uint32_t>(v);
-        }
-      }
-    }
+    x.load(head + 8 * item);
+    if (8 * item < 2 * a.pairs) partners.load(a, head, 8 * item);
   }
-  // One path for all of a warp's lanes but for the partners' reading: the first half's, the
-  // second half's and the mixed units' code one after the other took 87 us where
-  // this takes 77 (16384 x 40 heads of 80, 50 columns rotated; a pair at a time 139).
   __device__ __forceinline__ void finish(const RopeArgs& a, E* head, const float2* cs, int item) {
-    const int c = 8 * item, h = a.pairs;
-    if (c < 2 * h) {
-      float f[8], g[8];
-      x.get(f);
+    const int c = 8 * item, n = 2 * a.pairs;
+    if (c < n) {
+      const F8 f = get8(x), g = partners.get(a, c);
+      const float4* w = reinterpret_cast<const float4*>(cs) + item;
+      F8 r;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 v = w[i * a.items];
+        const float2 t = fma2(g.p[i], make_float2(v.z, v.w), mul2(f.p[i], make_float2(v.x, v.y)));
+        r.p[i] = T != MP_FP32 || c + 2 * i < n ? t : f.p[i];
+      }
       if constexpr (T == MP_FP32) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = __uint_as_float(p[e]);
-      } else {
+        put8(x, r);
+      } else {  // what is past the rotation stays bit by bit
         Pack8<T> y;
-        if (pieces(a, c))
-          y.across(head + (c < h ? c + h : c - h), make_uint4(p[0], p[1], p[2], p[3]),
-                   make_uint4(p[4], p[5], p[6], p[7]));  // on the same place of the grid as in load()
-        else
-          y.v = make_uint4(p[0] | p[1] << 16, p[2] | p[3] << 16, p[4] | p[5] << 16, p[6] | p[7] << 16);
-        y.get(g);
+        put8(y, r);
+        x.v = make_uint4(y.v.x, c + 2 < n ? y.v.y : x.v.y, c + 4 < n ? y.v.z : x.v.z, c + 6 < n ? y.v.w : x.v.w);
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int k = c + e;
-        const bool first = k < h;
-        const float t = turned(f[e], first ? -g[e] : g[e], cs[first ? k : min(k - h, h - 1)]);
-        f[e] = k < 2 * h ? t : f[e];
-      }
-      x.put(f);
     }
     x.store(head + c);
   }
@@ -198,9 +246,9 @@ struct AnyHalfItem {
 
 // Interleaved: two vectors, four pairs each.
 template <int T>
-struct InterleavedItem {
+struct InterleavedItem : PairAngles {
   using E = typename Elem<T>::type;
-  static constexpr int kBlocks = T == MP_FP32 ? 6 : 8;
+  static constexpr int kBlocks = T == MP_FP32 ? 6 : 8, kRounds = 2;
   Pack8<T> x[2];
 
   static __device__ __forceinline__ bool second(const RopeArgs& a, int item) {
@@ -242,11 +290,11 @@ template <int T, typename Item>
 __global__ void __launch_bounds__(kRopeThreads, Item::kBlocks) rope_kernel(RopeArgs a) {
   pdl_enter();
   using S = typename Elem<T>::type;
-  extern __shared__ __align__(16) float2 angle[];  // [token of the block][pair]
+  extern __shared__ __align__(16) float2 angle[];  // [token of the block][angles]
   const int heads = a.heads[0] + a.heads[1];
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens_per_block;
   const int tokens = static_cast<int>(min(static_cast<int64_t>(a.tokens_per_block), a.tokens - t0));
-  make_angles(angle, a, t0, tokens);
+  make_angles(angle, a, t0, tokens, [&](float2* of, int pair, float2 w) { Item::put(a, of, pair, w); });
   __syncthreads();
   for (int n = threadIdx.x; n < tokens * heads * a.items; n += kRopeThreads) {
     const int row = divide(n, a.by_items), item = n - row * a.items;
@@ -257,7 +305,7 @@ __global__ void __launch_bounds__(kRopeThreads, Item::kBlocks) rope_kernel(RopeA
     const RopeSide& s = a.side[is_k];
     Item part;
     part.load(a, static_cast<const S*>(s.in) + (t0 + token) * s.in_token + head * s.in_head, item);
-    part.finish(a, static_cast<S*>(s.out) + (t0 + token) * s.out_token + head * s.out_head, angle + token * a.pairs,
+    part.finish(a, static_cast<S*>(s.out) + (t0 + token) * s.out_token + head * s.out_head, angle + token * a.angles,
                 item);
   }
 }
@@ -273,7 +321,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_pairs_kernel(RopeArgs a) {
   extern __shared__ __align__(16) float2 angle[];
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens_per_block;
   const int tokens = static_cast<int>(min(static_cast<int64_t>(a.tokens_per_block), a.tokens - t0));
-  make_angles(angle, a, t0, tokens);
+  make_angles(angle, a, t0, tokens, [&](float2* of, int pair, float2 w) { of[pair] = w; });
   __syncthreads();
   const int lanes = min(a.items, kRopeThreads), slots = kRopeThreads / lanes, slot = threadIdx.x / lanes;
   if (slot >= slots) return;
@@ -352,23 +400,38 @@ bool side_wide(const RopeSide& s, int64_t tokens, int heads, int32_t type) {
   return heads == 0 || (ok(s.out, s.out_token, s.out_head) && ok(s.in, s.in_token, s.in_head));
 }
 
-// Tokens of a block: several rounds of its threads, angles within 16 KB, fewer where
-// there are few tokens for all SMs.
-int tokens_of_block(const RopeArgs& a) {
-  const int64_t per_token = static_cast<int64_t>(a.heads[0] + a.heads[1]) * a.items;
+// Tokens of a block: `rounds` rounds of its threads, angles within 16 KB, and one
+// wave of blocks where there are few tokens (4097 x 40 heads of 128 bf16 in 16.5 us,
+// rounded down 17.7; 5110 x 2 heads of 96 in 3.1 instead of 3.7; 4097 x 24 of 64 fp32 in
+// 11.1 instead of 10.9).
+//
+// More rounds make the angles of more tokens at once and have fewer starts, fewer
+// overlap one block's angles with another's loads (us with 2 / 4 / 8 rounds, 16384 x 40
+// heads, 8192 of fp32): half layout bf16 128 54.6 / 53.2 / 54.3, 80 39.3 / 37.8 / 40.2,
+// fp32 128 52.0 / 57.1 / 63.0; interleaved bf16 128 51.4 / 52.5 / 54.8; 50 of 80 columns
+// bf16 62.9 / 58.5 / 55.8, 34 of 64 fp32 59.9 / 57.1 / 59.4.
+int tokens_of_block(const RopeArgs& a, int rounds) {
+  const int64_t per_token = static_cast<int64_t>(a.heads[0] + a.heads[1]) * a.items, wave = 8 * kRopeSms;
   return static_cast<int>(std::max<int64_t>(
-      1, std::min<int64_t>({(4 * kRopeThreads + per_token - 1) / per_token, 2048 / a.pairs, a.tokens / (8 * kRopeSms)})));
+      1, std::min<int64_t>({(rounds * kRopeThreads + per_token - 1) / per_token, 2048 / a.angles,
+                            (a.tokens + wave - 1) / wave})));
 }
 
-cudaError_t rope_launch(void (*kernel)(RopeArgs), RopeArgs& a, int items, cudaStream_t s) {
+cudaError_t rope_launch(void (*kernel)(RopeArgs), RopeArgs& a, int items, int angles, int rounds, cudaStream_t s) {
   a.items = items;
-  a.tokens_per_block = tokens_of_block(a);
-  // n < tokens heads items, below 1024 + heads items: n items < 2^32
+  a.angles = angles;
+  a.tokens_per_block = tokens_of_block(a, rounds);
+  // n < tokens heads items, below 2048 + heads items: n items < 2^32
   a.by_items = divisor(items);
   a.by_heads = divisor(a.heads[0] + a.heads[1]);
   const int64_t blocks = (a.tokens + a.tokens_per_block - 1) / a.tokens_per_block;
-  const size_t smem = static_cast<size_t>(a.tokens_per_block) * a.pairs * sizeof(float2);
+  const size_t smem = static_cast<size_t>(a.tokens_per_block) * a.angles * sizeof(float2);
   return launch_pdl_smem(kernel, static_cast<unsigned>(blocks), kRopeThreads, smem, s, a);
+}
+
+template <int T, typename Item>
+cudaError_t rope_items(RopeArgs& a, int items, cudaStream_t s) {
+  return rope_launch(rope_kernel<T, Item>, a, items, Item::angles(a), Item::kRounds, s);
 }
 
 template <int T>
@@ -377,13 +440,13 @@ cudaError_t rope(RopeArgs& a, bool interleaved, cudaStream_t s) {
   const bool over = (a.heads[0] && a.side[0].in == a.side[0].out) || (a.heads[1] && a.side[1].in == a.side[1].out);
   if (a.head_dim % 8 == 0 && side_wide(a.side[0], a.tokens, a.heads[0], T) &&
       side_wide(a.side[1], a.tokens, a.heads[1], T)) {
-    if (interleaved) return rope_launch(rope_kernel<T, InterleavedItem<T>>, a, (a.head_dim / 8 + 1) / 2, s);
-    if (a.pairs % 8 == 0) return rope_launch(rope_kernel<T, HalfItem<T>>, a, a.pairs / 8 + (rest / 8 + 1) / 2, s);
+    if (interleaved) return rope_items<T, InterleavedItem<T>>(a, (a.head_dim / 8 + 1) / 2, s);
+    if (a.pairs % 8 == 0) return rope_items<T, HalfItem<T>>(a, a.pairs / 8 + (rest / 8 + 1) / 2, s);
     // over its input a pair has to be one lane's
-    if (!over) return rope_launch(rope_kernel<T, AnyHalfItem<T>>, a, a.head_dim / 8, s);
+    if (!over) return rope_items<T, AnyHalfItem<T>>(a, a.head_dim / 8, s);
   }
   return rope_launch(interleaved ? rope_pairs_kernel<T, true> : rope_pairs_kernel<T, false>, a,
-                     a.pairs + (rest + 1) / 2, s);
+                     a.pairs + (rest + 1) / 2, a.pairs, 4, s);
 }
 
 }  // namespace

@@ -496,6 +496,45 @@ def test_rope_positions(mp, positions, far):  # noqa: F811
               scaling=mp.RopeScaling("ramp", 16.0))
 
 
+@pytest.mark.parametrize("dtype", [BF, HF, FF])
+@pytest.mark.parametrize("dim", [8, 16, 40])
+def test_rope_any_number_of_pairs(mp, dim, dtype):  # noqa: F811
+    for rot in range(2, dim + 1, 2):
+        rope_case(mp, 11, 3, 2, dim, rot, dtype, inverse=rot % 4 == 0)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FF])
+def test_rope_many_uneven_pairs(mp, dtype):  # noqa: F811
+    rope_case(mp, 5, 3, 1, 1024, 1022, dtype)
+    rope_case(mp, 2500, 5, 1, 80, 50, dtype)  # several tokens a block, the last one short
+    rope_case(mp, 2500, 1, 0, 24, 6, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FF])
+@pytest.mark.parametrize("rot", [2, 6, 14, 16, 18, 26, 30, 32])
+def test_rope_copied_columns_keep_their_bits(mp, rot, dtype):  # noqa: F811
+    """Whatever they hold, and none of it gets into the rotated ones."""
+    turns, _ = mp.mp_rope_frequencies(rot, 10000.0)
+    g = gen(rot)
+    x = randn((70, 3, 32), g, 1.0, dtype)
+    bits = x.view(torch.int32 if dtype == FF else torch.int16)
+    n = bits[..., rot:].shape
+    special = [0x7F800001, -0x00000001, -0x80000000, 0x7F800000, 0x00000001] if dtype == FF else \
+        [0x7F81, 0x7C01, -1, -0x8000, 0x7F80, 0x7C00, 1]
+    pick = torch.randint(0, len(special), n, generator=g, device=x.device)
+    bits[..., rot:] = torch.tensor(special, device=x.device, dtype=torch.int64).to(bits.dtype)[pick]
+    clean = x.clone()
+    clean[..., rot:] = 0
+    o, c = torch.empty_like(x), torch.empty_like(x)
+    mp.mp_rope(o, x, None, None, turns, first_position=3)
+    mp.mp_rope(c, clean, None, None, turns, first_position=3)
+    assert torch.equal(o.view(bits.dtype)[..., rot:], bits[..., rot:])
+    assert torch.equal(o[..., :rot], c[..., :rot])
+    keep = bits[..., rot:].clone()
+    mp.mp_rope(x, x, None, None, turns, first_position=3)
+    assert torch.equal(bits[..., rot:], keep) and torch.equal(x[..., :rot], c[..., :rot])
+
+
 def test_rope_far_positions(mp):  # noqa: F811
     # positions that 32 bits do not hold, and negative ones
     turns, _ = mp.mp_rope_frequencies(64, 10000.0)
