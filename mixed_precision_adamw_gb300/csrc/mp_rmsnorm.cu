@@ -904,7 +904,12 @@ cudaError_t forward_wide(const RmsArgs& a, const DeviceInfo& dev, cudaStream_t s
   // residual 35 against 31, y in 8 bits 45 against 40). Rows off the grid: two, as four take more
   // code than the instruction caches hold, unless they leave a block with few warps.
   const bool full = units == 64 * warps(2) && busy(2) >= 14 && a.residual && a.y && !a.y8;
-  if (Wide ? full : busy(2) >= 12) return forward_staged<T, Wide, 2>(a, warps(2), dev, s);
+  // With a residual also two for three warps a row (1025 to 1536 columns), where two
+  // warps with four would leave a quarter of their lanes or more without work (3789 x 1280 bf16 y 10.9 us
+  // instead of 13.5, 16384 x 1280 32.6 instead of 35.5, 16384 x 1536 to 8 bits 36.7 instead of 38.4; without a
+  // residual 19.8 against 18.0).
+  const bool three = warps(2) == 3 && a.residual;
+  if (Wide ? full || three : busy(2) >= 12) return forward_staged<T, Wide, 2>(a, warps(2), dev, s);
   return forward_staged<T, Wide, 4>(a, warps(4), dev, s);
 }
 
