@@ -14,7 +14,9 @@
 namespace mpk {
 namespace {
 
-constexpr int kThreadsG = 256;
+// 8192 x 14336 bf16, backward from 8 bits 142 us, with 256 threads 149; 1021 x 2731
+// fp16 5.6 and 6.0; packing 16384 x 4096 with 64 34.3 instead of 31.8.
+constexpr int kAcrossMost = 7, kThreadsG = 1 << kAcrossMost;
 
 struct GatedArgs {
   void* y;
@@ -135,7 +137,7 @@ __global__ void __launch_bounds__(kThreadsG) gated_forward_kernel(GatedArgs a, T
 
 // ---- backward ---------------------------------------------------------------------
 template <int T, bool Wide, bool Kept, int Act, int R>
-__global__ void __launch_bounds__(kThreadsG, Wide && T != MP_FP32 ? 4 : 0) gated_backward_kernel(GatedArgs a, Tiling g) {
+__global__ void __launch_bounds__(kThreadsG, Wide && T != MP_FP32 ? 7 : 0) gated_backward_kernel(GatedArgs a, Tiling g) {
   pdl_enter();
   using E = typename Elem<T>::type;
   const auto [r0, base, l, down] = place(g, R);
@@ -323,9 +325,9 @@ __global__ void __launch_bounds__(kThreadsG) unpack_kernel(Rows8Args a, Tiling g
 Tiling tiling(int64_t d, int least) {
   const int units = static_cast<int>((d + 31) / 32 * 4);
   Tiling best = {};
-  for (int across = 8; across >= least; --across) {
+  for (int across = kAcrossMost; across >= least; --across) {
     const int chunks = (units + (1 << across) - 1) >> across;
-    if (across == 8 || (chunks << across) < (best.chunks << best.across)) best = {across, chunks};
+    if (across == kAcrossMost || (chunks << across) < (best.chunks << best.across)) best = {across, chunks};
   }
   return best;
 }
@@ -355,7 +357,7 @@ cudaError_t launch_tiled(void (*kernel)(Args, Tiling), const Args& a, int least,
 // 4097 into fp32 in 72 us instead of 98, packing 2047 x 1365 bf16 in 4.2
 // instead of 5.4, 16384 x 4097 in 62 instead of 60). The forward pass keeps two
 // there (94 us instead of 104), and on the grid one row costs every kernel of
-// many rows (the backward pass of 8192 x 14336 164 us, with one 208).
+// many rows (the backward pass of 8192 x 14336 164 us, with one 208). (All with 256 threads.)
 constexpr int kRows = 2, kBackwardRowsOther = 1, kRows8 = 4, kRows8Other = 2;
 
 template <int T, int Act>
