@@ -687,6 +687,58 @@ def test_rows_far_apart(mp, d):  # noqa: F811
     assert torch.equal(y[:, :n * 64].unflatten(1, (n, 64)), o)
 
 
+@pytest.mark.parametrize("rows,d", [(4_500_011, 8), (1_200_013, 5), (70_001, 1100)])
+def test_many_rows(mp, rows, d):  # noqa: F811
+    """More strips of rows than one dimension of a grid counts: what calls of fewer rows give."""
+    g = gen(21)
+    part = 60_000  # rows of the calls to compare with
+    a, b, dy = (randn((rows, d), g, 1.0, BF) for _ in range(3))
+
+    def rows8():
+        return torch.zeros(rows, d, dtype=torch.uint8, device="cuda"), scales(rows, d, "block")
+
+    def calls(r, o):
+        mp.mp_gated_forward(o["y"][r], a[r], b[r], gate8=o["a8"][0][r], gate8_scale=o["a8"][1][r], up8=o["b8"][0][r],
+                            up8_scale=o["b8"][1][r])
+        mp.mp_gated_backward(o["da"][r], o["db"][r], dy[r], a[r], b[r])
+        mp.mp_gated_backward(o["ka"][r], o["kb"][r], dy[r], o["a8"][0][r], o["b8"][0][r], gate_scale=o["a8"][1][r],
+                             up_scale=o["b8"][1][r])
+        mp.mp_pack8(o["q"][0][r], o["q"][1][r], dy[r])
+        mp.mp_pack8(o["p"][r], o["s"][r], dy[r])
+        mp.mp_unpack8(o["x"][r], o["q"][0][r], o["q"][1][r])
+        mp.mp_rmsnorm_forward(o["n"][r], a[r], None, residual=b[r], h=o["h"][r], rstd=o["r"][r])
+        mp.mp_rmsnorm_backward(o["dx"][r], None, dy[r], o["h"][r], None, o["r"][r])
+
+    def outputs():
+        o = {k: torch.zeros_like(a) for k in ("y", "da", "db", "ka", "kb", "x", "n", "h", "dx")}
+        return {**o, "a8": rows8(), "b8": rows8(), "q": rows8(), "p": torch.zeros_like(a, dtype=torch.uint8),
+                "s": f32(rows), "r": f32(rows)}
+
+    whole, parts = outputs(), outputs()
+    calls(slice(0, rows), whole)
+    for i in range(0, rows, part):
+        calls(slice(i, min(i + part, rows)), parts)
+    for k in ("y", "da", "db", "ka", "kb", "x", "p", "s"):
+        assert torch.equal(whole[k], parts[k]), k
+    for k in ("a8", "b8", "q"):
+        assert torch.equal(whole[k][0], parts[k][0]) and torch.equal(whole[k][1], parts[k][1]), k
+    # another number of rows may be summed by another split of a row
+    (ry, rr), (ty, tr) = R.rms_forward(whole["h"][-999:], None, 1e-5)
+    R.assert_within(whole["n"][-999:], ry, R.rounded(ry, ty, BF), "n")
+    R.assert_within(whole["r"][-999:], rr, tr, "rstd")
+    (rdx, _), (tdx, _) = R.rms_backward(dy[-999:], None, whole["h"][-999:].double(), None, whole["r"][-999:])
+    R.assert_within(whole["dx"][-999:], rdx, R.rounded(rdx, tdx, BF), "dx")
+    if d > 1024:  # longer than a head may be
+        return
+    turns, _ = mp.mp_rope_frequencies(d // 2 * 2)
+    o, c, x = (t.view(rows, 1, d) for t in (torch.zeros_like(a), torch.zeros_like(a), a))
+    mp.mp_rope(o, x, None, None, turns, first_position=5)
+    for i in range(0, rows, part):
+        r = slice(i, min(i + part, rows))
+        mp.mp_rope(c[r], x[r], None, None, turns, first_position=5 + i)
+    assert torch.equal(o, c)
+
+
 # --- streams, graphs, two at once ---------------------------------------------------------------
 
 def test_on_another_stream(mp):  # noqa: F811
