@@ -264,12 +264,26 @@ struct InterleavedItem : PairAngles {
       const int j = item + k * a.items;
       if (k && !second(a, item)) break;
       if (4 * j < a.pairs) {
-        float f[8];
-        x[k].get(f);
+        if constexpr (T == MP_FP32) {
+          float f[8];
+          x[k].get(f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (4 * j + i < a.pairs) rotate(f[2 * i], f[2 * i + 1], cs[4 * j + i]);
-        x[k].put(f);
+          for (int i = 0; i < 4; ++i)
+            if (4 * j + i < a.pairs) rotate(f[2 * i], f[2 * i + 1], cs[4 * j + i]);
+          x[k].put(f);
+        } else {  // a pair a word; what is past the rotation stays bit by bit
+          const int most = min(a.pairs - 4 * j, 4);
+          const float2* c = cs + 4 * j;
+          uint32_t w[4] = {x[k].v.x, x[k].v.y, x[k].v.z, x[k].v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < most) {
+              float f = Elem<T>::get(static_cast<uint16_t>(w[i])), g = Elem<T>::get(static_cast<uint16_t>(w[i] >> 16));
+              rotate(f, g, c[i]);
+              w[i] = T == MP_BF16 ? pack2_bf16(f, g) : pack2_fp16(f, g);
+            }
+          x[k].v = make_uint4(w[0], w[1], w[2], w[3]);
+        }
       }
       x[k].store(head + 8 * j);
     }
