@@ -131,8 +131,8 @@ int mp_rmsnorm_backward(void* dx, void* dweight, const void* dy, const void* dh,
  *
  *   q_out, q    [tokens, q_heads, head_dim] of `type`: token and head distances
  *               given, a head's values contiguous. q_out may be q itself (same
- *               distances).
- *   k_out, k    the same with k_heads; unused when k_heads is 0.
+ *               distances), not k.
+ *   k_out, k    the same with k_heads; unused when k_heads is 0. k_out is not q.
  *   turns       uint64[rotary_dim / 2], 8-B aligned, on the device.
  *   positions   [tokens] of `index_type`, any value (negative ones turn
  *               backwards); NULL: first_position + t.

@@ -485,7 +485,7 @@ extern "C" int mp_rope(void* q_out, const void* q, void* k_out, const void* k, c
   if (tokens == 0) return MP_OK;
   if (!turns || (q_heads && (!q_out || !q)) || (k_heads && (!k_out || !k))) return MP_ERR_NULL;
   if (!side_alias_ok(a.side[0], tokens, q_heads) || !side_alias_ok(a.side[1], tokens, k_heads) ||
-      (q_heads && k_heads && q_out == k_out))
+      (q_heads && k_heads && (q_out == k_out || q_out == k || k_out == q)))
     return MP_ERR_RANGE;
   if (!side_aligned(a.side[0], q_heads, type) || !side_aligned(a.side[1], k_heads, type) || !aligned_to(turns, 8) ||
       !index_aligned(positions, index_type))

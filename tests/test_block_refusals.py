@@ -1,0 +1,15 @@
+"""Calls of a block's operators that are refused although each argument alone is
+right: a buffer that is given for two things (no GPU needed: refused before any
+device work)."""
+import pytest
+
+from test_block_args import RO
+from test_train_args import FAKE, call, mp  # noqa: F401
+
+
+@pytest.mark.parametrize("kw", [dict(q_out=4 * FAKE), dict(k_out=2 * FAKE), dict(q_out=4 * FAKE, k_out=2 * FAKE)])
+def test_rope_over_the_other_input(mp, kw):  # noqa: F811
+    # whose heads other blocks have yet to read
+    assert call(mp, "mp_rope", list(RO), RO, **kw) == mp.MP_ERR_RANGE
+    no_keys = {**RO, "k_heads": 0, "k_out": None}  # then nobody reads them
+    assert call(mp, "mp_rope", list(RO), no_keys, q_out=4 * FAKE, turns=None) == mp.MP_ERR_NULL
