@@ -444,6 +444,7 @@ extern "C" int mp_gated_forward(void* y, void* gate8, void* gate8_scale, void* u
       (up8 && (up8 == y || up8 == gate || up8 == up)))
     return MP_ERR_RANGE;
   if (!type_aligned(y, type) || !type_aligned(gate, type) || !type_aligned(up, type)) return MP_ERR_ALIGN;
+  if (gate8 && up8 && gate8_scale == up8_scale) return MP_ERR_RANGE;
   GatedArgs a = {};
   a.y = y;
   a.gate = gate;

@@ -1055,6 +1055,7 @@ extern "C" int mp_rmsnorm_forward(void* y, void* h, float* rstd, void* y8, void*
   if (!type_aligned(y, type) || !type_aligned(h, type) || !type_aligned(x, type) || !type_aligned(residual, type) ||
       !type_aligned(weight, weight_type) || !aligned4(rstd) || (y8 && !scale8_aligned(y8_scale, y8_kind)))
     return MP_ERR_ALIGN;
+  if (y8 && h8 && y8_scale == h8_scale) return MP_ERR_RANGE;
   DeviceInfo dev;
   cudaError_t e = device_info(&dev);
   if (e != cudaSuccess) return record_cuda_error(e);

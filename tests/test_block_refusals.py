@@ -3,7 +3,7 @@ right: a buffer that is given for two things (no GPU needed: refused before any
 device work)."""
 import pytest
 
-from test_block_args import RO
+from test_block_args import GF, RF, RO
 from test_train_args import FAKE, call, mp  # noqa: F401
 
 
@@ -13,3 +13,12 @@ def test_rope_over_the_other_input(mp, kw):  # noqa: F811
     assert call(mp, "mp_rope", list(RO), RO, **kw) == mp.MP_ERR_RANGE
     no_keys = {**RO, "k_heads": 0, "k_out": None}  # then nobody reads them
     assert call(mp, "mp_rope", list(RO), no_keys, q_out=4 * FAKE, turns=None) == mp.MP_ERR_NULL
+
+
+@pytest.mark.parametrize("name,base,kw", [
+    ("mp_rmsnorm_forward", RF, dict(y8_scale=2 * FAKE, h8_scale=2 * FAKE)),
+    ("mp_rmsnorm_forward", RF, dict(y8_scale=2 * FAKE, h8_scale=2 * FAKE, y8_kind=2)),
+    ("mp_gated_forward", GF, dict(gate8_scale=6 * FAKE, up8_scale=6 * FAKE)),
+])
+def test_one_buffer_for_both_scales(mp, name, base, kw):  # noqa: F811
+    assert call(mp, name, list(base), base, **kw) == mp.MP_ERR_RANGE
