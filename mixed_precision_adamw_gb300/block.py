@@ -194,7 +194,8 @@ def mp_rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optiona
                         device=None) -> Tuple[torch.Tensor, float]:
     """(turns, factor) for mp_rope: int64 [rotary_dim / 2], each frequency as a
     64-bit fraction of a turn, copied to `device` (the current CUDA device unless given)."""
-    turns = torch.empty(max(0, rotary_dim) // 2, dtype=torch.int64)
+    rotary_dim = max(0, min(rotary_dim, 1 << 20))  # within 32 bits; longer than a head may be: refused below
+    turns = torch.empty(rotary_dim // 2, dtype=torch.int64)
     factor = ctypes.c_float()
     _check(_lib.mp_rope_frequencies(turns.data_ptr(), ctypes.byref(factor), rotary_dim, base,
                                     None if scaling is None else ctypes.byref(scaling._s)), "mp_rope_frequencies")

@@ -1,6 +1,6 @@
 """Calls of a block's operators that are refused although each argument alone is
-right: a buffer that is given for two things (no GPU needed: refused before any
-device work)."""
+right: a buffer that is given for two things; and a size beyond 32 bits (no GPU
+needed: refused before any device work)."""
 import pytest
 
 from test_block_args import GF, RF, RO
@@ -22,3 +22,10 @@ def test_rope_over_the_other_input(mp, kw):  # noqa: F811
 ])
 def test_one_buffer_for_both_scales(mp, name, base, kw):  # noqa: F811
     assert call(mp, name, list(base), base, **kw) == mp.MP_ERR_RANGE
+
+
+@pytest.mark.parametrize("rotary_dim", [(1 << 32) + 64, 1 << 40, 1 << 70, -(1 << 32) + 64])
+def test_rotary_dim_beyond_32_bits(mp, rotary_dim):  # noqa: F811
+    with pytest.raises(mp.MpError) as e:
+        mp.mp_rope_frequencies(rotary_dim, device="cpu")
+    assert e.value.status == mp.MP_ERR_RANGE
