@@ -1,6 +1,7 @@
 """mixed_precision_adamw_gb300 — Python binding of libmpadamw.so.
 
-A thin ctypes layer over the C ABI in include/mp_adamw.h: it checks tensor
+A thin layer over the C ABI in include/ (ctypes; ordinary calls of mp_block.h
+through a small CPython extension where it was built): it checks tensor
 dtypes, devices and sizes, passes raw device pointers and the current CUDA
 stream, and raises MpError on a non-OK status. Every step of the optimizer
 runs in the library's CUDA kernels; there is no fallback of any kind, and

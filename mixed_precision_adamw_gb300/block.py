@@ -11,11 +11,12 @@ contiguous float32 [rows], or uint8 [rows, ceil(d / 32)] of exponents + 127.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 from typing import Optional, Tuple
 
 import torch
 
-from . import _binding, _check, _lib, _raw_stream, _stream
+from . import _check, _lib, _raw_stream, _stream
 from .train import MP_FP32, MP_INT64, _F32, _INDEX_TYPES, _TYPES, _U8, _index_type, _matrix, _on, _rows, _vector, _weight_type
 
 MP_SCALE_ROW, MP_SCALE_BLOCK = 1, 2
@@ -62,9 +63,21 @@ def _current_stream(device: int) -> int:
 
 _current_stream = _raw_stream or _current_stream  # without a Stream object, where PyTorch can
 
+
+class _NoBinding:
+    """In place of _binding where it was not built (or by another Python): makes no call."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 # _binding makes the ordinary calls (each function below begins with it) and
 # returns None for all others: those go through the checks here, which name
 # what is wrong.
+if importlib.util.find_spec("._binding", __package__) is None:
+    _binding = _NoBinding()
+else:
+    from . import _binding
 _binding.bind(torch.Tensor, torch.nn.Parameter,
               (torch.bfloat16, torch.float16, torch.float32, torch.uint8, torch.float8_e4m3fn, torch.int32,
                torch.int64), _device, _current_stream,

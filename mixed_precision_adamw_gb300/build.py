@@ -1,5 +1,5 @@
-"""Build libmpadamw.so in-tree with nvcc for GB300 (sm_103a), and _binding.so, a
-CPython extension, with gcc.
+"""Build libmpadamw.so in-tree with nvcc for GB300 (sm_103a), and _binding, a
+CPython extension, with gcc where that and Python's headers are there.
 
 Each .cu translation unit is compiled in parallel, then linked into one
 shared library (CUDA runtime linked statically, so the library needs only the
@@ -20,8 +20,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmpadamw.so")
-# the ordinary calls of include/mp_block.h from Python without ctypes
-BINDING = os.path.join(PKG, "_binding.so")
+# The ordinary calls of include/mp_block.h from Python without ctypes. The name has
+# the interpreter's tag, so that no other Python takes it for its own.
+BINDING = os.path.join(PKG, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 # compute-free stream probes, a separate library that only the benchmark loads
 PROBE_LIB = os.path.join(PKG, "libmpprobe.so")
 
@@ -53,11 +54,14 @@ def _inputs():
 
 
 def is_stale() -> bool:
-    built = (LIB, PROBE_LIB, BINDING)
+    built = [LIB, PROBE_LIB] + ([BINDING] if _binding_needs() is None else [])
     if not all(os.path.exists(f) for f in built):
         return True
-    t = min(os.path.getmtime(f) for f in built)
-    return any(os.path.getmtime(f) > t for f in _inputs())
+    return any(_outdated(f) for f in built)
+
+
+def _outdated(built: str) -> bool:
+    return any(os.path.getmtime(f) > os.path.getmtime(built) for f in _inputs())
 
 
 def _compile(src: str, extra) -> str:
@@ -86,12 +90,27 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     return LIB
 
 
+def _cc():
+    return shutil.which("gcc") or shutil.which("cc")
+
+
+def _binding_needs():
+    """What keeps _binding from being built; None if nothing does."""
+    include = sysconfig.get_paths()["include"]
+    if _cc() is None:
+        return "a C compiler"
+    return None if os.path.exists(os.path.join(include, "Python.h")) else f"{include}/Python.h"
+
+
 def _binding():
-    cc = shutil.which("gcc") or shutil.which("cc")
-    if cc is None:
-        raise RuntimeError("gcc not found: it is required to build _binding.so")
+    needs = _binding_needs()
+    if needs is not None:  # the package works without it, through ctypes
+        sys.stderr.write(f"_binding not built: {needs} not found; small calls of mp_block.h cost twice as much\n")
+        if os.path.exists(BINDING) and _outdated(BINDING):
+            os.remove(BINDING)
+        return
     tmp = BINDING + f".tmp{os.getpid()}"
-    cmd = [cc, "-O2", "-std=c11", "-Wall", "-Wextra", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"],
+    cmd = [_cc(), "-O2", "-std=c11", "-Wall", "-Wextra", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"],
            "-I", INCLUDE, os.path.join(CSRC, "mp_binding.c"), "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -99,6 +118,9 @@ def _binding():
     if r.stderr.strip():
         sys.stderr.write(r.stderr)
     os.replace(tmp, BINDING)
+    untagged = os.path.join(PKG, "_binding.so")  # an earlier build's, which any Python would take
+    if os.path.exists(untagged) and untagged != BINDING:
+        os.remove(untagged)
 
 
 def _link(objs, out):
