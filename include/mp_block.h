@@ -24,8 +24,10 @@
  *
  * Rows in 8 bits: e4m3 values (1 sign, 4 exponent, 3 mantissa bits, bias 7, no
  * infinities, 448 the largest) and their scales, value = e4m3 * scale, as mp_scale8_t says:
- *  MP_SCALE_ROW    float[rows]: scale = max(amax / 448, 2^-126) to a few roundings,
- *                  amax the row's largest magnitude. A row that holds NaN or an
+ *  MP_SCALE_ROW    float[rows]: scale = max(amax / 448, 2^-126), amax the row's
+ *                  largest magnitude; it and the quotients by it to a few fp32
+ *                  roundings, so that a quotient next to the middle of two
+ *                  e4m3 values may become either. A row that holds NaN or an
  *                  infinity has scale NaN and reads back as NaN throughout.
  *  MP_SCALE_BLOCK  uint8[rows, ceil(d / 32)], contiguous: for every 32 columns
  *                  (the last block may be shorter) a power of two, held as its
@@ -33,7 +35,8 @@
  *                  2^-127. 255 is NaN, as for a row. (In blocks whose largest
  *                  magnitude is above 1.75 times the largest power of two of
  *                  the element type, magnitudes are limited to 240 * scale, so that nothing
- *                  reads back above the type's range.)
+ *                  reads back above the type's range. For y8, made from fp32 values, that
+ *                  type is fp32.)
  */
 #ifndef MP_BLOCK_H
 #define MP_BLOCK_H
@@ -71,7 +74,10 @@ typedef enum mp_scale8 {
  *   x, residual [rows, d] of `type`; residual NULL: none.
  *   weight      [d] of `weight_type`; NULL: ones.
  *   rows >= 0 (0 is a no-op), d in [1, 2^24], eps finite and >= 0.
- * The sum of squares is fp32: a row whose sum is above 3.4e38 has rstd 0.
+ * The sum of squares is fp32: a row whose sum is above 3.4e38 has rstd 0, and
+ * squares below 2^-150 add nothing (with eps = 0 a row of such values, zeros among
+ * them, has rstd infinity). For MP_SCALE_ROW the largest |h * weight| is taken
+ * before it is multiplied by rstd: above 3.4e38 it makes the row NaN.
  * Errors: MP_ERR_NULL (also when no output is given), MP_ERR_ALIGN,
  *         MP_ERR_RANGE, MP_ERR_CUDA.
  * ------------------------------------------------------------------------- */
@@ -188,7 +194,8 @@ int mp_rope_frequencies(uint64_t* turns, float* factor, int32_t rotary_dim, doub
  *   gate8, up8  [rows, d], gate and up in 8 bits with gate8_scale and up8_scale
  *               of kind MP_SCALE_BLOCK, for the backward pass; NULL: not wanted.
  *   rows in [0, 2^31 - 1] (0 is a no-op), d in [1, 2^24].
- * A gate of -inf gives NaN.
+ * (GELU in its form with tanh, which is up to 5e-4 from the one with erf.) A gate
+ * of -inf gives NaN. The factor of a in act, in both passes, is 0 where it would be below 2^-126.
  * Errors: MP_ERR_NULL, MP_ERR_ALIGN, MP_ERR_RANGE, MP_ERR_CUDA.
  * ------------------------------------------------------------------------- */
 typedef enum mp_activation {

@@ -305,7 +305,8 @@ def mp_gated_forward(y: torch.Tensor, gate: torch.Tensor, up: Optional[torch.Ten
                      up8_scale: Optional[torch.Tensor] = None, stream=None) -> None:
     """Enqueue y = act(gate) * up (act(gate) without up), and gate and up in 8
     bits (scales of 32 columns) for the backward pass if wanted. y may be gate
-    or up itself."""
+    or up itself. activation: "silu", or "gelu", which is its form with tanh
+    (PyTorch's approximate="tanh")."""
     act = _activation(activation)
     st = _binding.gated_forward(y, gate, up, act, gate8, gate8_scale, up8, up8_scale, stream)
     if st is None:

@@ -350,14 +350,15 @@ cudaError_t launch_tiled(void (*kernel)(Args, Tiling), const Args& a, int least,
 }
 
 // Rows a thread: two for the activation, whose three and four streams take the
-// registers, four for the two streams of 8 bits. A unit off the grid is loaded
+// registers, four for the two streams of 8 bits. On the grid fewer cost every
+// kernel of many rows (the backward pass of 8192 x 14336 bf16 162 us, with one row
+// 190; packing 16384 x 4096 31.7, with two 34.5). A unit off the grid is loaded
 // as several words, which hold more registers until they are put together: its
-// backward pass takes one row (32768 x 2731 bf16 in 153 us instead of 185,
-// 1021 x 2731 fp16 in 5.7 instead of 6.3), its 8 bits two (unpacking 16384 x
-// 4097 into fp32 in 72 us instead of 98, packing 2047 x 1365 bf16 in 4.2
-// instead of 5.4, 16384 x 4097 in 62 instead of 60). The forward pass keeps two
-// there (94 us instead of 104), and on the grid one row costs every kernel of
-// many rows (the backward pass of 8192 x 14336 164 us, with one 208). (All with 256 threads.)
+// backward pass takes one row (32768 x 2731 bf16 in 151 us instead of 162 with two,
+// 1021 x 2731 fp16 in 5.6 instead of 6.2), its 8 bits two (unpacking 16384 x
+// 4097 into fp32 in 71 us instead of 77 with four, packing 2047 x 1365 bf16 in 4.2
+// instead of 5.8, though 16384 x 4097 in 61 instead of 59; with one 72). The forward
+// pass keeps two there (32768 x 2731 in 91 us instead of 98 with one).
 constexpr int kRows = 2, kBackwardRowsOther = 1, kRows8 = 4, kRows8Other = 2;
 
 template <int T, int Act>

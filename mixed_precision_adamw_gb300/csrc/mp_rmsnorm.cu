@@ -1,10 +1,11 @@
 // mp_rmsnorm.cu — RMS norm with the residual's addition, forward and backward,
 // with outputs and kept activations in 8 bits.
 //
-// A row is read once and stays in registers from the sum of its squares to its
-// outputs. All sums are fp32. Everything is bound by HBM: 8 B an element forward
-// with a residual and 16-bit types (7 with the output in 8 bits), 8 B backward
-// (7 with h kept in 8 bits).
+// A row of up to 8192 columns is read once and stays in registers from the sum of
+// its squares to its outputs; longer ones are read twice, backward with the weight
+// gradient three times. All sums are fp32. HBM is the bound: 8 B an element
+// forward with a residual and 16-bit types (7 with the output in 8 bits, 9 with h kept in
+// 8 bits as well), 8 B backward (7 with h kept in 8 bits).
 #include "mp_device.cuh"
 #include "mp_internal.h"
 #include "mp_tma.cuh"
@@ -133,8 +134,8 @@ __device__ __forceinline__ void fill_nan(Pack8<T>& u) {
 // as fast or faster (8192 x 8192 81 us, 94 without), except off the grid (8192 x 4097: 72, 65 without).
 //
 // Of wide rows with scales of 32 columns (kSetBlocks) a thread's four units go through
-// each output together (put_units): 16384 x 4096 bf16 with y and h in 8 bits 10 us less than
-// asking for each unit, 3789 x 1280 with h in 8 bits 15.5 us instead of 16.5. Without
+// each output together (put_units): 16384 x 4096 bf16 with y and h in 8 bits (88 to 90 us) 10 us less
+// than asking for each unit, 3789 x 1280 with h in 8 bits, when it took four, 15.5 us instead of 16.5. Without
 // such scales that measured slower (8192 x 8192 y 86 us, for each unit 82).
 constexpr int kSetBlocks = -2;
 enum : int { kHasRes = 1, kHasH = 2, kHasY = 4, kHasRow8 = 8, kHasBlock8 = 16, kHasH8 = 32 };
@@ -905,9 +906,9 @@ cudaError_t forward_wide(const RmsArgs& a, const DeviceInfo& dev, cudaStream_t s
   // code than the instruction caches hold, unless they leave a block with few warps.
   const bool full = units == 64 * warps(2) && busy(2) >= 14 && a.residual && a.y && !a.y8;
   // With a residual also two for three warps a row (1025 to 1536 columns), where two
-  // warps with four would leave a quarter of their lanes or more without work (3789 x 1280 bf16 y 10.9 us
-  // instead of 13.5, 16384 x 1280 32.6 instead of 35.5, 16384 x 1536 to 8 bits 36.7 instead of 38.4; without a
-  // residual 19.8 against 18.0).
+  // warps with four would leave a quarter of their lanes or more without work (bf16 y, 3789 x 1280
+  // 10.9 us instead of 13.5, 16384 rows of 1032 to 1472 columns, every 64th, 31.8 to 33.3 instead of 35.4 to 37.1, of
+  // 1536 33.8 both ways; 16384 x 1536 to 8 bits 36.7 instead of 38.4; without a residual 19.8 against 18.0).
   const bool three = warps(2) == 3 && a.residual;
   if (Wide ? full || three : busy(2) >= 12) return forward_staged<T, Wide, 2>(a, warps(2), dev, s);
   return forward_staged<T, Wide, 4>(a, warps(4), dev, s);
