@@ -107,7 +107,7 @@ def _binding():
     if needs is not None:  # the package works without it, through ctypes
         sys.stderr.write(f"_binding not built: {needs} not found; small calls of mp_block.h cost twice as much\n")
         if os.path.exists(BINDING) and _outdated(BINDING):
-            os.remove(BINDING)
+            _remove(BINDING)
         return
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = [_cc(), "-O2", "-std=c11", "-Wall", "-Wextra", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"],
@@ -119,8 +119,15 @@ def _binding():
         sys.stderr.write(r.stderr)
     os.replace(tmp, BINDING)
     untagged = os.path.join(PKG, "_binding.so")  # an earlier build's, which any Python would take
-    if os.path.exists(untagged) and untagged != BINDING:
-        os.remove(untagged)
+    if untagged != BINDING:
+        _remove(untagged)
+
+
+def _remove(path):
+    try:
+        os.remove(path)
+    except FileNotFoundError:  # another process was first
+        pass
 
 
 def _link(objs, out):
